@@ -401,6 +401,179 @@ v4_status v4_attn_layer_fwd(const v4_config* cfg, const v4_layer_inputs* in,
                             v4_layer_outputs* out, void* workspace, size_t ws_bytes,
                             void* stream);
 
+/* ----------------------------------------------------------------------
+ * Rotary positions at given positions (no counterpart of its own on the
+ * pages: [PR] items 2 and 8 and [BLOG] "Kernel fusions", row "Interleaved
+ * partial RoPE", give the rotation that the other entry points apply inside
+ * their kernels).
+ *
+ *   out[t, h, c] = x[t, h, c] outside [rope_begin, rope_begin + R); inside,
+ *   pair j = (a, b) becomes mscale * (a cos p - b sin p, a sin p + b cos p)
+ *   with p = pos[t] * inv_freq[j], or -p with inverse = 1.
+ *   V4_ROPE_INTERLEAVED: pair j = dims rope_begin + 2j, + 2j + 1;
+ *   V4_ROPE_HALF:        pair j = dims rope_begin + j, + j + R/2.
+ * The gradient of sum(dout * out) with respect to x is the same call on dout
+ * with inverse = 1 and the same mscale.  (Where x was broadcast over heads or
+ * rows, the caller sums that result over the broadcast axis.)
+ *
+ *   x, out   : element (t, h, c) at t * row_stride + h * head_stride + c, in
+ *              elements; strides >= 0, multiples of 16 bytes.  x may be
+ *              broadcast (a stride of 0); out's rows must not overlap
+ *              (refused).  out may be x with the same strides (in place:
+ *              only the rotated dims are touched); otherwise the two must not
+ *              overlap.
+ *   pos      : [rows] int32, any value.   inv_freq : [rope_dim/2] fp32,
+ *              finite (the table of v4_rope_inv_freq, or any other scaling).
+ *   dim a multiple of 8 up to 8192; rope_dim a multiple of 8 (16 for
+ *   V4_ROPE_HALF), <= 1024; rope_begin a multiple of 8, rope_begin +
+ *   rope_dim <= dim.  rows = 0 is valid.  dtype: a v4_dtype.
+ * Angles are formed from a 64-bit fraction of a turn (any int32 position);
+ * the rotation is fp32 with one rounding to the storage type.
+ * --------------------------------------------------------------------*/
+typedef enum { V4_ROPE_INTERLEAVED = 0, V4_ROPE_HALF = 1 } v4_rope_layout;
+v4_status v4_rope(const void* x, int64_t rows, int32_t heads, int32_t dim, int64_t x_row_stride,
+                  int64_t x_head_stride, const int32_t* pos, const float* inv_freq, int32_t rope_dim,
+                  int32_t rope_begin, int32_t layout, int32_t inverse, float mscale, int32_t dtype,
+                  void* out, int64_t out_row_stride, int64_t out_head_stride, void* stream);
+
+/* ----------------------------------------------------------------------
+ * Paged cache write: row t of x, its last rope_dim dims rotated at pos[t]
+ * (interleaved pairs, the layout of every rotated key here), is stored at
+ * row slot[t] of the cache.  Token rows of the window and compressed entries
+ * go into their caches this way.
+ *   x      : [rows, dim], rows x_row_stride elements apart.
+ *   pos    : [rows] int32; NULL = rows stored as they are (rotated already).
+ *   slot   : [rows] int32, page * page_size + row within the page; -1 = the
+ *            row is not stored.  Values < -1 or >= n_slots are skipped and
+ *            flagged (V4_ERR_BAD_INDEX in the device status).  Slots other
+ *            than -1 must be distinct: what a slot named twice holds
+ *            afterwards is not defined.
+ *   cache  : [n_slots, dim], dense.  Must not overlap x.
+ * dim, rope_dim, dtype and angles as v4_rope.  Rows of the cache that no slot
+ * names keep their values.
+ * --------------------------------------------------------------------*/
+v4_status v4_cache_append(const void* x, int64_t rows, int32_t dim, int64_t x_row_stride,
+                          const int32_t* pos, const float* inv_freq, int32_t rope_dim,
+                          const int32_t* slot, int64_t n_slots, int32_t dtype, void* cache,
+                          void* stream);
+
+/* ----------------------------------------------------------------------
+ * Drafted token trees over a paged cache: decoding (one node for each
+ * sequence) and the verification of drafted tokens (a tree of up to
+ * V4_TREE_MAX_NODES nodes for each sequence).
+ *
+ * Sequence b holds seq_len[b] committed tokens; its nodes are the rows
+ * node_begin[b] .. node_begin[b+1]-1 of the call, in an order in which a
+ * parent precedes its children.  Node j sits at position seq_len[b] +
+ * depth(j), depth 0 for a child of the last committed token.
+ *
+ * v4_tree_plan describes the rows once for all layers of a step:
+ *   node_begin  : [B+1] int32, ascending, node_begin[B] <= n_rows.  Rows
+ *                 before the first sequence and behind the last are padding.
+ *   seq_len     : [B] int32 >= 0.
+ *   parent      : [n_rows] int32, the parent's node number within the
+ *                 sequence, -1 = a child of the last committed token; NULL =
+ *                 every sequence's nodes form a chain.
+ *   block_table : [B, max_blocks] int32, the page of each block of page_size
+ *                 tokens; nullable iff slot is NULL.
+ *   plan        : [n_rows, 8] int32 out: sequence (-1 = padding), node
+ *                 number, position, committed length, and 128 bits (bit j of
+ *                 word 4 + j/32): the node itself and its ancestors.
+ *   pos         : [n_rows] int32 out, nullable: the positions (0 on padding).
+ *   slot        : [n_rows] int32 out, nullable: the cache row of token
+ *                 seq_len[b] + node number, where v4_cache_append puts the
+ *                 node's key before v4_tree_mqa_fwd reads it (-1 on padding).
+ * Bad values are flagged (V4_ERR_BAD_INDEX in the device status): a node
+ * whose parent is not an earlier node is treated as a child of the last
+ * committed token; a sequence with a bad range, more than V4_TREE_MAX_NODES
+ * nodes or a negative length becomes padding; a slot outside the table or
+ * the cache becomes -1.
+ * After acceptance the caller appends the accepted nodes' rows again at the
+ * slots of tokens seq_len[b], seq_len[b] + 1, ...
+ * --------------------------------------------------------------------*/
+#define V4_TREE_MAX_NODES 128
+v4_status v4_tree_plan(int32_t batch, int32_t n_rows, const int32_t* node_begin,
+                       const int32_t* seq_len, const int32_t* parent, const int32_t* block_table,
+                       int32_t max_blocks, int32_t page_size, int64_t n_slots, int32_t* plan,
+                       int32_t* pos, int32_t* slot, void* stream);
+
+/* Pointers and sizes of one call. Nullable fields are marked. */
+typedef struct v4_tree_inputs {
+  const void* q;             /* [n_rows, H, D] un-rotated */
+  const int32_t* plan;       /* [n_rows, 8] of v4_tree_plan */
+  const void* tok_cache;     /* [tok_slots, D] rotated token rows; NULL iff window == 0 */
+  const int32_t* tok_table;  /* [B, tok_blocks] page of each block of tok_page tokens */
+  const void* ent_cache;     /* [ent_slots, D] rotated entries (r > 0) */
+  const int32_t* ent_table;  /* [B, ent_blocks] page of each block of ent_page entries */
+  const int32_t* ent_len;    /* [B] entries that the cache holds of each sequence (r > 0) */
+  const int32_t* idx;        /* [n_rows, K] selected entries (K > 0) */
+  const float* sink;         /* [H], nullable */
+  const float* inv_freq;     /* [R/2] */
+  int64_t tok_slots, ent_slots;                            /* rows of the caches */
+  int32_t n_rows;
+  int32_t tok_blocks, tok_page, ent_blocks, ent_page;      /* page sizes >= 1 */
+} v4_tree_inputs;
+
+/* ----------------------------------------------------------------------
+ * v4_tree_mqa_fwd: v4_sparse_mqa_fwd for the planned rows.  Keys of row i
+ * (position t, sequence b, committed length L):
+ *   - entries s < min((t+1)/r, ent_len[b]): every one (K = 0), or those of
+ *     idx[i] (-1 = unused slot; other values outside that range are skipped
+ *     and flagged);
+ *   - committed tokens u < L with t - W < u <= t (W = -1: all u <= t);
+ *   - the nodes j of its bits with 0 <= t - t_j < W (W = -1: any t_j <= t),
+ *     read from token row L + j of the cache.
+ * o = softmax-weighted sum (V = K) with the optional sink, de-rotated at -t;
+ * lse natural log.  An empty key set yields o = 0 and lse = -inf (with a
+ * sink: o = 0, lse = sink).  Rows of padding (plan sequence -1) keep their o
+ * and lse.  Only the rows of the caches named above are read; a token or
+ * entry whose page the table does not hold (a negative or too large value)
+ * is skipped and flagged.
+ *   cfg  : batch, n_heads, head_dim, rope_dim, ratio, window, topk,
+ *          softmax_scale, dtype and path are used; seqlen need not bound the
+ *          positions.  q_begin must be 0.
+ *   o    : [n_rows, H, D] out.    lse : [n_rows, H] fp32 out, nullable.
+ * Tensor-core path: bf16, H a multiple of 64 up to 512, D = 512, R = 64;
+ * every other shape runs on CUDA cores.  Workspace: v4_tree_workspace_size
+ * bytes, 256-byte aligned; calls that may overlap need one each.  Results do
+ * not depend on what the workspace held, and repeat bit for bit on the same
+ * inputs.
+ * --------------------------------------------------------------------*/
+v4_status v4_tree_workspace_size(const v4_config* cfg, int32_t n_rows, size_t* bytes);
+v4_status v4_tree_mqa_fwd(const v4_config* cfg, const v4_tree_inputs* in, void* o, float* lse,
+                          void* workspace, size_t ws_bytes, void* stream);
+
+/* ----------------------------------------------------------------------
+ * Projections of single tokens with 4-bit weights and group scales: the
+ * decode form of v4_q_proj and v4_grouped_o_proj, where every weight is read
+ * once for a few rows.
+ *   y[t, g, n] = sum_k x[t, g, k] * (code[g, n, k] - 8) * scale[g, n, k / gs]
+ * and with norm_dim > 0 every block of norm_dim outputs is RMS-normalised:
+ * y / sqrt(mean(y^2) + eps) * norm_w (norm_w [norm_dim] fp32, NULL = ones).
+ *   x      : [rows, groups, K] bf16.      y : [rows, groups, N] bf16 out.
+ *   codes  : [groups, N, K/2] bytes.  Each 64-byte block holds 128 inputs:
+ *            its little-endian 32-bit word 4 t + c (t, c = 0..3) holds inputs
+ *            32 c + 8 t .. + 7 of the block, from the lowest nibble in the
+ *            order 0, 2, 4, 6, 1, 3, 5, 7.
+ *   scales : [groups, N, K/gs] bf16.
+ * K a multiple of 128, N a multiple of 64, gs 32, 64 or 128, norm_dim 0, 64,
+ * 128, 256 or 512 dividing N (other shapes return V4_ERR_UNSUPPORTED); rows
+ * >= 0.  Products of bf16 inputs and exact codes are summed in fp32 within a
+ * scale group, the groups' sums scaled and added in fp32, and rounded to
+ * bf16 once (after the norm).  Meant for up to about 64 rows; more are
+ * computed in slices of 64 that each read the weights again.
+ *
+ * v4_w4_pack makes codes and scales of a bf16 weight w [groups, K, N] (the
+ * layout of wq and wo_a): scale = bf16(max|w| / 7) over the group's gs
+ * inputs, code = 8 + clamp(round_to_even(w / scale), -8, 7); a group whose
+ * scale is 0 gets codes 8.  Weights must be finite.
+ * --------------------------------------------------------------------*/
+v4_status v4_w4_pack(const void* w, int32_t groups, int32_t K, int32_t N, int32_t group_size,
+                     uint8_t* codes, void* scales, void* stream);
+v4_status v4_w4_proj(const void* x, int64_t rows, int32_t groups, int32_t K, int32_t N,
+                     int32_t group_size, const uint8_t* codes, const void* scales,
+                     int32_t norm_dim, float eps, const float* norm_w, void* y, void* stream);
+
 /* Text of the last non-OK status returned on this host thread ("" if none). */
 const char* v4_last_error(void);
 
@@ -439,7 +612,9 @@ v4_status v4_selftest_wait_timeout(int32_t limit_us, void* stream);
  * 7 backward prep (clears, tables, key rotation, query/gradient rotation and
  * delta), 8 attention backward, 9 window-gradient de-rotation, 10 E4M3
  * quantisation of the indexer operands, 11 query projections, 12 indexer
- * distillation target.
+ * distillation target, 13 rotary positions, 14 paged cache write, 15 tree
+ * plan, 16 tree attention, 17 join of split tree attention, 18 4-bit
+ * packing, 19 4-bit projection.
  * --------------------------------------------------------------------*/
 v4_status v4_profile_enable(int32_t on);
 int32_t v4_profile_count(void);

@@ -18,6 +18,8 @@ V4_OK, V4_ERR_INVALID_ARG, V4_ERR_UNSUPPORTED, V4_ERR_WORKSPACE, V4_ERR_CUDA, \
     V4_ERR_TIMEOUT, V4_ERR_BAD_INDEX, V4_ERR_BOUND = range(8)
 V4_F32, V4_BF16 = 0, 1
 V4_PATH_AUTO, V4_PATH_SIMT, V4_PATH_TC = 0, 1, 2
+V4_ROPE_INTERLEAVED, V4_ROPE_HALF = 0, 1
+V4_TREE_MAX_NODES = 128
 
 STATUS_NAMES = {0: "V4_OK", 1: "V4_ERR_INVALID_ARG", 2: "V4_ERR_UNSUPPORTED", 3: "V4_ERR_WORKSPACE",
                 4: "V4_ERR_CUDA", 5: "V4_ERR_TIMEOUT", 6: "V4_ERR_BAD_INDEX", 7: "V4_ERR_BOUND"}
@@ -28,10 +30,13 @@ EXPORTS = ["v4_rope_inv_freq", "v4_workspace_size", "v4_compress", "v4_indexer_p
            "v4_last_error", "v4_get_device_status", "v4_reset_device_status", "v4_launch_count",
            "v4_profile_enable", "v4_profile_count", "v4_profile_get", "v4_sparse_mqa_fwd_noalloc",
            "v4_bwd_workspace_size", "v4_sparse_mqa_bwd", "v4_quantize_e4m3", "v4_indexer_topk_e4m3",
-           "v4_q_proj", "v4_indexer_kl_target", "v4_selftest_wait_timeout", "v4_build_info"]
+           "v4_q_proj", "v4_indexer_kl_target", "v4_selftest_wait_timeout", "v4_build_info",
+           "v4_rope", "v4_cache_append", "v4_tree_plan", "v4_tree_workspace_size", "v4_tree_mqa_fwd",
+           "v4_w4_pack", "v4_w4_proj"]
 PROFILE_KINDS = {0: "compress", 1: "window_rotate", 2: "indexer_prep", 3: "indexer_scores", 4: "topk",
                  5: "attention", 6: "o_proj", 7: "bwd_prep", 8: "bwd_attention", 9: "bwd_derotate",
-                 10: "indexer_quant", 11: "q_proj", 12: "kl_target"}
+                 10: "indexer_quant", 11: "q_proj", 12: "kl_target", 13: "rope", 14: "cache_append",
+                 15: "tree_plan", 16: "tree_attention", 17: "tree_join", 18: "w4_pack", 19: "w4_proj"}
 
 
 class V4Error(RuntimeError):
@@ -58,6 +63,13 @@ class v4_layer_outputs(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in ("o", "lse", "ent", "ikey", "idx", "iscore", "y")]
 
 
+class v4_tree_inputs(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in (
+        "q", "plan", "tok_cache", "tok_table", "ent_cache", "ent_table", "ent_len", "idx", "sink", "inv_freq")] + [
+        (n, C.c_int64) for n in ("tok_slots", "ent_slots")] + [
+        (n, C.c_int32) for n in ("n_rows", "tok_blocks", "tok_page", "ent_blocks", "ent_page")]
+
+
 _lib = None
 
 
@@ -73,7 +85,7 @@ def lib(path=None):
         raise RuntimeError("CUDA library %s is missing: build it with "
                            "sparse_compressed_attention_gb300.build.build()" % path)
     L = C.CDLL(path)
-    vp, i32, f32, sz = C.c_void_p, C.c_int32, C.c_float, C.c_size_t
+    vp, i32, i64, f32, sz = C.c_void_p, C.c_int32, C.c_int64, C.c_float, C.c_size_t
     cfgp = C.POINTER(v4_config)
     sig = {
         "v4_rope_inv_freq": [f32, i32, f32, i32, f32, f32, vp],
@@ -96,6 +108,13 @@ def lib(path=None):
         "v4_profile_enable": [i32],
         "v4_profile_get": [i32, C.POINTER(i32), C.POINTER(f32)],
         "v4_selftest_wait_timeout": [i32, vp],
+        "v4_rope": [vp, i64, i32, i32, i64, i64, vp, vp, i32, i32, i32, i32, f32, i32, vp, i64, i64, vp],
+        "v4_cache_append": [vp, i64, i32, i64, vp, vp, i32, vp, i64, i32, vp, vp],
+        "v4_tree_plan": [i32, i32, vp, vp, vp, vp, i32, i32, i64, vp, vp, vp, vp],
+        "v4_tree_workspace_size": [cfgp, i32, C.POINTER(sz)],
+        "v4_tree_mqa_fwd": [cfgp, C.POINTER(v4_tree_inputs), vp, vp, vp, sz, vp],
+        "v4_w4_pack": [vp, i32, i32, i32, i32, vp, vp, vp],
+        "v4_w4_proj": [vp, i64, i32, i32, i32, i32, vp, vp, i32, f32, vp, vp, vp],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -333,6 +352,183 @@ def v4_attn_layer_fwd(cfg, inputs, outputs, workspace, stream=None):
                                    _ptr(workspace, "workspace", torch.uint8), workspace.numel(),
                                    _stream(stream)))
     return outputs
+
+
+def _shaped(t, name, shape, dtype):
+    """Pointer of a dense tensor of exactly this shape on the current device."""
+    p = _ptr(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    return _here(t, name, p)
+
+
+def _here(t, name, p):
+    """The call runs on the current device's stream: tensors of another one are refused."""
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError("%s is on %s, the current device is cuda:%d" % (name, t.device, torch.cuda.current_device()))
+    return p
+
+
+def _strided(t, name, dims):
+    """Pointer of a tensor whose last dim is dense; its other strides go to the library."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be on a CUDA device" % name)
+    if t.dim() != dims:
+        raise ValueError("%s must have %d dims, got %d" % (name, dims, t.dim()))
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("%s must be bfloat16 or float32, got %s" % (name, t.dtype))
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError("%s must be contiguous in its last dim" % name)
+    return _here(t, name, t.data_ptr())
+
+
+def _storage_code(t):
+    return V4_BF16 if t.dtype == torch.bfloat16 else V4_F32
+
+
+def v4_rope(x, pos, inv_freq, out, rope_begin=None, layout=V4_ROPE_INTERLEAVED, inverse=False, mscale=1.0,
+            stream=None):
+    """Rotate dims [rope_begin, rope_begin + R) of x [rows, heads, dim] at pos [rows] into out (or in place).
+
+    R = 2 * len(inv_freq); rope_begin defaults to the last R dims.  x and out may be
+    strided views (dense last dim).  The gradient of x is the call on the gradient of out
+    with inverse=True and the same mscale."""
+    px, po = _strided(x, "x", 3), _strided(out, "out", 3)
+    if out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError("out must have x's shape and type")
+    rows, heads, dim = x.shape
+    R = 2 * inv_freq.numel()
+    begin = dim - R if rope_begin is None else int(rope_begin)
+    if x.numel() == 0:
+        return out
+    _check(lib().v4_rope(px, rows, heads, dim, x.stride(0), x.stride(1), _shaped(pos, "pos", (rows,), torch.int32),
+                         _shaped(inv_freq, "inv_freq", (R // 2,), torch.float32), R, begin, int(layout),
+                         int(bool(inverse)), float(mscale), _storage_code(x), po, out.stride(0), out.stride(1),
+                         _stream(stream)))
+    return out
+
+
+def v4_cache_append(x, pos, inv_freq, slot, cache, stream=None):
+    """Store rows x [rows, dim], rotated at pos (None: as they are), at rows slot of cache [..., dim]."""
+    px = _strided(x, "x", 2)
+    rows, dim = x.shape
+    pc = _here(cache, "cache", _ptr(cache, "cache", x.dtype))
+    if cache.shape[-1] != dim:
+        raise ValueError("cache rows must have %d elements, got %d" % (dim, cache.shape[-1]))
+    R = 2 * inv_freq.numel() if pos is not None else 0
+    if x.numel() == 0:
+        return cache
+    _check(lib().v4_cache_append(px, rows, dim, x.stride(0),
+                                 None if pos is None else _shaped(pos, "pos", (rows,), torch.int32),
+                                 None if pos is None else _shaped(inv_freq, "inv_freq", (R // 2,), torch.float32), R,
+                                 _shaped(slot, "slot", (rows,), torch.int32), cache.numel() // dim,
+                                 _storage_code(x), pc, _stream(stream)))
+    return cache
+
+
+def v4_tree_plan(node_begin, seq_len, parent, plan, pos=None, slot=None, block_table=None, page_size=0, n_slots=0,
+                 stream=None):
+    """Describe drafted trees (see the header): plan [n_rows, 8], and optionally pos and slot [n_rows]."""
+    B, n = seq_len.numel(), plan.shape[0]
+    i32 = torch.int32
+    blocks = 0
+    if slot is not None:
+        if block_table is None or block_table.dim() != 2:
+            raise ValueError("slot needs block_table [batch, max_blocks]")
+        blocks = block_table.shape[1]
+    if n == 0:
+        return plan
+    _check(lib().v4_tree_plan(B, n, _shaped(node_begin, "node_begin", (B + 1,), i32), _shaped(seq_len, "seq_len", (B,), i32),
+                              None if parent is None else _shaped(parent, "parent", (n,), i32),
+                              None if slot is None else _shaped(block_table, "block_table", (B, blocks), i32),
+                              blocks, int(page_size), int(n_slots), _shaped(plan, "plan", (n, 8), i32),
+                              None if pos is None else _shaped(pos, "pos", (n,), i32),
+                              None if slot is None else _shaped(slot, "slot", (n,), i32), _stream(stream)))
+    return plan
+
+
+def v4_tree_workspace_size(cfg, n_rows):
+    n = C.c_size_t(0)
+    _check(lib().v4_tree_workspace_size(C.byref(cfg), int(n_rows), C.byref(n)))
+    return n.value
+
+
+def alloc_tree_workspace(cfg, n_rows, device=None):
+    return torch.empty(max(v4_tree_workspace_size(cfg, n_rows), 256), dtype=torch.uint8, device=device or "cuda")
+
+
+def v4_tree_mqa_fwd(cfg, inputs, o, lse, workspace, stream=None):
+    """Attention of planned rows over paged caches.  inputs: a dict keyed like v4_tree_inputs' pointers, with
+    tok_cache / ent_cache [pages, page_size, D] and tok_table / ent_table [B, blocks]."""
+    dt, i32, f32 = _storage(cfg), torch.int32, torch.float32
+    q = inputs["q"]
+    n, H, D, B = q.shape[0], cfg.n_heads, cfg.head_dim, cfg.batch
+    vin = v4_tree_inputs()
+    vin.n_rows = n
+    vin.q = _shaped(q, "q", (n, H, D), dt)
+    vin.plan = _shaped(inputs["plan"], "plan", (n, 8), i32)
+    for kind, used in (("tok", cfg.window != 0), ("ent", cfg.ratio > 0)):
+        if not used:
+            continue
+        cache, table = inputs.get(kind + "_cache"), inputs.get(kind + "_table")
+        p = _ptr(cache, kind + "_cache", dt)
+        if cache.dim() != 3 or cache.shape[2] != D:
+            raise ValueError("%s_cache must have shape [pages, page_size, %d], got %s" % (kind, D, tuple(cache.shape)))
+        setattr(vin, kind + "_cache", _here(cache, kind + "_cache", p))
+        if not isinstance(table, torch.Tensor) or table.dim() != 2:
+            raise ValueError("%s_table must be a tensor [batch, blocks]" % kind)
+        setattr(vin, kind + "_table", _shaped(table, kind + "_table", (B, table.shape[1]), i32))
+        setattr(vin, kind + "_slots", cache.shape[0] * cache.shape[1])
+        setattr(vin, kind + "_page", cache.shape[1])
+        setattr(vin, kind + "_blocks", table.shape[1])
+    if cfg.ratio > 0:
+        vin.ent_len = _shaped(inputs.get("ent_len"), "ent_len", (B,), i32)
+    if cfg.topk > 0:
+        vin.idx = _shaped(inputs.get("idx"), "idx", (n, cfg.topk), i32)
+    if inputs.get("sink") is not None:
+        vin.sink = _shaped(inputs["sink"], "sink", (H,), f32)
+    if cfg.rope_dim > 0:
+        vin.inv_freq = _shaped(inputs.get("inv_freq"), "inv_freq", (cfg.rope_dim // 2,), f32)
+    _check(lib().v4_tree_mqa_fwd(C.byref(cfg), C.byref(vin), _shaped(o, "o", (n, H, D), dt),
+                                 None if lse is None else _shaped(lse, "lse", (n, H), f32),
+                                 _here(workspace, "workspace", _ptr(workspace, "workspace", torch.uint8)),
+                                 workspace.numel(), _stream(stream)))
+    return o
+
+
+def v4_w4_pack(w, group_size, codes, scales, stream=None):
+    """Quantise w [groups, K, N] bf16 to codes [groups, N, K/2] uint8 and scales [groups, N, K/group_size] bf16."""
+    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise ValueError("w must be a tensor [groups, K, N]")
+    G, K, N = w.shape
+    gs = int(group_size)
+    if gs not in (32, 64, 128):
+        raise ValueError("group_size must be 32, 64 or 128")
+    _check(lib().v4_w4_pack(_shaped(w, "w", (G, K, N), torch.bfloat16), G, K, N, gs,
+                            _shaped(codes, "codes", (G, N, K // 2), torch.uint8),
+                            _shaped(scales, "scales", (G, N, K // gs), torch.bfloat16), _stream(stream)))
+    return codes, scales
+
+
+def v4_w4_proj(x, codes, scales, y, norm_dim=0, eps=1e-6, norm_w=None, stream=None):
+    """y [rows, groups, N] = x [rows, groups, K] . dequantised weights, RMS-normalised over runs of norm_dim outputs."""
+    if not isinstance(codes, torch.Tensor) or codes.dim() != 3 or not isinstance(scales, torch.Tensor) or scales.dim() != 3:
+        raise ValueError("codes must be [groups, N, K/2] and scales [groups, N, K/group_size]")
+    G, N, K = codes.shape[0], codes.shape[1], codes.shape[2] * 2
+    if scales.shape[2] < 1 or K % scales.shape[2]:
+        raise ValueError("scales must have shape [groups, N, K/group_size]")
+    gs = K // scales.shape[2]
+    rows = x.shape[0]
+    b16 = torch.bfloat16
+    px, py = _shaped(x, "x", (rows, G, K), b16), _shaped(y, "y", (rows, G, N), b16)
+    _check(lib().v4_w4_proj(px, rows, G, K, N, gs, _shaped(codes, "codes", (G, N, K // 2), torch.uint8),
+                            _shaped(scales, "scales", (G, N, K // gs), b16), int(norm_dim), float(eps),
+                            None if norm_w is None or not norm_dim else _shaped(norm_w, "norm_w", (int(norm_dim),),
+                                                                                torch.float32),
+                            py, _stream(stream)))
+    return y
 
 
 def v4_last_error():

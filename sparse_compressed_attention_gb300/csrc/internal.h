@@ -150,4 +150,31 @@ cudaError_t launch_mqa_bwd_tc(const v4_config& c, const void* qr, const void* do
 // dkv[b, u] = rot(dkv[b, u], -u) in place
 cudaError_t launch_mqa_bwd_derotate(const v4_config& c, float* dkv, const float2* cs_table, cudaStream_t st);
 
+// ---- rotary positions and the paged cache write (rope.cu)
+struct RopeCall {
+  const void* x;
+  void* out;
+  const int32_t* pos;           // null: rows stored as they are
+  const float* inv_freq;
+  const int32_t* slot;          // null: row t to row t
+  long long n_slots, rows, x_row_stride, x_head_stride, out_row_stride, out_head_stride;
+  int heads, dim, rope_dim, rope_begin, layout, inverse, dtype;
+  float mscale;
+};
+cudaError_t launch_rope(const RopeCall& c, int* status, cudaStream_t st);
+
+// ---- drafted token trees (tree.cu, tree_tc.cu)
+struct TreeArgs;
+cudaError_t launch_tree_plan(int B, int n_rows, const int32_t* node_begin, const int32_t* seq_len,
+                             const int32_t* parent, const int32_t* table, int max_blocks, int page, long long n_slots,
+                             int32_t* plan, int32_t* pos, int32_t* slot, int* status, cudaStream_t st);
+cudaError_t launch_tree_simt(const TreeArgs& a, int dtype, cudaStream_t st);
+
+// ---- 4-bit projections (w4.cu)
+cudaError_t launch_w4_pack(const void* w, int groups, int K, int N, int gs, uint8_t* codes, void* scales,
+                           cudaStream_t st);
+cudaError_t launch_w4_proj(const void* x, long long rows, int groups, int K, int N, int gs, const uint8_t* codes,
+                           const void* scales, int norm_dim, float eps, const float* norm_w, void* y,
+                           cudaStream_t st);
+
 }  // namespace v4
