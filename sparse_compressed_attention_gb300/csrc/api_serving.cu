@@ -71,10 +71,7 @@ static v4_status check_stride(int64_t s, int es, const char* name) {
   return V4_OK;
 }
 
-static bool tree_tc_supported(const v4_config& c) {
-  return c.dtype == V4_BF16 && c.n_heads >= 64 && c.n_heads % 64 == 0 && c.n_heads <= 512 && c.head_dim == 512 &&
-         c.rope_dim == 64;
-}
+static bool tree_on_tc(const v4_config& c) { return tree_tc_supported(c) && c.path != V4_PATH_SIMT; }
 
 }  // namespace v4
 
@@ -214,7 +211,7 @@ v4_status v4_tree_workspace_size(const v4_config* cfg, int32_t n_rows, size_t* b
   TRY(validate_config(cfg));
   if (!bytes) return bad("bytes is NULL");
   if (n_rows < 0) return bad("n_rows must be >= 0");
-  *bytes = 0;
+  *bytes = tree_on_tc(*cfg) ? tree_tc_workspace(*cfg, n_rows) : 0;
   return V4_OK;
 }
 
@@ -225,7 +222,7 @@ v4_status v4_tree_mqa_fwd(const v4_config* cfg, const v4_tree_inputs* in, void* 
   const v4_config& c = *cfg;
   if (c.q_begin != 0) return set_error(V4_ERR_UNSUPPORTED, "the tree attention needs q_begin = 0");
   if (in->n_rows < 0) return bad("n_rows must be >= 0");
-  const bool tc = tree_tc_supported(c) && c.path != V4_PATH_SIMT;
+  const bool tc = tree_on_tc(c);
   if (c.path == V4_PATH_TC && !tc)
     return set_error(V4_ERR_UNSUPPORTED, "tensor-core tree attention needs bf16, H a multiple of 64 up to 512, D=512, R=64");
   if (in->n_rows == 0) return V4_OK;
@@ -291,7 +288,7 @@ v4_status v4_tree_mqa_fwd(const v4_config* cfg, const v4_tree_inputs* in, void* 
   a.scale = c.softmax_scale > 0.f ? c.softmax_scale : 1.0f / sqrtf((float)c.head_dim);
   cudaStream_t st = (cudaStream_t)stream;
   StageTiming ps(16, st);
-  return cuda_result(launch_tree_simt(a, c.dtype, st), "tree attention kernel");
+  return cuda_result(tc ? launch_tree_tc(a, workspace, st) : launch_tree_simt(a, c.dtype, st), "tree attention kernel");
 }
 
 static v4_status check_w4(int32_t groups, int32_t K, int32_t N, int32_t group_size) {

@@ -66,7 +66,12 @@ __device__ __forceinline__ TreeRow tree_row(const TreeArgs& a, int row) {
   }
   r.ne = a.K > 0 ? a.K : r.nv;
   // committed tokens u < min(L, t + 1), u > t - W
-  const int hi = r.L <= r.t ? r.L : r.t + 1;
+  int hi = r.L <= r.t ? r.L : r.t + 1;
+  const long long held = (long long)a.tok_blocks * a.tok_page;
+  if (a.window != 0 && hi > held) {               // the table ends before the tokens do
+    set_status(a.status, kStatusBadIndex);
+    hi = (int)held;
+  }
   r.lo = a.window < 0 ? 0 : max(0, r.t - a.window + 1);
   r.nw = a.window == 0 ? 0 : max(0, hi - r.lo);
   return r;
@@ -114,6 +119,8 @@ __device__ __forceinline__ long long tree_token_row(const TreeArgs& a, const Tre
   return paged_row(a.tok_table, a.tok_blocks, a.tok_page, a.tok_slots, r.b, at, a.status);
 }
 
+bool tree_tc_supported(const v4_config& c);
+size_t tree_tc_workspace(const v4_config& c, int n_rows);
 cudaError_t launch_tree_tc(const TreeArgs& a, void* workspace, cudaStream_t st);
 
 }  // namespace v4

@@ -1,0 +1,779 @@
+// Tree attention on the 5th-generation tensor cores (tcgen05, TMEM
+// accumulators) for the DeepSeek-V4-Flash shapes: 64-head slices of one 512-d
+// latent that is key and value, last 64 dims rotated, bf16 storage.
+//
+// Work.  An item is (row, 64-head slice); its keys (entries, committed window
+// tokens, drafted ancestors) are numbered and cut into tiles of 128.  Lengths
+// live on the device, so every block computes the same prefix sum of the
+// items' tile counts and takes an equal share of all tiles: a long row is
+// split over many blocks, a block walks several short rows.  A block that
+// holds an item whole writes its output; pieces of a cut item leave their
+// unnormalised sums, maxima and denominators in the workspace, and the join
+// kernel merges them.  The cut depends on the lengths alone, so results repeat
+// bit for bit.
+//
+// Per tile (one block, M = 128 keys or dims, N = 64 heads):
+//   S^T[key, head]  = K_tile . Q^T             (K = 512, + 64 for q's low part)
+//   P^T             = exp2(S^T c - m_head), bf16
+//   O^T[dim, head] += K_tile^T . P^T           (4 x M = 128 dims)
+// The rotated 64 dims of q are kept as two bf16 terms (high and low), so the
+// logits, and with them lse, carry no rounding of the rotation; it costs 4
+// products of 68.  m is a running maximum that is only raised when a logit
+// exceeds it by more than 8 (a factor of 256, well inside bf16 P and fp32 sums):
+// the O^T rescale through registers is then rare, and a vote of one
+// barrier is all that a tile pays for it.
+//
+// Roles (448 threads): warp 0 shares out the work and loads query rows (TMA),
+// warp 1 issues the products, warps 2-3 and 12-13 look up and gather key rows
+// (16-byte cp.async, masked rows zero-filled so that nothing a mask hides is
+// ever read), warps 4-11 softmax and output (two per TMEM lane quarter, 32
+// heads each).
+#include <cuda.h>
+#include <math.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "sm100.cuh"
+#include "tree.cuh"
+#include "turn.cuh"
+
+namespace v4 {
+
+using namespace sm100;
+
+namespace {
+
+constexpr int kH = 64, kD = 512, kR = 64;
+constexpr int kThreads = 448;
+constexpr int kSoftThreads = 256;                 // warps 4-11
+constexpr int kGatherWarps = 4;                   // 32 key rows each
+constexpr int kTile = 128;
+constexpr int kSlots = 8;                         // K-blocks of 64 dims: one tile
+constexpr uint32_t kSlotBytes = kTile * 128;
+constexpr uint32_t kQBlockBytes = kH * 128;
+constexpr uint32_t kPBytes = kTile * kH * 2;
+constexpr int kMaxCtas = 152;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kRaise = 8.f;                     // how far (log2) a logit may exceed m
+
+constexpr uint32_t OFF_Q = 0;                                     // 8 K-blocks, then q's low part
+constexpr uint32_t OFF_SLOT = OFF_Q + 9 * kQBlockBytes;           // 73728
+constexpr uint32_t OFF_P = OFF_SLOT + kSlots * kSlotBytes;        // 204800
+constexpr uint32_t OFF_CTL = OFF_P + kPBytes;                     // 221184
+
+// A block's piece of an item.
+struct Piece {
+  int row, hs, tile0, tiles, done;
+  int part;                              // workspace part of a cut item, -1: the item is whole
+};
+
+struct Ctl {
+  uint64_t full[kSlots], empty[kSlots];
+  uint64_t valid_full[2];
+  uint64_t q_full, q_ready, q_empty;
+  uint64_t s_full[2], p_ready[2];
+  uint64_t o_full, o_empty;
+  uint64_t info_full[2], info_empty[2];
+  uint64_t fin;
+  Piece info[2];
+  uint32_t valid[2][kGatherWarps];       // bit per key row of a tile
+  float2 cs[2][kR / 2];                  // cos/sin of the piece's position
+  float m[kH];                           // shift of each head (log2 units)
+  float hmax[4][kH];
+  float fac[kH];
+  float part_l[4][kH];
+  float inv[kH];
+  int scan[kThreads / 32];
+  int start_item, start_unit, total;     // where this block's share begins
+  uint32_t tmem_base;
+  int abort;
+  int decision;
+};
+constexpr uint32_t kSmemBytes = OFF_CTL + sizeof(Ctl);
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+
+// Workspace: parts of cut items (two a block: the item its share begins
+// inside, the item it ends inside), then for each item the blocks that hold it.
+struct PartHead {
+  float m[kH], l[kH];
+};
+constexpr size_t kPartFloats = (size_t)kH * kD;
+constexpr size_t kPartBytes = kPartFloats * 4 + sizeof(PartHead);
+
+struct Args {
+  TreeArgs t;
+  int HS, items;
+  char* parts;
+  int2* cuts;                            // per item: first and last block, (-1, -1) when whole
+};
+
+__device__ __forceinline__ int tree_tiles(const TreeArgs& a, int row) {
+  const TreeRow r = tree_row(a, row);
+  if (!r.live) return 0;
+  const int4 w = *reinterpret_cast<const int4*>(a.plan + (size_t)row * kPlanWords + 4);
+  const int nd = a.window == 0 ? 0 : __popc(w.x) + __popc(w.y) + __popc(w.z) + __popc(w.w);
+  const long long nk = (long long)r.ne + r.nw + nd;
+  return nk == 0 ? 1 : (int)((nk + kTile - 1) / kTile);
+}
+
+// Node of the i-th set bit.
+__device__ __forceinline__ int nth_node(const int4 w, int i) {
+  const uint32_t m[4] = {(uint32_t)w.x, (uint32_t)w.y, (uint32_t)w.z, (uint32_t)w.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int n = __popc(m[k]);
+    if (i < n) return 32 * k + (int)__fns(m[k], 0, i + 1);
+    i -= n;
+  }
+  return -1;
+}
+
+// Cache row behind position `at` of a row's key list; null where there is no key.
+__device__ __forceinline__ const bf16* key_row(const TreeArgs& a, const TreeRow& r, const int4 bits, int row,
+                                               long long at) {
+  if (at < r.ne) {
+    const long long s = tree_entry_row(a, r, row, (int)at);
+    return s < 0 ? nullptr : reinterpret_cast<const bf16*>(a.ent_cache) + s * kD;
+  }
+  at -= r.ne;
+  long long u;
+  if (at < r.nw) {
+    u = r.lo + at;
+  } else {
+    if (a.window == 0 || at - r.nw >= V4_TREE_MAX_NODES) return nullptr;
+    const int j = nth_node(bits, (int)(at - r.nw));
+    if (j < 0 || !tree_draft_key(a, r, row, j, 0xFFFFFFFFu)) return nullptr;
+    u = (long long)r.L + j;
+  }
+  const long long s = tree_token_row(a, r, u);
+  return s < 0 ? nullptr : reinterpret_cast<const bf16*>(a.tok_cache) + s * kD;
+}
+
+// 16 bytes of global memory, or zeros, into shared memory.
+__device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
+      "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])),
+      "r"(__float_as_uint(v[8])), "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
+      "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])),
+      "r"(__float_as_uint(v[15])), "r"(__float_as_uint(v[16])), "r"(__float_as_uint(v[17])),
+      "r"(__float_as_uint(v[18])), "r"(__float_as_uint(v[19])), "r"(__float_as_uint(v[20])),
+      "r"(__float_as_uint(v[21])), "r"(__float_as_uint(v[22])), "r"(__float_as_uint(v[23])),
+      "r"(__float_as_uint(v[24])), "r"(__float_as_uint(v[25])), "r"(__float_as_uint(v[26])),
+      "r"(__float_as_uint(v[27])), "r"(__float_as_uint(v[28])), "r"(__float_as_uint(v[29])),
+      "r"(__float_as_uint(v[30])), "r"(__float_as_uint(v[31]))
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Barrier of n threads that also tells whether any of them saw `p`.
+__device__ __forceinline__ bool bar_any(int id, int n, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)p), "r"(id), "r"(n)
+      : "memory");
+  return r != 0;
+}
+
+// Five butterfly rounds over a warp: lane L is left with the fold of r[L] over
+// the lanes.
+template <typename F>
+__device__ __forceinline__ float fold_lanes(float* r, int lane, F f) {
+#pragma unroll
+  for (int o = 16, w = 16; o >= 1; o >>= 1, w >>= 1) {
+    const bool hi = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < w; ++i) {
+      const float send = hi ? r[i] : r[w + i];
+      const float keep = hi ? r[w + i] : r[i];
+      r[i] = f(keep, __shfl_xor_sync(0xffffffffu, send, o));
+    }
+  }
+  return r[0];
+}
+
+// Units of a share: each item is one unit (its query rows and output) plus
+// its tiles.  Block c of the grid takes units [c * share, (c + 1) * share).
+__device__ __forceinline__ int share_of(int total, int ctas) { return (total + ctas - 1) / ctas; }
+
+__global__ void __launch_bounds__(kThreads, 1)
+tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const Args p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Ctl* c = reinterpret_cast<Ctl*>(smem + OFF_CTL);
+  const TreeArgs& a = p.t;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if ((smem_u32(smem) & 1023u) != 0) {          // swizzled operands need 1 KB alignment
+    if (threadIdx.x == 0) set_status(a.status, V4_ERR_UNSUPPORTED);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&c->full[i], 32 * kGatherWarps);
+      mbar_init(&c->empty[i], 1);
+    }
+    mbar_init(&c->q_full, 1);
+    mbar_init(&c->q_ready, kSoftThreads);
+    mbar_init(&c->q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&c->valid_full[i], kGatherWarps);
+      mbar_init(&c->s_full[i], 1);
+      mbar_init(&c->p_ready[i], kSoftThreads);
+      mbar_init(&c->info_full[i], 1);
+      mbar_init(&c->info_empty[i], 1 + kSoftThreads + 32 * kGatherWarps);
+    }
+    mbar_init(&c->o_full, 1);
+    mbar_init(&c->o_empty, kSoftThreads);
+    mbar_init(&c->fin, 1);
+    c->abort = 0;
+    fence_barrier_init();
+    prefetch_tmap(&map_q);
+  }
+
+  // ---- this block's share: prefix sum of the items' units
+  const int per = (p.items + kThreads - 1) / kThreads;
+  const int i0 = threadIdx.x * per, i1 = min(i0 + per, p.items);
+  int mine = 0;
+  for (int i = i0; i < i1; ++i) {
+    const int n = tree_tiles(a, i / p.HS);
+    mine += n ? n + 1 : 0;
+  }
+  int upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
+  }
+  if (lane == 31) c->scan[warp] = upto;
+  __syncthreads();
+  int before = upto - mine, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += c->scan[w];
+    total += c->scan[w];
+  }
+  const int share = share_of(total, gridDim.x);
+  const int s0 = min(blockIdx.x * share, total), s1 = min(s0 + share, total);
+  if (s0 >= s1) return;                          // nothing for this block
+  if (before <= s0 && s0 < before + mine) {
+    int at = before;
+    for (int i = i0; i < i1; ++i) {
+      const int n = tree_tiles(a, i / p.HS);
+      const int u = n ? n + 1 : 0;
+      if (s0 < at + u) {
+        c->start_item = i;
+        c->start_unit = at;
+        break;
+      }
+      at += u;
+    }
+  }
+  if (warp == 1) {
+    tmem_alloc(&c->tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = c->tmem_base;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ shares and query rows
+    int item = c->start_item, unit = c->start_unit, qc = 0;
+    bool ok = true;
+    while (ok) {
+      Piece pc;
+      pc.done = 1;
+      while (item < p.items && unit < s1) {
+        const int n = tree_tiles(a, item / p.HS);
+        const int base = unit + 1;               // unit of the item's tile 0
+        const int lo = max(s0, base), hi = min(s1, base + n);
+        if (n > 0 && lo < hi) {
+          pc.done = 0;
+          pc.row = item / p.HS;
+          pc.hs = item % p.HS;
+          pc.tile0 = lo - base;
+          pc.tiles = hi - lo;
+          // a share that begins behind tile 0 leaves its part in the block's
+          // first place, one that begins with it in the second
+          pc.part = pc.tiles == n ? -1 : 2 * (int)blockIdx.x + (lo > base ? 0 : 1);
+          if (lo == base && lane == 0)           // the block with tile 0 says who has the rest
+            p.cuts[item] = pc.tiles == n ? make_int2(-1, -1)
+                                         : make_int2((int)blockIdx.x, (base + n - 1) / share);
+        }
+        unit += n ? n + 1 : 0;
+        ++item;
+        if (!pc.done) break;
+      }
+      if (lane == 0) {
+        const int is = qc & 1;
+        if (qc >= 2) ok = mbar_wait(&c->info_empty[is], ((qc >> 1) - 1) & 1, &c->abort, a.status);
+        c->info[is] = pc;
+        mbar_arrive(&c->info_full[is]);
+        if (ok && !pc.done) {
+          if (qc >= 1) ok = mbar_wait(&c->q_empty, (qc - 1) & 1, &c->abort, a.status);
+          if (ok) mbar_expect_tx(&c->q_full, 8 * kQBlockBytes);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+      if (pc.done || !ok) break;
+      if (lane < 8)
+        tma_load_2d(smem + OFF_Q + lane * kQBlockBytes, &map_q, 64 * lane, pc.row * a.H + kH * pc.hs, &c->q_full);
+      __syncwarp();
+      ++qc;
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ products
+    if (lane == 0) {
+      const uint32_t id1 = idesc_bf16_f32(128, 64, 0, 0);
+      const uint32_t id2 = idesc_bf16_f32(128, 64, 1, 1);
+      const uint64_t dA1 = smem_desc(smem_u32(smem + OFF_SLOT), 16, 1024, kLayoutSW128);
+      const uint64_t dQ = smem_desc(smem_u32(smem + OFF_Q), 16, 1024, kLayoutSW128);
+      const uint64_t dA2 = smem_desc(smem_u32(smem + OFF_SLOT), kSlotBytes, 1024, kLayoutSW128);
+      const uint64_t dP = smem_desc(smem_u32(smem + OFF_P), 128, 2048, kLayoutNone);
+      int qc = 0, g = 0;
+      bool ok = true;
+      while (ok) {
+        const int is = qc & 1;
+        ok = mbar_wait(&c->info_full[is], (qc >> 1) & 1, &c->abort, a.status);
+        if (!ok) break;
+        const Piece pc = c->info[is];
+        mbar_arrive(&c->info_empty[is]);
+        if (pc.done) break;
+        ok = mbar_wait(&c->q_ready, qc & 1, &c->abort, a.status);
+        tc_fence_after();
+        for (int j = 0; j < pc.tiles && ok; ++j) {
+          const int sb = g & 1;
+          const uint32_t s_tmem = tmem + 64 * sb;
+#pragma unroll
+          for (int kb = 0; kb < kSlots; ++kb) {
+            ok = ok && mbar_wait(&c->full[kb], g & 1, &c->abort, a.status);
+            fence_proxy_async_smem();               // cp.async writes -> tensor-core reads
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              umma_f16_ss(s_tmem, dA1 + (uint64_t)((kb * kSlotBytes + 32 * ks) >> 4),
+                          dQ + (uint64_t)((kb * kQBlockBytes + 32 * ks) >> 4), id1, (kb | ks) != 0);
+          }
+          // the rotated dims once more, against q's low part
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            umma_f16_ss(s_tmem, dA1 + (uint64_t)((7 * kSlotBytes + 32 * ks) >> 4),
+                        dQ + (uint64_t)((8 * kQBlockBytes + 32 * ks) >> 4), id1, 1u);
+          umma_commit(&c->s_full[sb]);
+          if (j == pc.tiles - 1) umma_commit(&c->q_empty);
+          if (!ok) break;
+          ok = mbar_wait(&c->p_ready[sb], (g >> 1) & 1, &c->abort, a.status);
+          if (ok && j == 0 && qc >= 1) ok = mbar_wait(&c->o_empty, (qc - 1) & 1, &c->abort, a.status);
+          tc_fence_after();
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              umma_f16_ss(tmem + 128 + 64 * m, dA2 + (uint64_t)((2 * m * kSlotBytes + 2048 * ks) >> 4),
+                          dP + (uint64_t)((256 * ks) >> 4), id2, (j > 0 || ks > 0) ? 1u : 0u);
+            umma_commit(&c->empty[2 * m]);
+            umma_commit(&c->empty[2 * m + 1]);
+          }
+          ++g;
+        }
+        umma_commit(&c->o_full);
+        ++qc;
+      }
+      umma_commit(&c->fin);                        // every product completes before TMEM is released
+      mbar_wait(&c->fin, 0, &c->abort, a.status, 200000000ull);
+    }
+    __syncwarp();
+  } else if (warp < 4 || warp >= 12) {
+    // ------------------------------------------------------------ key rows
+    const int gw = warp < 4 ? warp - 2 : warp - 10;
+    const int chunk = lane & 7;
+    int qc = 0, g = 0;
+    bool ok = true;
+    while (ok) {
+      const int is = qc & 1;
+      ok = mbar_wait(&c->info_full[is], (qc >> 1) & 1, &c->abort, a.status);
+      ok = __all_sync(0xffffffffu, ok);
+      const Piece pc = c->info[is];
+      __syncwarp();
+      mbar_arrive(&c->info_empty[is]);
+      if (!ok || pc.done) break;
+      const TreeRow r = tree_row(a, pc.row);
+      const int4 bits = *reinterpret_cast<const int4*>(a.plan + (size_t)pc.row * kPlanWords + 4);
+      for (int j = 0; j < pc.tiles && ok; ++j) {
+        // lane i looks up key row 32 gw + i; this runs while the tile before
+        // is still in use
+        const bf16* src =
+            key_row(a, r, bits, pc.row, (long long)(pc.tile0 + j) * kTile + 32 * gw + lane);
+        const uint32_t live = __ballot_sync(0xffffffffu, src != nullptr);
+        if (lane == 0) {
+          // tile g - 2's bits have been read: its O products completed before
+          // this warp could fill the slots of tile g - 1
+          c->valid[g & 1][gw] = live;
+          mbar_arrive(&c->valid_full[g & 1]);
+        }
+        const bf16* rows[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          rows[i] = reinterpret_cast<const bf16*>(
+              __shfl_sync(0xffffffffu, (unsigned long long)src, 4 * i + (lane >> 3)));
+        for (int kb = 0; kb < kSlots; ++kb) {
+          if (lane == 0 && g >= 1) ok = mbar_wait(&c->empty[kb], (g - 1) & 1, &c->abort, a.status);
+          ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+          if (!ok) break;
+          const uint32_t d0 = smem_u32(smem + OFF_SLOT + kb * kSlotBytes);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = 32 * gw + 4 * i + (lane >> 3);
+            const bool key = rows[i] != nullptr;
+            const bf16* from = key ? rows[i] + kb * 64 + chunk * 8 : reinterpret_cast<const bf16*>(a.q);
+            cp_async_16_or_zero(d0 + row * 128 + ((chunk ^ (row & 7)) << 4), from, key);
+          }
+          cp_async_mbar_arrive(&c->full[kb]);
+        }
+        ++g;
+      }
+      ++qc;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else {
+    // ------------------------------------------------------------ softmax and output
+    const int ts = threadIdx.x - 128;         // 0..255
+    const int quarter = warp & 3;             // TMEM lane quarter
+    const int hh = (warp - 4) >> 2;           // head half
+    const int h0 = 32 * hh;
+    const int krow = 32 * quarter + lane;     // key row / dim row owned in TMEM
+    const uint32_t lane_base = (uint32_t)(32 * quarter) << 16;
+    const float c1 = a.scale * kLog2e;
+    const uint64_t F = ts < kR / 2 ? turn_fraction(a.inv_freq[ts]) : 0;
+    const auto fmax2 = [](float x, float y) { return fmaxf(x, y); };
+    const auto fadd2 = [](float x, float y) { return x + y; };
+
+    auto next_piece = [&](int qc, Piece& pc) -> bool {
+      const int is = qc & 1;
+      mbar_wait(&c->info_full[is], (qc >> 1) & 1, &c->abort, a.status);
+      pc = c->info[is];
+      mbar_arrive(&c->info_empty[is]);
+      if (ts == 0) c->decision = (c->abort || pc.done) ? 1 : 0;
+      if (!pc.done && ts < kR / 2) {
+        float cs, sn;
+        turn_cos_sin(a.plan[(size_t)pc.row * kPlanWords + 2], F, &cs, &sn);
+        c->cs[is][ts] = make_float2(cs, sn);
+      }
+      named_bar_sync(1, kSoftThreads);
+      const bool more = c->decision == 0;
+      named_bar_sync(1, kSoftThreads);
+      return more;
+    };
+    // Rotate the last 64 dims of each head (four threads a head), as a high
+    // and a low bf16 term.
+    auto setup_query = [&](int qc) {
+      const int h = ts >> 2, part = ts & 3;
+      mbar_wait(&c->q_full, qc & 1, &c->abort, a.status);
+      uint8_t* hi_row = smem + OFF_Q + 7 * kQBlockBytes + h * 128;
+      uint8_t* lo_row = smem + OFF_Q + 8 * kQBlockBytes + h * 128;
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) {
+        const int ch = 2 * part + cc;                        // 16-byte chunk of dims 448..511
+        const int at = (ch ^ (h & 7)) * 16;
+        uint4 u = *reinterpret_cast<uint4*>(hi_row + at), v;
+        __nv_bfloat162* hv = reinterpret_cast<__nv_bfloat162*>(&u);
+        __nv_bfloat162* lv = reinterpret_cast<__nv_bfloat162*>(&v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 cs = c->cs[qc & 1][4 * ch + i];
+          float2 f = __bfloat1622float2(hv[i]);
+          rot_pair(f.x, f.y, cs.x, cs.y);
+          hv[i] = __floats2bfloat162_rn(f.x, f.y);
+          const float2 b = __bfloat1622float2(hv[i]);
+          lv[i] = __floats2bfloat162_rn(f.x - b.x, f.y - b.y);
+        }
+        *reinterpret_cast<uint4*>(hi_row + at) = u;
+        *reinterpret_cast<uint4*>(lo_row + at) = v;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&c->q_ready);
+    };
+
+    int qc = 0, g = 0;
+    Piece pc;
+    bool more = next_piece(0, pc);
+    if (more) setup_query(0);
+    while (more) {
+      float lsum[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) lsum[i] = 0.f;
+      for (int j = 0; j < pc.tiles; ++j) {
+        const int sb = g & 1;
+        mbar_wait(&c->valid_full[sb], (g >> 1) & 1, &c->abort, a.status);
+        const bool valid = (c->valid[sb][quarter] >> lane) & 1u;
+        mbar_wait(&c->s_full[sb], (g >> 1) & 1, &c->abort, a.status);
+        tc_fence_after();
+        float v[32];
+        tmem_ld32(tmem + lane_base + 64 * sb + h0, v);
+        tmem_wait_ld();
+        bool over = j == 0;
+        if (j > 0 && valid) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float4 m4 = *reinterpret_cast<const float4*>(&c->m[h0 + i]);
+            over = over || v[i] * c1 > m4.x + kRaise || v[i + 1] * c1 > m4.y + kRaise ||
+                   v[i + 2] * c1 > m4.z + kRaise || v[i + 3] * c1 > m4.w + kRaise;
+          }
+        }
+        if (bar_any(2 + hh, 128, over)) {
+          // raise this half's shifts to the running maximum and rescale
+          float r[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) r[i] = valid ? v[i] * c1 : -INFINITY;
+          c->hmax[quarter][h0 + lane] = fold_lanes(r, lane, fmax2);
+          named_bar_sync(2 + hh, 128);
+          const int hd = h0 + lane;
+          const float old = j == 0 ? -INFINITY : c->m[hd];
+          const float m = fmaxf(fmaxf(fmaxf(c->hmax[0][hd], c->hmax[1][hd]), fmaxf(c->hmax[2][hd], c->hmax[3][hd])), old);
+          named_bar_sync(2 + hh, 128);            // every warp has read the old shifts
+          if (quarter == 0) {
+            c->m[hd] = m;
+            c->fac[hd] = old == m ? 1.f : ex2_approx(old - m);
+          }
+          named_bar_sync(2 + hh, 128);
+          if (j > 0) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) lsum[i] *= c->fac[h0 + i];
+            for (int mb = 0; mb < 4; ++mb) {      // the products into O^T so far completed before S
+              tmem_ld32(tmem + lane_base + 128 + 64 * mb + h0, r);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) r[i] *= c->fac[h0 + i];
+              tmem_st32(tmem + lane_base + 128 + 64 * mb + h0, r);
+            }
+          }
+        }
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          const float4 m4 = *reinterpret_cast<const float4*>(&c->m[h0 + i]);
+          const float x0 = valid ? ex2_approx(fmaf(v[i], c1, -m4.x)) : 0.f;
+          const float x1 = valid ? ex2_approx(fmaf(v[i + 1], c1, -m4.y)) : 0.f;
+          const float x2 = valid ? ex2_approx(fmaf(v[i + 2], c1, -m4.z)) : 0.f;
+          const float x3 = valid ? ex2_approx(fmaf(v[i + 3], c1, -m4.w)) : 0.f;
+          // denominators from the unrounded values: the roundings of P average
+          // out in the output, and lse stays exact to fp32
+          lsum[i] += x0;
+          lsum[i + 1] += x1;
+          lsum[i + 2] += x2;
+          lsum[i + 3] += x3;
+          pk[i / 2] = pack_bf16x2(x0, x1);
+          pk[i / 2 + 1] = pack_bf16x2(x2, x3);
+        }
+        // P^T [8-head column block][key].  One buffer: this tile's S completing
+        // implies that the previous tile's O products have completed.
+        uint8_t* prow = smem + OFF_P + krow * 16 + (4 * hh) * 2048;
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc)
+          *reinterpret_cast<uint4*>(prow + cc * 2048) =
+              make_uint4(pk[4 * cc], pk[4 * cc + 1], pk[4 * cc + 2], pk[4 * cc + 3]);
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(&c->p_ready[sb]);
+        ++g;
+      }
+      // denominators of this piece, and its shifts
+      c->part_l[quarter][h0 + lane] = fold_lanes(lsum, lane, fadd2);
+      named_bar_sync(1, kSoftThreads);
+      float m_row = 0.f, l_row = 0.f;
+      if (ts < kH) {
+        m_row = c->m[ts];
+        l_row = (c->part_l[0][ts] + c->part_l[1][ts]) + (c->part_l[2][ts] + c->part_l[3][ts]);
+      }
+      const Piece cur = pc;
+      const int par = qc & 1;
+      // the next piece's queries go first, so that its first products overlap
+      // this piece's output
+      more = next_piece(qc + 1, pc);
+      if (more) setup_query(qc + 1);
+
+      const size_t orow = (size_t)cur.row * a.H + kH * cur.hs;
+      PartHead* head = nullptr;
+      float* part = nullptr;
+      if (cur.part >= 0) {
+        char* at = p.parts + (size_t)cur.part * kPartBytes;
+        part = reinterpret_cast<float*>(at);
+        head = reinterpret_cast<PartHead*>(at + kPartFloats * 4);
+        if (ts < kH) {
+          head->m[ts] = m_row;
+          head->l[ts] = l_row;
+        }
+      } else {
+        if (ts < kH) {
+          float m = m_row, l = l_row, f = 1.f;
+          if (a.sink != nullptr) {
+            const float s2 = a.sink[kH * cur.hs + ts] * kLog2e;
+            m = fmaxf(m_row, s2);
+            f = m_row == m ? 1.f : ex2_approx(m_row - m);
+            l = l_row * f + (s2 > -INFINITY ? ex2_approx(s2 - m) : 0.f);
+          }
+          c->inv[ts] = l == 0.f ? 0.f : f / l;
+          if (a.lse) a.lse[orow + ts] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+        }
+        named_bar_sync(1, kSoftThreads);
+      }
+      mbar_wait(&c->o_full, par, &c->abort, a.status);
+      tc_fence_after();
+      bf16* obase = reinterpret_cast<bf16*>(a.o) + (orow + h0) * kD + krow;
+      for (int m = 0; m < 4; ++m) {
+        float v[32];
+        tmem_ld32(tmem + lane_base + 128 + 64 * m + h0, v);
+        tmem_wait_ld();
+        if (m == 3) {
+          tc_fence_before();
+          mbar_arrive(&c->o_empty);
+        }
+        if (part != nullptr) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) part[(size_t)(h0 + i) * kD + 128 * m + krow] = v[i];
+          continue;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] *= c->inv[h0 + i];
+        if (m == 3 && quarter >= 2) {             // dims 448..511 turn back; the pair's partner is the next lane
+          const float2 cs = c->cs[par][(krow - 64) >> 1];
+          const bool odd = lane & 1;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float other = __shfl_xor_sync(0xffffffffu, v[i], 1);
+            v[i] = odd ? v[i] * cs.x - other * cs.y : v[i] * cs.x + other * cs.y;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) obase[(size_t)i * kD + 128 * m] = __float2bfloat16_rn(v[i]);
+      }
+      named_bar_sync(1, kSoftThreads);            // this piece's shifts and factors are read
+      ++qc;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Join of cut items: block (item, eight heads), 32 threads a head with 16 dims
+// each.  sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s over the item's parts.
+// ---------------------------------------------------------------------------
+constexpr int kJoinHeads = 8;
+
+__global__ void __launch_bounds__(kJoinHeads * 32) tree_join_kernel(const Args p) {
+  const TreeArgs& a = p.t;
+  const int item = blockIdx.x, row = item / p.HS, hs = item % p.HS;
+  const int h = blockIdx.y * kJoinHeads + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const TreeRow r = tree_row(a, row);
+  if (!r.live) return;
+  const int2 cut = p.cuts[item];
+  if (cut.x < 0) return;
+  // the first block holds the item from tile 0 (its second place), the others
+  // begin inside it (their first place)
+  auto place = [&](int cta) { return p.parts + (size_t)(2 * cta + (cta == cut.x ? 1 : 0)) * kPartBytes; };
+  float m = -INFINITY;
+  for (int s = cut.x; s <= cut.y; ++s)
+    m = fmaxf(m, reinterpret_cast<const PartHead*>(place(s) + kPartFloats * 4)->m[h]);
+  float l = 0.f;
+  if (a.sink != nullptr) {
+    const float s2 = a.sink[kH * hs + h] * kLog2e;
+    m = fmaxf(m, s2);
+    if (s2 > -INFINITY) l = ex2_approx(s2 - m);
+  }
+  float o[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) o[i] = 0.f;
+  for (int s = cut.x; s <= cut.y; ++s) {
+    const char* at = place(s);
+    const PartHead* hd = reinterpret_cast<const PartHead*>(at + kPartFloats * 4);
+    const float ms = hd->m[h];
+    const float f = ms == m ? 1.f : ex2_approx(ms - m);
+    l = fmaf(hd->l[h], f, l);
+    const float4* src = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(at) + (size_t)h * kD) + lane;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = src[32 * i];
+      o[4 * i] = fmaf(v.x, f, o[4 * i]);
+      o[4 * i + 1] = fmaf(v.y, f, o[4 * i + 1]);
+      o[4 * i + 2] = fmaf(v.z, f, o[4 * i + 2]);
+      o[4 * i + 3] = fmaf(v.w, f, o[4 * i + 3]);
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const size_t orow = (size_t)row * a.H + kH * hs + h;
+  if (a.lse && lane == 0) a.lse[orow] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+  bf16* dst = reinterpret_cast<bf16*>(a.o) + orow * kD + 4 * lane;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float x[4] = {o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv};
+    const int dim = 128 * i + 4 * lane;
+    if (dim >= kD - kR) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float cs, sn;
+        turn_cos_sin(r.t, turn_fraction(a.inv_freq[(dim - (kD - kR)) / 2 + e]), &cs, &sn);
+        rot_pair(x[2 * e], x[2 * e + 1], cs, -sn);
+      }
+    }
+    uint2 u;
+    u.x = pack_bf16x2(x[0], x[1]);
+    u.y = pack_bf16x2(x[2], x[3]);
+    *reinterpret_cast<uint2*>(dst + 128 * i) = u;
+  }
+}
+
+}  // namespace
+
+bool tree_tc_supported(const v4_config& c) {
+  return c.dtype == V4_BF16 && c.n_heads >= kH && c.n_heads % kH == 0 && c.n_heads <= 8 * kH && c.head_dim == kD &&
+         c.rope_dim == kR;
+}
+
+size_t tree_tc_workspace(const v4_config& c, int n_rows) {
+  return (size_t)2 * kMaxCtas * kPartBytes + (((size_t)n_rows * (c.n_heads / kH) * sizeof(int2) + 255) & ~(size_t)255);
+}
+
+cudaError_t launch_tree_tc(const TreeArgs& a, void* workspace, cudaStream_t st) {
+  Args p;
+  p.t = a;
+  p.HS = a.H / kH;
+  p.items = a.n_rows * p.HS;
+  p.parts = (char*)workspace;
+  p.cuts = (int2*)((char*)workspace + (size_t)2 * kMaxCtas * kPartBytes);
+  CUtensorMap mq;
+  if (make_tmap_bf16_2d(&mq, a.q, kD, (uint64_t)a.n_rows * a.H, 64, 64, true)) return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  if (e != cudaSuccess) return e;
+  int sms = 0, dev = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int grid = sms < kMaxCtas ? sms : kMaxCtas;
+  tree_tc_kernel<<<grid, kThreads, kSmemBytes, st>>>(mq, p);
+  note_launch();
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  {
+    StageTiming ps(17, st);
+    tree_join_kernel<<<dim3(p.items, kH / kJoinHeads), kJoinHeads * 32, 0, st>>>(p);
+    note_launch();
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace v4
