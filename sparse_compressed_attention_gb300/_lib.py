@@ -354,38 +354,59 @@ def v4_attn_layer_fwd(cfg, inputs, outputs, workspace, stream=None):
     return outputs
 
 
-def _shaped(t, name, shape, dtype):
-    """Pointer of a dense tensor of exactly this shape on the current device."""
-    p = _ptr(t, name, dtype)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    return _here(t, name, p)
+# The serving calls are short (a few microseconds on the device), so their
+# checks are kept cheap: one combined test per tensor, the slow path only to
+# say what is wrong, and the raw stream of the current device.
+_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _here(t, name, p):
-    """The call runs on the current device's stream: tensors of another one are refused."""
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError("%s is on %s, the current device is cuda:%d" % (name, t.device, torch.cuda.current_device()))
-    return p
+def _stream_on(stream, dev):
+    if stream is None:
+        return _raw_stream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
-def _strided(t, name, dims):
-    """Pointer of a tensor whose last dim is dense; its other strides go to the library."""
+def _current(t, name):
+    """Index of the current device; a host tensor is refused before CUDA is touched."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a tensor" % name)
     if not t.is_cuda:
         raise ValueError("%s must be on a CUDA device" % name)
+    return _device()
+
+
+def _shaped(t, name, shape, dtype, dev):
+    """Pointer of a dense tensor of exactly this shape on device `dev` (the current one)."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev \
+            and t.is_contiguous():
+        return t.data_ptr()
+    _ptr(t, name, dtype)
+    if t.get_device() != dev:
+        raise ValueError("%s is on %s, the current device is cuda:%d" % (name, t.device, dev))
+    raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+
+
+def _strided(t, name, dims, dev):
+    """Pointer and strides of a tensor whose last dim is dense; the library checks the strides."""
+    if isinstance(t, torch.Tensor) and t.get_device() == dev and t.dim() == dims and t.dtype in _STORAGE_CODE:
+        st = t.stride()
+        if st[-1] == 1 or t.shape[-1] <= 1:
+            return t.data_ptr(), st
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be on a CUDA device" % name)
+    if t.get_device() != dev:
+        raise ValueError("%s is on %s, the current device is cuda:%d" % (name, t.device, dev))
     if t.dim() != dims:
         raise ValueError("%s must have %d dims, got %d" % (name, dims, t.dim()))
-    if t.dtype not in (torch.bfloat16, torch.float32):
+    if t.dtype not in _STORAGE_CODE:
         raise TypeError("%s must be bfloat16 or float32, got %s" % (name, t.dtype))
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError("%s must be contiguous in its last dim" % name)
-    return _here(t, name, t.data_ptr())
+    raise ValueError("%s must be contiguous in its last dim" % name)
 
 
-def _storage_code(t):
-    return V4_BF16 if t.dtype == torch.bfloat16 else V4_F32
+_STORAGE_CODE = {torch.bfloat16: V4_BF16, torch.float32: V4_F32}
 
 
 def v4_rope(x, pos, inv_freq, out, rope_begin=None, layout=V4_ROPE_INTERLEAVED, inverse=False, mscale=1.0,
@@ -395,57 +416,62 @@ def v4_rope(x, pos, inv_freq, out, rope_begin=None, layout=V4_ROPE_INTERLEAVED, 
     R = 2 * len(inv_freq); rope_begin defaults to the last R dims.  x and out may be
     strided views (dense last dim).  The gradient of x is the call on the gradient of out
     with inverse=True and the same mscale."""
-    px, po = _strided(x, "x", 3), _strided(out, "out", 3)
-    if out.shape != x.shape or out.dtype != x.dtype:
+    dev = _current(x, "x")
+    px, sx = _strided(x, "x", 3, dev)
+    po, so = _strided(out, "out", 3, dev)
+    if out.shape != x.shape or out.dtype is not x.dtype:
         raise ValueError("out must have x's shape and type")
     rows, heads, dim = x.shape
-    R = 2 * inv_freq.numel()
-    begin = dim - R if rope_begin is None else int(rope_begin)
-    if x.numel() == 0:
+    half = inv_freq.numel()
+    if not rows or not heads or not dim:
         return out
-    _check(lib().v4_rope(px, rows, heads, dim, x.stride(0), x.stride(1), _shaped(pos, "pos", (rows,), torch.int32),
-                         _shaped(inv_freq, "inv_freq", (R // 2,), torch.float32), R, begin, int(layout),
-                         int(bool(inverse)), float(mscale), _storage_code(x), po, out.stride(0), out.stride(1),
-                         _stream(stream)))
+    _check(lib().v4_rope(px, rows, heads, dim, sx[0], sx[1], _shaped(pos, "pos", (rows,), torch.int32, dev),
+                         _shaped(inv_freq, "inv_freq", (half,), torch.float32, dev), 2 * half,
+                         dim - 2 * half if rope_begin is None else rope_begin, layout, 1 if inverse else 0, mscale,
+                         _STORAGE_CODE[x.dtype], po, so[0], so[1], _stream_on(stream, dev)))
     return out
 
 
 def v4_cache_append(x, pos, inv_freq, slot, cache, stream=None):
     """Store rows x [rows, dim], rotated at pos (None: as they are), at rows slot of cache [..., dim]."""
-    px = _strided(x, "x", 2)
+    dev = _current(x, "x")
+    px, sx = _strided(x, "x", 2, dev)
     rows, dim = x.shape
-    pc = _here(cache, "cache", _ptr(cache, "cache", x.dtype))
-    if cache.shape[-1] != dim:
-        raise ValueError("cache rows must have %d elements, got %d" % (dim, cache.shape[-1]))
-    R = 2 * inv_freq.numel() if pos is not None else 0
-    if x.numel() == 0:
+    if not isinstance(cache, torch.Tensor) or cache.dim() < 2 or cache.shape[-1] != dim:
+        raise ValueError("cache must be a tensor [..., %d]" % dim)
+    pc = _shaped(cache, "cache", cache.shape, x.dtype, dev)
+    if not rows or not dim:
         return cache
-    _check(lib().v4_cache_append(px, rows, dim, x.stride(0),
-                                 None if pos is None else _shaped(pos, "pos", (rows,), torch.int32),
-                                 None if pos is None else _shaped(inv_freq, "inv_freq", (R // 2,), torch.float32), R,
-                                 _shaped(slot, "slot", (rows,), torch.int32), cache.numel() // dim,
-                                 _storage_code(x), pc, _stream(stream)))
+    half = 0 if pos is None else inv_freq.numel()
+    _check(lib().v4_cache_append(px, rows, dim, sx[0],
+                                 None if pos is None else _shaped(pos, "pos", (rows,), torch.int32, dev),
+                                 None if pos is None else _shaped(inv_freq, "inv_freq", (half,), torch.float32, dev),
+                                 2 * half, _shaped(slot, "slot", (rows,), torch.int32, dev), cache.numel() // dim,
+                                 _STORAGE_CODE[x.dtype], pc, _stream_on(stream, dev)))
     return cache
 
 
 def v4_tree_plan(node_begin, seq_len, parent, plan, pos=None, slot=None, block_table=None, page_size=0, n_slots=0,
                  stream=None):
     """Describe drafted trees (see the header): plan [n_rows, 8], and optionally pos and slot [n_rows]."""
+    dev = _current(plan, "plan")
     B, n = seq_len.numel(), plan.shape[0]
     i32 = torch.int32
     blocks = 0
     if slot is not None:
-        if block_table is None or block_table.dim() != 2:
+        if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
             raise ValueError("slot needs block_table [batch, max_blocks]")
         blocks = block_table.shape[1]
     if n == 0:
         return plan
-    _check(lib().v4_tree_plan(B, n, _shaped(node_begin, "node_begin", (B + 1,), i32), _shaped(seq_len, "seq_len", (B,), i32),
-                              None if parent is None else _shaped(parent, "parent", (n,), i32),
-                              None if slot is None else _shaped(block_table, "block_table", (B, blocks), i32),
-                              blocks, int(page_size), int(n_slots), _shaped(plan, "plan", (n, 8), i32),
-                              None if pos is None else _shaped(pos, "pos", (n,), i32),
-                              None if slot is None else _shaped(slot, "slot", (n,), i32), _stream(stream)))
+    _check(lib().v4_tree_plan(B, n, _shaped(node_begin, "node_begin", (B + 1,), i32, dev),
+                              _shaped(seq_len, "seq_len", (B,), i32, dev),
+                              None if parent is None else _shaped(parent, "parent", (n,), i32, dev),
+                              None if slot is None else _shaped(block_table, "block_table", (B, blocks), i32, dev),
+                              blocks, int(page_size), int(n_slots), _shaped(plan, "plan", (n, 8), i32, dev),
+                              None if pos is None else _shaped(pos, "pos", (n,), i32, dev),
+                              None if slot is None else _shaped(slot, "slot", (n,), i32, dev),
+                              _stream_on(stream, dev)))
     return plan
 
 
@@ -459,56 +485,56 @@ def alloc_tree_workspace(cfg, n_rows, device=None):
     return torch.empty(max(v4_tree_workspace_size(cfg, n_rows), 256), dtype=torch.uint8, device=device or "cuda")
 
 
+def _paged(inputs, kind, used, D, B, dt, dev):
+    """Cache pointer, table pointer, slots, blocks, page size of one paged cache."""
+    if not used:
+        return None, None, 0, 0, 0
+    cache, table = inputs.get(kind + "_cache"), inputs.get(kind + "_table")
+    if not isinstance(cache, torch.Tensor) or cache.dim() != 3 or cache.shape[2] != D:
+        raise ValueError("%s_cache must be a tensor [pages, page_size, %d]" % (kind, D))
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError("%s_table must be a tensor [batch, blocks]" % kind)
+    shape, blocks = cache.shape, table.shape[1]
+    return (_shaped(cache, kind + "_cache", shape, dt, dev),
+            _shaped(table, kind + "_table", (B, blocks), torch.int32, dev), shape[0] * shape[1], blocks, shape[1])
+
+
 def v4_tree_mqa_fwd(cfg, inputs, o, lse, workspace, stream=None):
     """Attention of planned rows over paged caches.  inputs: a dict keyed like v4_tree_inputs' pointers, with
     tok_cache / ent_cache [pages, page_size, D] and tok_table / ent_table [B, blocks]."""
     dt, i32, f32 = _storage(cfg), torch.int32, torch.float32
-    q = inputs["q"]
-    n, H, D, B = q.shape[0], cfg.n_heads, cfg.head_dim, cfg.batch
-    vin = v4_tree_inputs()
-    vin.n_rows = n
-    vin.q = _shaped(q, "q", (n, H, D), dt)
-    vin.plan = _shaped(inputs["plan"], "plan", (n, 8), i32)
-    for kind, used in (("tok", cfg.window != 0), ("ent", cfg.ratio > 0)):
-        if not used:
-            continue
-        cache, table = inputs.get(kind + "_cache"), inputs.get(kind + "_table")
-        p = _ptr(cache, kind + "_cache", dt)
-        if cache.dim() != 3 or cache.shape[2] != D:
-            raise ValueError("%s_cache must have shape [pages, page_size, %d], got %s" % (kind, D, tuple(cache.shape)))
-        setattr(vin, kind + "_cache", _here(cache, kind + "_cache", p))
-        if not isinstance(table, torch.Tensor) or table.dim() != 2:
-            raise ValueError("%s_table must be a tensor [batch, blocks]" % kind)
-        setattr(vin, kind + "_table", _shaped(table, kind + "_table", (B, table.shape[1]), i32))
-        setattr(vin, kind + "_slots", cache.shape[0] * cache.shape[1])
-        setattr(vin, kind + "_page", cache.shape[1])
-        setattr(vin, kind + "_blocks", table.shape[1])
-    if cfg.ratio > 0:
-        vin.ent_len = _shaped(inputs.get("ent_len"), "ent_len", (B,), i32)
-    if cfg.topk > 0:
-        vin.idx = _shaped(inputs.get("idx"), "idx", (n, cfg.topk), i32)
-    if inputs.get("sink") is not None:
-        vin.sink = _shaped(inputs["sink"], "sink", (H,), f32)
-    if cfg.rope_dim > 0:
-        vin.inv_freq = _shaped(inputs.get("inv_freq"), "inv_freq", (cfg.rope_dim // 2,), f32)
-    _check(lib().v4_tree_mqa_fwd(C.byref(cfg), C.byref(vin), _shaped(o, "o", (n, H, D), dt),
-                                 None if lse is None else _shaped(lse, "lse", (n, H), f32),
-                                 _here(workspace, "workspace", _ptr(workspace, "workspace", torch.uint8)),
-                                 workspace.numel(), _stream(stream)))
+    q, sink, half = inputs["q"], inputs.get("sink"), cfg.rope_dim // 2
+    dev = _current(q, "q")
+    n, H, D, B, r, K = q.shape[0], cfg.n_heads, cfg.head_dim, cfg.batch, cfg.ratio, cfg.topk
+    tc, tt, ts, tb, tp = _paged(inputs, "tok", cfg.window != 0, D, B, dt, dev)
+    ec, et, es, eb, ep = _paged(inputs, "ent", r > 0, D, B, dt, dev)
+    shape = (n, H, D)
+    vin = v4_tree_inputs(
+        _shaped(q, "q", shape, dt, dev), _shaped(inputs["plan"], "plan", (n, 8), i32, dev), tc, tt, ec, et,
+        _shaped(inputs.get("ent_len"), "ent_len", (B,), i32, dev) if r > 0 else None,
+        _shaped(inputs.get("idx"), "idx", (n, K), i32, dev) if K > 0 else None,
+        None if sink is None else _shaped(sink, "sink", (H,), f32, dev),
+        _shaped(inputs.get("inv_freq"), "inv_freq", (half,), f32, dev) if half else None,
+        ts, es, n, tb, tp, eb, ep)
+    _check(lib().v4_tree_mqa_fwd(C.byref(cfg), C.byref(vin), _shaped(o, "o", shape, dt, dev),
+                                 None if lse is None else _shaped(lse, "lse", (n, H), f32, dev),
+                                 _shaped(workspace, "workspace", workspace.shape, torch.uint8, dev), workspace.numel(),
+                                 _stream_on(stream, dev)))
     return o
 
 
 def v4_w4_pack(w, group_size, codes, scales, stream=None):
     """Quantise w [groups, K, N] bf16 to codes [groups, N, K/2] uint8 and scales [groups, N, K/group_size] bf16."""
-    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+    dev = _current(w, "w")
+    if w.dim() != 3:
         raise ValueError("w must be a tensor [groups, K, N]")
     G, K, N = w.shape
     gs = int(group_size)
     if gs not in (32, 64, 128):
         raise ValueError("group_size must be 32, 64 or 128")
-    _check(lib().v4_w4_pack(_shaped(w, "w", (G, K, N), torch.bfloat16), G, K, N, gs,
-                            _shaped(codes, "codes", (G, N, K // 2), torch.uint8),
-                            _shaped(scales, "scales", (G, N, K // gs), torch.bfloat16), _stream(stream)))
+    _check(lib().v4_w4_pack(_shaped(w, "w", (G, K, N), torch.bfloat16, dev), G, K, N, gs,
+                            _shaped(codes, "codes", (G, N, K // 2), torch.uint8, dev),
+                            _shaped(scales, "scales", (G, N, K // gs), torch.bfloat16, dev), _stream_on(stream, dev)))
     return codes, scales
 
 
@@ -516,18 +542,16 @@ def v4_w4_proj(x, codes, scales, y, norm_dim=0, eps=1e-6, norm_w=None, stream=No
     """y [rows, groups, N] = x [rows, groups, K] . dequantised weights, RMS-normalised over runs of norm_dim outputs."""
     if not isinstance(codes, torch.Tensor) or codes.dim() != 3 or not isinstance(scales, torch.Tensor) or scales.dim() != 3:
         raise ValueError("codes must be [groups, N, K/2] and scales [groups, N, K/group_size]")
-    G, N, K = codes.shape[0], codes.shape[1], codes.shape[2] * 2
-    if scales.shape[2] < 1 or K % scales.shape[2]:
+    dev = _current(x, "x")
+    G, N, half = codes.shape
+    K, sg, rows, b16 = 2 * half, scales.shape[2], x.shape[0], torch.bfloat16
+    if sg < 1 or K % sg:
         raise ValueError("scales must have shape [groups, N, K/group_size]")
-    gs = K // scales.shape[2]
-    rows = x.shape[0]
-    b16 = torch.bfloat16
-    px, py = _shaped(x, "x", (rows, G, K), b16), _shaped(y, "y", (rows, G, N), b16)
-    _check(lib().v4_w4_proj(px, rows, G, K, N, gs, _shaped(codes, "codes", (G, N, K // 2), torch.uint8),
-                            _shaped(scales, "scales", (G, N, K // gs), b16), int(norm_dim), float(eps),
-                            None if norm_w is None or not norm_dim else _shaped(norm_w, "norm_w", (int(norm_dim),),
-                                                                                torch.float32),
-                            py, _stream(stream)))
+    px, py = _shaped(x, "x", (rows, G, K), b16, dev), _shaped(y, "y", (rows, G, N), b16, dev)
+    _check(lib().v4_w4_proj(px, rows, G, K, N, K // sg, _shaped(codes, "codes", (G, N, half), torch.uint8, dev),
+                            _shaped(scales, "scales", (G, N, sg), b16, dev), norm_dim, eps,
+                            _shaped(norm_w, "norm_w", (norm_dim,), torch.float32, dev) if norm_w is not None and norm_dim
+                            else None, py, _stream_on(stream, dev)))
     return y
 
 

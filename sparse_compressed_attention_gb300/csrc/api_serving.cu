@@ -211,7 +211,7 @@ v4_status v4_tree_workspace_size(const v4_config* cfg, int32_t n_rows, size_t* b
   TRY(validate_config(cfg));
   if (!bytes) return bad("bytes is NULL");
   if (n_rows < 0) return bad("n_rows must be >= 0");
-  *bytes = tree_on_tc(*cfg) ? tree_tc_workspace(*cfg, n_rows) : 0;
+  *bytes = tree_on_tc(*cfg) ? tree_tc_workspace() : 0;
   return V4_OK;
 }
 

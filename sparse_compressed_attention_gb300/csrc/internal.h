@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "v4attn.h"
 
 namespace v4 {
@@ -37,6 +39,27 @@ class StageTiming {
  private:
   void* rec_;
   cudaStream_t st_;
+};
+
+// Runs a set-up call once per device (kernel attributes, which stay set for
+// the process): the calls it guards cost more than a short kernel's launch.
+class OncePerDevice {
+ public:
+  template <typename F>
+  cudaError_t run(F f) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kDevices) return f();
+    if (done_[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    e = f();                                     // twice in a race: harmless
+    if (e == cudaSuccess) done_[dev].store(true, std::memory_order_release);
+    return e;
+  }
+
+ private:
+  static constexpr int kDevices = 128;
+  std::atomic<bool> done_[kDevices] = {};
 };
 
 // Workspace carve-up for one configuration (Sq = q_rows).  Offsets are

@@ -3,10 +3,11 @@
 //
 // y = mscale * R(sign * pos * f) x on the rotated dims, a copy elsewhere; the
 // gradient is the same map with the sign turned.  Memory bound: every element
-// is read and written once.  A block takes a tile of rows x heads, forms the
-// tile's (row, pair) angles once in shared memory (they are shared by the
-// heads), and streams the tile in 8-element units, all of a thread's loads in
-// flight before the angles are formed.
+// is read and written once.  A block takes a tile of rows x heads and streams
+// it in units of eight elements: a thread's loads are all in flight, as raw
+// bits (most units of a partly rotated head are copies and are never
+// converted), while the block forms the tile's (row, pair) angles once in
+// shared memory for all heads.
 #include <math.h>
 
 #include "common.cuh"
@@ -23,9 +24,8 @@ constexpr int kMaxAngles = 1024;                 // (row, pair) angles of a tile
 
 // Division by a run-time constant below 2^31: n / d for n < 2^31.
 struct FastDiv {
-  uint32_t mul, sh, d;
+  uint32_t mul, sh;
   void set(uint32_t v) {
-    d = v;
     sh = 0;
     while ((1u << sh) < v) ++sh;                 // 2^sh >= v
     mul = (uint32_t)(((uint64_t)1 << 32) * (((uint64_t)1 << sh) - v) / v + 1);
@@ -45,18 +45,28 @@ struct RopeArgs {
   long long xr, xh, yr, yh;    // strides in elements
   int* status;
   float mscale;
-  int heads, R, begin, half, inverse;
+  int heads, R, begin, inverse;
   int rot_units, units;        // units of a (row, head): rotated ones first, then copied ones
   int rb, hb;                  // rows and heads of a tile
   FastDiv by_unit, by_head;
 };
 
+// Eight elements as raw 16-byte words: one for bf16, two for float.
 template <typename T>
-struct Unit {
-  float a[8], b[8];            // interleaved and copied units use a alone
+struct Raw {
+  uint4 w[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) reinterpret_cast<uint4*>(p)[i] = w[i];
+  }
+  __device__ __forceinline__ void floats(float* v) const { load8(reinterpret_cast<const T*>(w), v); }
 };
 
-// `kHalf`: pairs half a rotation apart.
+// kHalf: pairs half a rotation apart.
 template <typename T, bool kHalf>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs p) {
   __shared__ float2 s_cs[kMaxAngles];
@@ -67,37 +77,42 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs p) {
   const int nh = min(p.hb, p.heads - head0);
   const int n = nr * p.hb * p.units;
   const int half = p.R >> 1;
-  const T* x = reinterpret_cast<const T*>(p.x);
-  T* out = reinterpret_cast<T*>(p.out);
+  const T* x = reinterpret_cast<const T*>(p.x) + row0 * p.xr + (long long)head0 * p.xh;
+  T* out = reinterpret_cast<T*>(p.out) + (long long)head0 * p.yh;
 
-  auto place = [&](int i, int& r, int& h, int& u) {
-    const int q = (int)p.by_unit.div((uint32_t)i);
-    u = i - q * p.units;
-    r = (int)p.by_head.div((uint32_t)q);
-    h = q - r * p.hb;
-  };
-  // first dim of a unit: rotated units from `begin`, the others around the
-  // rotated part
-  auto dim_of = [&](int u) {
-    if (u < p.rot_units) return p.begin + 8 * u;
-    const int c = 8 * (u - p.rot_units);
-    return c < p.begin ? c : c + p.R;
-  };
-  bool angles = p.pos == nullptr;                 // formed after the first loads are in flight
-  for (int i0 = threadIdx.x; i0 - (int)threadIdx.x < n; i0 += kRopeThreads * kUnitsPerThread) {
-    Unit<T> v[kUnitsPerThread];
+  bool angles = p.pos == nullptr;                 // formed once the first loads are in flight
+  for (int base = 0; base < n; base += kRopeThreads * kUnitsPerThread) {
+    Raw<T> a[kUnitsPerThread], b[kHalf ? kUnitsPerThread : 1];
+    int where[kUnitsPerThread];                   // first angle of a rotated unit, -1: a copied one
+    T* dst[kUnitsPerThread];                      // null: nothing to do
 #pragma unroll
     for (int k = 0; k < kUnitsPerThread; ++k) {
-      const int i = i0 + k * kRopeThreads;
-      if (i < n) {
-        int r, h, u;
-        place(i, r, h, u);
-        if (h < nh) {
-          const T* src = x + (row0 + r) * p.xr + (long long)(head0 + h) * p.xh + dim_of(u);
-          load8(src, v[k].a);
-          if (kHalf && u < p.rot_units) load8(src + half, v[k].b);
+      const int i = base + k * kRopeThreads + (int)threadIdx.x;
+      dst[k] = nullptr;
+      if (i >= n) continue;
+      const int q = (int)p.by_unit.div((uint32_t)i);
+      const int u = i - q * p.units;
+      const int r = (int)p.by_head.div((uint32_t)q);
+      const int h = q - r * p.hb;
+      if (h >= nh) continue;
+      // rotated units from `begin`, the others around the rotated part
+      const bool rot = u < p.rot_units;
+      const int c = 8 * (u - p.rot_units);
+      const int dim = rot ? p.begin + 8 * u : (c < p.begin ? c : c + p.R);
+      where[k] = rot ? r * half + (kHalf ? 8 : 4) * u : -1;
+      const T* src = x + r * p.xr + (long long)h * p.xh + dim;
+      a[k].load(src);
+      if (kHalf && rot) b[kHalf ? k : 0].load(src + half);
+      long long row = row0 + r;
+      if (p.slot != nullptr) {
+        const int s = p.slot[row];
+        if (s < 0 || s >= p.n_slots) {
+          if (s != -1) set_status(p.status, kStatusBadIndex);
+          continue;
         }
+        row = s;
       }
+      dst[k] = out + row * p.yr + (long long)h * p.yh + dim;
     }
     if (!angles) {
       angles = true;
@@ -113,34 +128,25 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs p) {
     }
 #pragma unroll
     for (int k = 0; k < kUnitsPerThread; ++k) {
-      const int i = i0 + k * kRopeThreads;
-      if (i >= n) continue;
-      int r, h, u;
-      place(i, r, h, u);
-      if (h >= nh) continue;
-      long long row = row0 + r;
-      if (p.slot != nullptr) {
-        const int s = p.slot[row];
-        if (s < 0 || s >= p.n_slots) {
-          if (s != -1) set_status(p.status, kStatusBadIndex);
-          continue;
-        }
-        row = s;
-      }
-      T* dst = out + row * p.yr + (long long)(head0 + h) * p.yh + dim_of(u);
-      if (u < p.rot_units) {
+      if (dst[k] == nullptr) continue;
+      if (where[k] >= 0) {
+        const float2* cs = s_cs + where[k];
+        float v[8];
+        a[k].floats(v);
         if (kHalf) {
-          const float2* cs = s_cs + r * half + 8 * u;
+          float w[8];
+          b[kHalf ? k : 0].floats(w);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) rot_pair(v[k].a[e], v[k].b[e], cs[e].x, cs[e].y);
-          store8(dst + half, v[k].b);
+          for (int e = 0; e < 8; ++e) rot_pair(v[e], w[e], cs[e].x, cs[e].y);
+          store8(dst[k] + half, w);
         } else {
-          const float2* cs = s_cs + r * half + 4 * u;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) rot_pair(v[k].a[2 * e], v[k].a[2 * e + 1], cs[e].x, cs[e].y);
+          for (int e = 0; e < 4; ++e) rot_pair(v[2 * e], v[2 * e + 1], cs[e].x, cs[e].y);
         }
+        store8(dst[k], v);
+      } else {
+        a[k].store(dst[k]);
       }
-      store8(dst, v[k].a);
     }
   }
 }
@@ -166,18 +172,20 @@ cudaError_t launch_rope(const RopeCall& c, int* status, cudaStream_t st) {
   p.heads = c.heads;
   p.R = c.pos != nullptr ? c.rope_dim : 0;
   p.begin = c.rope_begin;
-  p.half = c.layout == V4_ROPE_HALF;
   p.inverse = c.inverse;
-  p.rot_units = p.R / (p.half ? 16 : 8);
+  const bool by_half = c.layout == V4_ROPE_HALF;
+  p.rot_units = p.R / (by_half ? 16 : 8);
   const bool in_place = c.x == c.out && c.slot == nullptr;
   p.units = p.rot_units + (in_place ? 0 : (c.dim - p.R) / 8);
   if (p.units == 0) return cudaSuccess;          // in place with nothing rotated
-  // Tile: about kUnitsPerThread units a thread, heads first (they share the
-  // row's angles), then rows as far as the angle table reaches.
-  const int want = kRopeThreads * kUnitsPerThread;
+  // Tile: up to kUnitsPerThread units a thread, heads first (they share the
+  // row's angles), then rows as far as the angle table reaches; fewer while
+  // the tiles would not give every SM one.
+  const long long all = c.rows * c.heads * p.units;
+  int want = kRopeThreads * kUnitsPerThread;
+  while (want > kRopeThreads && all / want < 304) want /= 2;
   const int per_row = c.heads * p.units;
   p.hb = per_row <= want ? c.heads : (want / p.units > 1 ? want / p.units : 1);
-  if (p.hb > c.heads) p.hb = c.heads;
   long long rb = p.hb == c.heads ? want / per_row : 1;
   const int half = p.R / 2;
   if (half > 0 && rb > kMaxAngles / half) rb = kMaxAngles / half;
@@ -187,13 +195,12 @@ cudaError_t launch_rope(const RopeCall& c, int* status, cudaStream_t st) {
   p.by_unit.set((uint32_t)p.units);
   p.by_head.set((uint32_t)p.hb);
   const long long gx = (c.rows + rb - 1) / rb;
-  if (gx > 0x7FFFFFFFll) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)gx, (unsigned)((c.heads + p.hb - 1) / p.hb));
   if (c.dtype == V4_BF16) {
-    if (p.half) rope_kernel<bf16, true><<<grid, kRopeThreads, 0, st>>>(p);
+    if (by_half) rope_kernel<bf16, true><<<grid, kRopeThreads, 0, st>>>(p);
     else rope_kernel<bf16, false><<<grid, kRopeThreads, 0, st>>>(p);
   } else {
-    if (p.half) rope_kernel<float, true><<<grid, kRopeThreads, 0, st>>>(p);
+    if (by_half) rope_kernel<float, true><<<grid, kRopeThreads, 0, st>>>(p);
     else rope_kernel<float, false><<<grid, kRopeThreads, 0, st>>>(p);
   }
   note_launch();

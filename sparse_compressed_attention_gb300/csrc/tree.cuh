@@ -120,7 +120,7 @@ __device__ __forceinline__ long long tree_token_row(const TreeArgs& a, const Tre
 }
 
 bool tree_tc_supported(const v4_config& c);
-size_t tree_tc_workspace(const v4_config& c, int n_rows);
+size_t tree_tc_workspace();
 cudaError_t launch_tree_tc(const TreeArgs& a, void* workspace, cudaStream_t st);
 
 }  // namespace v4

@@ -70,13 +70,13 @@ w4_pack_kernel(const bf16* __restrict__ w, int K, int N, int gs, uint32_t* __res
 // x.  A nibble pair becomes two bf16 with one mask-or (0x4300 | n is 128 + n)
 // and one exact subtraction of 136.
 //
-// A block takes `cta_rows` outputs; its eight warps split the inputs `ks`
-// ways (128-input blocks dealt round robin) and the outputs 8 / ks ways, and the
-// partial sums meet in shared memory.  With a norm, the blocks of a
-// norm_dim run form a cluster and exchange their sums of squares through
-// distributed shared memory.
+// A warp takes RT tiles of 16 outputs and a contiguous part of the inputs,
+// kDepth blocks of 128 inputs ahead in registers: the bytes in flight, not the
+// arithmetic, set the speed of few rows.  `ks` warps share an output's inputs
+// and meet in shared memory.  With a norm, a block takes 64 outputs and the
+// blocks of a norm_dim run form a cluster and exchange their sums of squares
+// through distributed shared memory.
 // ---------------------------------------------------------------------------
-constexpr int kW4Warps = 8, kW4Threads = kW4Warps * 32;
 constexpr int kMaxCluster = 8;
 
 struct W4Args {
@@ -106,28 +106,52 @@ __device__ __forceinline__ uint32_t w4_pair(uint32_t w) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// NT tiles of 8 rows of x, RT tiles of 16 outputs of a warp.
-template <int NT, int RT>
-__global__ void __launch_bounds__(kW4Threads) w4_kernel(const W4Args p) {
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int c) {
+  return c == 0 ? v.x : c == 1 ? v.y : c == 2 ? v.z : v.w;
+}
+
+// Scales of one output and one block of 128 inputs: 4 / kFold bf16 values.
+template <int kFold>
+struct ScaleWord;
+template <>
+struct ScaleWord<1> { typedef uint2 type; };
+template <>
+struct ScaleWord<2> { typedef uint32_t type; };
+template <>
+struct ScaleWord<4> { typedef uint16_t type; };
+
+__device__ __forceinline__ float scale_of(uint2 v, int i) {
+  const uint32_t w = i < 2 ? v.x : v.y;
+  return __uint_as_float((i & 1) ? (w & 0xFFFF0000u) : (w << 16));
+}
+__device__ __forceinline__ float scale_of(uint32_t w, int i) {
+  return __uint_as_float(i ? (w & 0xFFFF0000u) : (w << 16));
+}
+__device__ __forceinline__ float scale_of(uint16_t w, int) { return __uint_as_float((uint32_t)w << 16); }
+
+// NT tiles of 8 rows of x, RT tiles of 16 outputs of a warp, kFold chunks of 32
+// inputs in a scale group.
+template <int NT, int RT, int kDepth, int kFold>
+__global__ void __launch_bounds__(RT == 1 ? 512 : 256) w4_kernel(const W4Args p) {
   constexpr int kTok = NT * 8;
   extern __shared__ __align__(16) uint8_t smem[];
-  auto s_red = reinterpret_cast<float(*)[RT * 16][kTok]>(smem);    // [warp]: partial sums of one pass
-  auto s_out = reinterpret_cast<float(*)[kTok + 1]>(s_red + kW4Warps);         // [64]
-  auto s_sq = reinterpret_cast<float(*)[kTok]>(s_out + 64);        // [block of the cluster]: sums of squares
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, threads = blockDim.x;
+  auto s_red = reinterpret_cast<float(*)[kTok]>(smem);                         // [ks][cta_rows]: partial sums
+  auto s_sq = reinterpret_cast<float(*)[kTok]>(s_red + p.ks * p.cta_rows);     // [block of the cluster]
   const int gq = lane >> 2, t = lane & 3;
   const int g = blockIdx.y;
   const long long row0 = (long long)blockIdx.z * kTok;
   const int live = (int)min((long long)kTok, p.rows - row0);
   const int n0 = blockIdx.x * p.cta_rows;
-  const int kw = warp % p.ks, rw = warp / p.ks, nrw = kW4Warps / p.ks;
+  const int rw = warp / p.ks, kw = warp - rw * p.ks;
   const int nkb = p.K >> 7;
-  const int per_pass = nrw * RT * 16;
+  const int kb0 = (int)((long long)nkb * kw / p.ks), kb1 = (int)((long long)nkb * (kw + 1) / p.ks);
   const size_t kbytes = (size_t)p.K >> 1;
-  const int sgroups = p.K / p.gs;
-  const int fold = p.gs >> 5;                                        // chunks of a scale group: 1, 2 or 4
-  const uint8_t* cbase = p.codes + (size_t)g * p.N * kbytes + t * 16;
-  const bf16* sbase = p.scales + (size_t)g * p.N * sgroups;
+  typedef typename ScaleWord<kFold>::type Scales;
+  const int sgroups = nkb * (4 / kFold);
+  const int nw = rw * RT * 16;                                       // first output of this warp within the block
+  const uint8_t* cbase = p.codes + ((size_t)g * p.N + n0 + nw + gq) * kbytes + t * 16;
+  const bf16* sbase = p.scales + ((size_t)g * p.N + n0 + nw + gq) * sgroups;
   const bf16* xbase = p.x + ((size_t)row0 * p.groups + g) * p.K + 8 * t;
   const size_t xrow = (size_t)p.groups * p.K;
   const int peers = p.norm_dim > p.cta_rows ? p.norm_dim / p.cta_rows : 1;
@@ -135,102 +159,142 @@ __global__ void __launch_bounds__(kW4Threads) w4_kernel(const W4Args p) {
   // shared memory: arrive here, wait before the exchange
   if (peers > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 
-  for (int pass = 0; pass < p.cta_rows; pass += per_pass) {
-    const int nw = n0 + pass + rw * RT * 16;                        // first output of this warp
-    float acc[RT][NT][4];
+  // Everything a block of inputs needs is asked for ahead: codes and scales
+  // kDepth blocks, the rows of x a block (few rows) or a chunk ahead.  A load
+  // in the loop that is waited for at once costs its whole latency: with
+  // scales and x fetched where they are used, one row of 1024 x 32768 took
+  // 15.7 us.
+  uint4 lo[kDepth][RT], hi[kDepth][RT];
+  Scales slo[kDepth][RT], shi[kDepth][RT];
+  auto fetch = [&](int d, int kb) {
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
+    for (int i = 0; i < RT; ++i) {
+      const uint8_t* src = cbase + (size_t)(16 * i) * kbytes + (size_t)kb * 64;
+      lo[d][i] = __ldg(reinterpret_cast<const uint4*>(src));
+      hi[d][i] = __ldg(reinterpret_cast<const uint4*>(src + 8 * kbytes));
+      const bf16* sp = sbase + (size_t)(16 * i) * sgroups + kb * (4 / kFold);
+      slo[d][i] = __ldg(reinterpret_cast<const Scales*>(sp));
+      shi[d][i] = __ldg(reinterpret_cast<const Scales*>(sp + (size_t)8 * sgroups));
+    }
+  };
+  constexpr int kAhead = NT <= 2 ? 4 : 1;                            // chunks of x in flight
+  uint4 xb[kAhead][NT];
+  auto fetch_x = [&](int slot, int chunk) {                          // chunk: 4 kb + c
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+    for (int j = 0; j < NT; ++j) {
+      const int tok = 8 * j + gq;
+      xb[slot][j] = tok < live ? __ldg(reinterpret_cast<const uint4*>(xbase + tok * xrow + 32 * chunk))
+                               : make_uint4(0, 0, 0, 0);
+    }
+  };
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
-    for (int kb = kw; kb < nkb; kb += p.ks) {
-      uint4 lo[RT], hi[RT];
+  for (int d = 0; d < kDepth; ++d)
+    if (kb0 + d < kb1) fetch(d, kb0 + d);
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        const uint8_t* src = cbase + (size_t)(nw + 16 * i + gq) * kbytes + (size_t)kb * 64;
-        lo[i] = __ldg(reinterpret_cast<const uint4*>(src));
-        hi[i] = __ldg(reinterpret_cast<const uint4*>(src + 8 * kbytes));
-      }
-      float part[RT][NT][4];
+  for (int i = 0; i < kAhead; ++i) fetch_x(i, 4 * kb0 + i);
+  float acc[RT][NT][4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (c % fold == 0) {
+  for (int i = 0; i < RT; ++i)
 #pragma unroll
-          for (int i = 0; i < RT; ++i)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
+      for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
+  for (int base = kb0; base < kb1; base += kDepth) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) part[i][j][e] = 0.f;
-        }
-        uint4 b[NT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const int tok = 8 * j + gq;
-          b[j] = tok < live ? __ldg(reinterpret_cast<const uint4*>(xbase + tok * xrow + kb * 128 + 32 * c))
-                            : make_uint4(0, 0, 0, 0);
-        }
+    for (int d = 0; d < kDepth; ++d) {
+      const int kb = base + d;
+      if (kb < kb1) {
+        uint4 cl[RT], ch[RT];
+        Scales sl[RT], sh[RT];
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
-          const uint32_t wl = c == 0 ? lo[i].x : c == 1 ? lo[i].y : c == 2 ? lo[i].z : lo[i].w;
-          const uint32_t wh = c == 0 ? hi[i].x : c == 1 ? hi[i].y : c == 2 ? hi[i].z : hi[i].w;
-          const uint32_t a0[4] = {w4_pair(wl), w4_pair(wh), w4_pair(wl >> 4), w4_pair(wh >> 4)};
-          const uint32_t a1[4] = {w4_pair(wl >> 8), w4_pair(wh >> 8), w4_pair(wl >> 12), w4_pair(wh >> 12)};
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            mma_bf16(part[i][j], a0, b[j].x, b[j].y);
-            mma_bf16(part[i][j], a1, b[j].z, b[j].w);
-          }
+          cl[i] = lo[d][i];
+          ch[i] = hi[d][i];
+          sl[i] = slo[d][i];
+          sh[i] = shi[d][i];
         }
-        if ((c + 1) % fold == 0) {
+        if (kb + kDepth < kb1) fetch(d, kb + kDepth);
+        // few rows: two sums a scale group (first and second halves of the
+        // words), two shorter chains of products
+        constexpr int kParts = NT > 2 ? 1 : 2;
+        float part[kParts][RT][NT][4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint4 b[NT];
+#pragma unroll
+          for (int j = 0; j < NT; ++j) b[j] = xb[c % kAhead][j];
+          if (4 * kb + c + kAhead < 4 * kb1) fetch_x(c % kAhead, 4 * kb + c + kAhead);
+          if (c % kFold == 0) {
+#pragma unroll
+            for (int h = 0; h < kParts; ++h)
+#pragma unroll
+              for (int i = 0; i < RT; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) part[h][i][j][e] = 0.f;
+          }
 #pragma unroll
           for (int i = 0; i < RT; ++i) {
-            const bf16* sp = sbase + (size_t)(nw + 16 * i + gq) * sgroups + (kb * 128 + 32 * c) / p.gs;
-            const float s0 = to_f(sp[0]), s1 = to_f(sp[(size_t)8 * sgroups]);
+            const uint32_t wl = word_of(cl[i], c), wh = word_of(ch[i], c);
+            const uint32_t a0[4] = {w4_pair(wl), w4_pair(wh), w4_pair(wl >> 4), w4_pair(wh >> 4)};
+            const uint32_t a1[4] = {w4_pair(wl >> 8), w4_pair(wh >> 8), w4_pair(wl >> 12), w4_pair(wh >> 12)};
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-              acc[i][j][0] = fmaf(part[i][j][0], s0, acc[i][j][0]);
-              acc[i][j][1] = fmaf(part[i][j][1], s0, acc[i][j][1]);
-              acc[i][j][2] = fmaf(part[i][j][2], s1, acc[i][j][2]);
-              acc[i][j][3] = fmaf(part[i][j][3], s1, acc[i][j][3]);
+              mma_bf16(part[0][i][j], a0, b[j].x, b[j].y);
+              mma_bf16(part[kParts - 1][i][j], a1, b[j].z, b[j].w);
+            }
+          }
+          if ((c + 1) % kFold == 0) {
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+              const float s0 = scale_of(sl[i], c / kFold), s1 = scale_of(sh[i], c / kFold);
+#pragma unroll
+              for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float v = kParts == 1 ? part[0][i][j][e] : part[0][i][j][e] + part[kParts - 1][i][j][e];
+                  acc[i][j][e] = fmaf(v, e < 2 ? s0 : s1, acc[i][j][e]);
+                }
             }
           }
         }
       }
     }
-    __syncthreads();                                                // the previous pass's sums are read
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        *reinterpret_cast<float2*>(&s_red[warp][16 * i + gq][8 * j + 2 * t]) = make_float2(acc[i][j][0], acc[i][j][1]);
-        *reinterpret_cast<float2*>(&s_red[warp][16 * i + gq + 8][8 * j + 2 * t]) =
-            make_float2(acc[i][j][2], acc[i][j][3]);
-      }
-    __syncthreads();
-    for (int o = threadIdx.x; o < per_pass * kTok; o += kW4Threads) {
-      const int tok = o % kTok, r = o / kTok;                        // r: output of the pass
-      const int w0 = (r / (RT * 16)) * p.ks, rr = r % (RT * 16);
-      float v = 0.f;
-      for (int k = 0; k < p.ks; ++k) v += s_red[w0 + k][rr][tok];
-      s_out[pass + r][tok] = v;
-    }
   }
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      float* at = s_red[kw * p.cta_rows + nw + 16 * i + gq] + 8 * j + 2 * t;
+      *reinterpret_cast<float2*>(at) = make_float2(acc[i][j][0], acc[i][j][1]);
+      *reinterpret_cast<float2*>(at + 8 * kTok) = make_float2(acc[i][j][2], acc[i][j][3]);
+    }
   __syncthreads();
+  if (p.ks > 1) {
+    float* red = &s_red[0][0];
+    const int n = p.cta_rows * kTok;
+    for (int o = threadIdx.x; o < n; o += threads) {
+      float v = red[o];
+      for (int k = 1; k < p.ks; ++k) v += red[k * n + o];
+      red[o] = v;
+    }
+    __syncthreads();
+  }
   if (p.norm_dim > 0) {
     uint32_t rank = 0;
     if (peers > 1) {
       asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
       asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
-    // a warp for each row of x: this block's sum of squares
-    for (int tok = warp; tok < kTok; tok += kW4Warps) {
+    // a warp for each row of x: this block's sum of squares, to every block
+    for (int tok = warp; tok < live; tok += threads / 32) {
       float q = 0.f;
-      for (int r = lane; r < p.cta_rows; r += 32) q = fmaf(s_out[r][tok], s_out[r][tok], q);
+      for (int r = lane; r < p.cta_rows; r += 32) q = fmaf(s_red[r][tok], s_red[r][tok], q);
       for (int o = 16; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
       if (lane < peers) {
-        const uint32_t here = (uint32_t)__cvta_generic_to_shared(&s_sq[rank][tok]);
         if (peers > 1) {
+          const uint32_t here = (uint32_t)__cvta_generic_to_shared(&s_sq[rank][tok]);
           uint32_t there;
           asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(here), "r"(lane));
           asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there), "f"(q) : "memory");
@@ -245,42 +309,42 @@ __global__ void __launch_bounds__(kW4Threads) w4_kernel(const W4Args p) {
     } else {
       __syncthreads();
     }
-    for (int o = threadIdx.x; o < p.cta_rows * live; o += kW4Threads) {
-      const int r = o % p.cta_rows, tok = o / p.cta_rows;
+  }
+  for (int o = threadIdx.x; o < p.cta_rows * live; o += threads) {
+    const int r = o % p.cta_rows, tok = o / p.cta_rows;
+    float v = s_red[r][tok];
+    if (p.norm_dim > 0) {
       float q = 0.f;
       for (int k = 0; k < peers; ++k) q += s_sq[k][tok];
-      const float inv = 1.0f / sqrtf(q / (float)p.norm_dim + p.eps);
-      const float w = p.norm_w ? p.norm_w[(n0 + r) % p.norm_dim] : 1.f;
-      p.y[((size_t)(row0 + tok) * p.groups + g) * p.N + n0 + r] = __float2bfloat16_rn(s_out[r][tok] * inv * w);
+      v *= 1.0f / sqrtf(q / (float)p.norm_dim + p.eps);
+      if (p.norm_w) v *= p.norm_w[(n0 + r) % p.norm_dim];
     }
-    return;
-  }
-  for (int o = threadIdx.x; o < p.cta_rows * live; o += kW4Threads) {
-    const int r = o % p.cta_rows, tok = o / p.cta_rows;
-    p.y[((size_t)(row0 + tok) * p.groups + g) * p.N + n0 + r] = __float2bfloat16_rn(s_out[r][tok]);
+    p.y[((size_t)(row0 + tok) * p.groups + g) * p.N + n0 + r] = __float2bfloat16_rn(v);
   }
 }
 
-template <int NT, int RT>
-cudaError_t w4_launch(W4Args p, cudaStream_t st) {
-  const int nkb = p.K / 128;
-  // inputs split as many ways as divide their blocks evenly, at most eight
-  p.ks = nkb % 8 == 0 ? 8 : nkb % 4 == 0 ? 4 : nkb % 2 == 0 ? 2 : 1;
-  if (nkb > 16 && p.ks < 8) p.ks = 8;                               // long rows: an uneven eight-way split
-  while (kW4Warps / p.ks * RT * 16 > 64) p.ks *= 2;
-  const int per_pass = kW4Warps / p.ks * RT * 16;
-  // a norm's blocks take 64 outputs (eight blocks cover 512); without one, the
-  // most outputs a block that still give two blocks an SM
-  p.cta_rows = 64;
-  if (p.norm_dim == 0)
-    while (p.cta_rows > per_pass && (long long)p.N / p.cta_rows * p.groups < 304) p.cta_rows /= 2;
-  constexpr size_t smem = (size_t)(kW4Warps * RT * 16 * NT * 8 + 64 * (NT * 8 + 1) + kMaxCluster * NT * 8) * 4;
-  cudaError_t e = cudaFuncSetAttribute(w4_kernel<NT, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+template <int NT, int RT, int kDepth, int kFold>
+cudaError_t w4_launch_fold(W4Args p, cudaStream_t st) {
+  constexpr int kMaxSmem = 16 * 16 * NT * 8 * 4 * RT + kMaxCluster * NT * 8 * 4;
+  static OncePerDevice once;
+  cudaError_t e = once.run([&] {
+    return cudaFuncSetAttribute(w4_kernel<NT, RT, kDepth, kFold>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  });
   if (e != cudaSuccess) return e;
+  const int nkb = p.K / 128;
+  const long long tiles = (long long)p.N / (16 * RT) * p.groups;      // warps without a split of the inputs
+  // split the inputs until about twelve warps an SM stream codes
+  p.ks = 1;
+  while (p.ks < 4 && tiles * p.ks < 1824 && nkb >= 4 * p.ks) p.ks *= 2;
+  // a norm's blocks take 64 outputs (eight blocks cover 512); without one a
+  // block is four warps
+  const int rt = p.norm_dim > 0 ? 4 / RT : (p.ks < 4 ? 4 / p.ks : 1);
+  p.cta_rows = 16 * RT * rt;
+  while (p.N % p.cta_rows) p.cta_rows /= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = (size_t)p.ks * p.cta_rows * NT * 8 * 4 + kMaxCluster * NT * 8 * 4;
   cfg.gridDim = dim3(p.N / p.cta_rows, p.groups, (unsigned)((p.rows + NT * 8 - 1) / (NT * 8)));
-  cfg.blockDim = dim3(kW4Threads);
+  cfg.blockDim = dim3(32 * p.ks * (p.cta_rows / (16 * RT)));
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   if (p.norm_dim > p.cta_rows) {
@@ -291,10 +355,17 @@ cudaError_t w4_launch(W4Args p, cudaStream_t st) {
     cfg.attrs = at;
     cfg.numAttrs = 1;
   }
-  e = cudaLaunchKernelEx(&cfg, w4_kernel<NT, RT>, (const W4Args)p);
+  e = cudaLaunchKernelEx(&cfg, w4_kernel<NT, RT, kDepth, kFold>, (const W4Args)p);
   if (e != cudaSuccess) return e;
   note_launch();
   return cudaGetLastError();
+}
+
+template <int NT, int RT, int kDepth>
+cudaError_t w4_launch(const W4Args& p, cudaStream_t st) {
+  if (p.gs == 32) return w4_launch_fold<NT, RT, kDepth, 1>(p, st);
+  if (p.gs == 64) return w4_launch_fold<NT, RT, kDepth, 2>(p, st);
+  return w4_launch_fold<NT, RT, kDepth, 4>(p, st);
 }
 
 }  // namespace
@@ -324,10 +395,10 @@ cudaError_t launch_w4_proj(const void* x, long long rows, int groups, int K, int
   p.norm_dim = norm_dim;
   p.eps = eps;
   p.ks = p.cta_rows = 0;
-  if (rows <= 8) return w4_launch<1, 4>(p, st);
-  if (rows <= 16) return w4_launch<2, 2>(p, st);
-  if (rows <= 32) return w4_launch<4, 2>(p, st);
-  return w4_launch<8, 1>(p, st);
+  if (rows <= 8) return w4_launch<1, 1, 4>(p, st);
+  if (rows <= 16) return w4_launch<2, 1, 4>(p, st);
+  if (rows <= 32) return w4_launch<4, 2, 2>(p, st);
+  return w4_launch<8, 2, 2>(p, st);
 }
 
 }  // namespace v4
