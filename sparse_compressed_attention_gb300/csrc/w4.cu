@@ -70,14 +70,33 @@ w4_pack_kernel(const bf16* __restrict__ w, int K, int N, int gs, uint32_t* __res
 // x.  A nibble pair becomes two bf16 with one mask-or (0x4300 | n is 128 + n)
 // and one exact subtraction of 136.
 //
-// A warp takes RT tiles of 16 outputs and a contiguous part of the inputs,
-// kDepth blocks of 128 inputs ahead in registers: the bytes in flight, not the
-// arithmetic, set the speed of few rows.  `ks` warps share an output's inputs
-// and meet in shared memory.  With a norm, a block takes 64 outputs and the
-// blocks of a norm_dim run form a cluster and exchange their sums of squares
-// through distributed shared memory.
+// Up to eight rows of x (w4_few_kernel): bound by how fast codes arrive and
+// are unpacked.  A warp takes 16 outputs and a contiguous part of the inputs and
+// keeps kDepth blocks of 128 inputs in flight through a ring in shared
+// memory, where every lane reads back exactly the bytes that it asked for
+// (cp.async: no registers wait for them, no barrier).  Scales and x are asked
+// for a block ahead: a load waited for where it is used costs its whole
+// latency (15.7 us for one row of 1024 x 32768 with scales and x fetched in the
+// loop body).  After that the instructions count (306 a warp and block in the
+// first streaming version, 96 of them unpacking and products: 9.5 us), so
+// pointers are incremented, rows of x beyond the last read the last one (their
+// columns are never stored), and a scale group's first product starts from
+// zero by itself.
+//
+// More rows (w4_rows_kernel): there the rows of x, read again for every 16
+// outputs, are the larger traffic (24 rows: eight times the codes; 18 us for
+// 8 x 4096 x 1024 with the kernel above).  Eight warps share each 128-input
+// block of x through a ring of stages in shared memory, one block barrier a
+// stage; rows lie 256 bytes apart with the halves of odd rows exchanged, so
+// that a fragment read touches every bank once.
+//
+// `ks` warps share an output's inputs and meet in shared memory.  With a norm,
+// the blocks of a norm_dim run form a cluster and exchange their sums of
+// squares through distributed shared memory.
 // ---------------------------------------------------------------------------
 constexpr int kMaxCluster = 8;
+constexpr int kDepth = 4;                    // blocks in flight (a power of two; eight measured 0.5 us slower: less L1)
+constexpr uint32_t kStageBytes = 1024;       // codes of 16 outputs x 128 inputs
 
 struct W4Args {
   const bf16* x;
@@ -86,7 +105,7 @@ struct W4Args {
   const float* norm_w;
   bf16* y;
   long long rows;
-  int groups, K, N, gs, norm_dim, ks, cta_rows;
+  int groups, K, N, gs, norm_dim, log_ks, log_rows;      // warps an output's inputs are split over, outputs of a block
   float eps;
 };
 
@@ -96,6 +115,14 @@ __device__ __forceinline__ void mma_bf16(float* d, const uint32_t* a, uint32_t b
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The same product from zero.
+__device__ __forceinline__ void mma_bf16_first(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // Nibbles p and p + 4 of a word as bf16 values n - 8.
@@ -129,243 +156,385 @@ __device__ __forceinline__ float scale_of(uint32_t w, int i) {
 }
 __device__ __forceinline__ float scale_of(uint16_t w, int) { return __uint_as_float((uint32_t)w << 16); }
 
-// NT tiles of 8 rows of x, RT tiles of 16 outputs of a warp, kFold chunks of 32
-// inputs in a scale group.
-template <int NT, int RT, int kDepth, int kFold>
-__global__ void __launch_bounds__(RT == 1 ? 512 : 256) w4_kernel(const W4Args p) {
-  constexpr int kTok = NT * 8;
-  extern __shared__ __align__(16) uint8_t smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, threads = blockDim.x;
-  auto s_red = reinterpret_cast<float(*)[kTok]>(smem);                         // [ks][cta_rows]: partial sums
-  auto s_sq = reinterpret_cast<float(*)[kTok]>(s_red + p.ks * p.cta_rows);     // [block of the cluster]
-  const int gq = lane >> 2, t = lane & 3;
-  const int g = blockIdx.y;
-  const long long row0 = (long long)blockIdx.z * kTok;
-  const int live = (int)min((long long)kTok, p.rows - row0);
-  const int n0 = blockIdx.x * p.cta_rows;
-  const int rw = warp / p.ks, kw = warp - rw * p.ks;
-  const int nkb = p.K >> 7;
-  const int kb0 = (int)((long long)nkb * kw / p.ks), kb1 = (int)((long long)nkb * (kw + 1) / p.ks);
-  const size_t kbytes = (size_t)p.K >> 1;
-  typedef typename ScaleWord<kFold>::type Scales;
-  const int sgroups = nkb * (4 / kFold);
-  const int nw = rw * RT * 16;                                       // first output of this warp within the block
-  const uint8_t* cbase = p.codes + ((size_t)g * p.N + n0 + nw + gq) * kbytes + t * 16;
-  const bf16* sbase = p.scales + ((size_t)g * p.N + n0 + nw + gq) * sgroups;
-  const bf16* xbase = p.x + ((size_t)row0 * p.groups + g) * p.K + 8 * t;
-  const size_t xrow = (size_t)p.groups * p.K;
-  const int peers = p.norm_dim > p.cta_rows ? p.norm_dim / p.cta_rows : 1;
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
+// What a warp's part of the work is.
+struct W4Part {
+  int warp, lane, gq, t, ks, rw, kw, cta_rows, g, live, n0, peers;
+  long long row0;
+};
+
+__device__ __forceinline__ W4Part w4_part(const W4Args& p, int tokens) {
+  W4Part q;
+  q.warp = threadIdx.x >> 5;
+  q.lane = threadIdx.x & 31;
+  q.gq = q.lane >> 2;
+  q.t = q.lane & 3;
+  q.ks = 1 << p.log_ks;
+  q.cta_rows = 1 << p.log_rows;
+  q.rw = q.warp >> p.log_ks;
+  q.kw = q.warp & (q.ks - 1);
+  q.g = blockIdx.y;
+  q.row0 = (long long)blockIdx.z * tokens;
+  q.live = (int)min((long long)tokens, p.rows - q.row0);
+  q.n0 = blockIdx.x << p.log_rows;
+  q.peers = p.norm_dim > q.cta_rows ? p.norm_dim >> p.log_rows : 1;
   // the cluster's blocks have all started before one writes to another's
   // shared memory: arrive here, wait before the exchange
-  if (peers > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  if (q.peers > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  return q;
+}
 
-  // Everything a block of inputs needs is asked for ahead: codes and scales
-  // kDepth blocks, the rows of x a block (few rows) or a chunk ahead.  A load
-  // in the loop that is waited for at once costs its whole latency: with
-  // scales and x fetched where they are used, one row of 1024 x 32768 took
-  // 15.7 us.
-  uint4 lo[kDepth][RT], hi[kDepth][RT];
-  Scales slo[kDepth][RT], shi[kDepth][RT];
-  auto fetch = [&](int d, int kb) {
+// Partial sums of every warp -> outputs.  `smem` (all of it free) takes
+// [ks][tokens][cta_rows + 4] sums and the cluster's sums of squares behind them:
+// outputs run along the rows, so that sums are stored without bank conflicts
+// (the pitch is 4 modulo 16 words) and leave in 16-byte words.
+template <int NT>
+__device__ __forceinline__ void w4_finish(const W4Args& p, const W4Part& q, float (&acc)[NT][4], uint8_t* smem) {
+  constexpr int kTok = NT * 8;
+  const int threads = blockDim.x, pitch = q.cta_rows + 4, part = kTok * pitch;
+  float* red = reinterpret_cast<float*>(smem);
+  auto s_sq = reinterpret_cast<float(*)[kTok]>(red + q.ks * part);
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const uint8_t* src = cbase + (size_t)(16 * i) * kbytes + (size_t)kb * 64;
-      lo[d][i] = __ldg(reinterpret_cast<const uint4*>(src));
-      hi[d][i] = __ldg(reinterpret_cast<const uint4*>(src + 8 * kbytes));
-      const bf16* sp = sbase + (size_t)(16 * i) * sgroups + kb * (4 / kFold);
-      slo[d][i] = __ldg(reinterpret_cast<const Scales*>(sp));
-      shi[d][i] = __ldg(reinterpret_cast<const Scales*>(sp + (size_t)8 * sgroups));
-    }
-  };
-  constexpr int kAhead = NT <= 2 ? 4 : 1;                            // chunks of x in flight
-  uint4 xb[kAhead][NT];
-  auto fetch_x = [&](int slot, int chunk) {                          // chunk: 4 kb + c
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int tok = 8 * j + gq;
-      xb[slot][j] = tok < live ? __ldg(reinterpret_cast<const uint4*>(xbase + tok * xrow + 32 * chunk))
-                               : make_uint4(0, 0, 0, 0);
-    }
-  };
-#pragma unroll
-  for (int d = 0; d < kDepth; ++d)
-    if (kb0 + d < kb1) fetch(d, kb0 + d);
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) fetch_x(i, 4 * kb0 + i);
-  float acc[RT][NT][4];
-#pragma unroll
-  for (int i = 0; i < RT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
-  for (int base = kb0; base < kb1; base += kDepth) {
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d) {
-      const int kb = base + d;
-      if (kb < kb1) {
-        uint4 cl[RT], ch[RT];
-        Scales sl[RT], sh[RT];
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          cl[i] = lo[d][i];
-          ch[i] = hi[d][i];
-          sl[i] = slo[d][i];
-          sh[i] = shi[d][i];
-        }
-        if (kb + kDepth < kb1) fetch(d, kb + kDepth);
-        // few rows: two sums a scale group (first and second halves of the
-        // words), two shorter chains of products
-        constexpr int kParts = NT > 2 ? 1 : 2;
-        float part[kParts][RT][NT][4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint4 b[NT];
-#pragma unroll
-          for (int j = 0; j < NT; ++j) b[j] = xb[c % kAhead][j];
-          if (4 * kb + c + kAhead < 4 * kb1) fetch_x(c % kAhead, 4 * kb + c + kAhead);
-          if (c % kFold == 0) {
-#pragma unroll
-            for (int h = 0; h < kParts; ++h)
-#pragma unroll
-              for (int i = 0; i < RT; ++i)
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) part[h][i][j][e] = 0.f;
-          }
-#pragma unroll
-          for (int i = 0; i < RT; ++i) {
-            const uint32_t wl = word_of(cl[i], c), wh = word_of(ch[i], c);
-            const uint32_t a0[4] = {w4_pair(wl), w4_pair(wh), w4_pair(wl >> 4), w4_pair(wh >> 4)};
-            const uint32_t a1[4] = {w4_pair(wl >> 8), w4_pair(wh >> 8), w4_pair(wl >> 12), w4_pair(wh >> 12)};
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              mma_bf16(part[0][i][j], a0, b[j].x, b[j].y);
-              mma_bf16(part[kParts - 1][i][j], a1, b[j].z, b[j].w);
-            }
-          }
-          if ((c + 1) % kFold == 0) {
-#pragma unroll
-            for (int i = 0; i < RT; ++i) {
-              const float s0 = scale_of(sl[i], c / kFold), s1 = scale_of(sh[i], c / kFold);
-#pragma unroll
-              for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const float v = kParts == 1 ? part[0][i][j][e] : part[0][i][j][e] + part[kParts - 1][i][j][e];
-                  acc[i][j][e] = fmaf(v, e < 2 ? s0 : s1, acc[i][j][e]);
-                }
-            }
-          }
-        }
-      }
-    }
+  for (int j = 0; j < NT; ++j) {
+    float* at = red + q.kw * part + (8 * j + 2 * q.t) * pitch + q.rw * 16 + q.gq;
+    at[0] = acc[j][0];
+    at[pitch] = acc[j][1];
+    at[8] = acc[j][2];
+    at[pitch + 8] = acc[j][3];
   }
-#pragma unroll
-  for (int i = 0; i < RT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      float* at = s_red[kw * p.cta_rows + nw + 16 * i + gq] + 8 * j + 2 * t;
-      *reinterpret_cast<float2*>(at) = make_float2(acc[i][j][0], acc[i][j][1]);
-      *reinterpret_cast<float2*>(at + 8 * kTok) = make_float2(acc[i][j][2], acc[i][j][3]);
-    }
   __syncthreads();
-  if (p.ks > 1) {
-    float* red = &s_red[0][0];
-    const int n = p.cta_rows * kTok;
-    for (int o = threadIdx.x; o < n; o += threads) {
-      float v = red[o];
-      for (int k = 1; k < p.ks; ++k) v += red[k * n + o];
-      red[o] = v;
-    }
-    __syncthreads();
-  }
   if (p.norm_dim > 0) {
     uint32_t rank = 0;
-    if (peers > 1) {
+    if (q.peers > 1) {
       asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
       asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
-    // a warp for each row of x: this block's sum of squares, to every block
-    for (int tok = warp; tok < live; tok += threads / 32) {
-      float q = 0.f;
-      for (int r = lane; r < p.cta_rows; r += 32) q = fmaf(s_red[r][tok], s_red[r][tok], q);
-      for (int o = 16; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
-      if (lane < peers) {
-        if (peers > 1) {
+    // a warp for each row of x: its sums joined, and their squares to every block
+    for (int tok = q.warp; tok < q.live; tok += threads / 32) {
+      float s = 0.f;
+      for (int r = q.lane; r < q.cta_rows; r += 32) {
+        float v = red[tok * pitch + r];
+        for (int k = 1; k < q.ks; ++k) v += red[k * part + tok * pitch + r];
+        red[tok * pitch + r] = v;
+        s = fmaf(v, v, s);
+      }
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (q.lane < q.peers) {
+        if (q.peers > 1) {
           const uint32_t here = (uint32_t)__cvta_generic_to_shared(&s_sq[rank][tok]);
           uint32_t there;
-          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(here), "r"(lane));
-          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there), "f"(q) : "memory");
+          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(here), "r"(q.lane));
+          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there), "f"(s) : "memory");
         } else {
-          s_sq[0][tok] = q;
+          s_sq[0][tok] = s;
         }
       }
     }
-    if (peers > 1) {
+    if (q.peers > 1) {
       asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
       asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     } else {
       __syncthreads();
     }
   }
-  for (int o = threadIdx.x; o < p.cta_rows * live; o += threads) {
-    const int r = o % p.cta_rows, tok = o / p.cta_rows;
-    float v = s_red[r][tok];
-    if (p.norm_dim > 0) {
-      float q = 0.f;
-      for (int k = 0; k < peers; ++k) q += s_sq[k][tok];
-      v *= 1.0f / sqrtf(q / (float)p.norm_dim + p.eps);
-      if (p.norm_w) v *= p.norm_w[(n0 + r) % p.norm_dim];
+  const int log8 = p.log_rows - 3, joined = p.norm_dim > 0 ? 1 : q.ks;
+  for (int o = threadIdx.x; o < q.live << log8; o += threads) {
+    const int r = (o & ((1 << log8) - 1)) * 8, tok = o >> log8;
+    float v[8];
+    load8(red + tok * pitch + r, v);
+    for (int k = 1; k < joined; ++k) {
+      float w[8];
+      load8(red + k * part + tok * pitch + r, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += w[e];
     }
-    p.y[((size_t)(row0 + tok) * p.groups + g) * p.N + n0 + r] = __float2bfloat16_rn(v);
+    if (p.norm_dim > 0) {
+      float s = 0.f;
+      for (int k = 0; k < q.peers; ++k) s += s_sq[k][tok];
+      const float inv = 1.0f / sqrtf(s / (float)p.norm_dim + p.eps);
+      const float* w = p.norm_w ? p.norm_w + ((q.n0 + r) & (p.norm_dim - 1)) : nullptr;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= w ? inv * w[e] : inv;
+    }
+    store8(p.y + ((size_t)(q.row0 + tok) * p.groups + q.g) * p.N + q.n0 + r, v);
   }
 }
 
-template <int NT, int RT, int kDepth, int kFold>
-cudaError_t w4_launch_fold(W4Args p, cudaStream_t st) {
-  constexpr int kMaxSmem = 16 * 16 * NT * 8 * 4 * RT + kMaxCluster * NT * 8 * 4;
-  static OncePerDevice once;
-  cudaError_t e = once.run([&] {
-    return cudaFuncSetAttribute(w4_kernel<NT, RT, kDepth, kFold>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-  });
+// Products of one chunk of 32 inputs: words wl, wh of outputs g and g + 8, x
+// of NT tiles.  kParts sums a scale group (shorter chains of products).
+template <int NT, int kParts>
+__device__ __forceinline__ void w4_chunk(float (&part)[kParts][NT][4], uint32_t wl, uint32_t wh, const uint4* x,
+                                         bool first) {
+  const uint32_t a0[4] = {w4_pair(wl), w4_pair(wh), w4_pair(wl >> 4), w4_pair(wh >> 4)};
+  const uint32_t a1[4] = {w4_pair(wl >> 8), w4_pair(wh >> 8), w4_pair(wl >> 12), w4_pair(wh >> 12)};
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    if (first) mma_bf16_first(part[0][j], a0, x[j].x, x[j].y);
+    else mma_bf16(part[0][j], a0, x[j].x, x[j].y);
+    if (kParts == 2 && first) mma_bf16_first(part[kParts - 1][j], a1, x[j].z, x[j].w);
+    else mma_bf16(part[kParts - 1][j], a1, x[j].z, x[j].w);
+  }
+}
+
+template <int NT, int kParts>
+__device__ __forceinline__ void w4_fold(float (&acc)[NT][4], const float (&part)[kParts][NT][4], float s0, float s1) {
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float v = kParts == 1 ? part[0][j][e] : part[0][j][e] + part[kParts - 1][j][e];
+      acc[j][e] = fmaf(v, e < 2 ? s0 : s1, acc[j][e]);
+    }
+}
+
+// Up to eight rows.  kFold chunks of 32 inputs in a scale group.
+template <int kFold>
+__global__ void __launch_bounds__(512) w4_few_kernel(const W4Args p) {
+  typedef typename ScaleWord<kFold>::type Scales;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const W4Part q = w4_part(p, 8);
+  const int nkb = p.K >> 7;
+  const int kb0 = (nkb * q.kw) >> p.log_ks, kb1 = (nkb * (q.kw + 1)) >> p.log_ks;
+  const size_t out0 = (size_t)q.g * p.N + q.n0 + q.rw * 16 + q.gq;
+  const size_t kbytes = (size_t)p.K >> 1;
+  const uint8_t* cp0 = p.codes + out0 * kbytes + (size_t)kb0 * 64 + q.t * 16;
+  const uint8_t* cp1 = cp0 + 8 * kbytes;
+  const Scales* sp0 = reinterpret_cast<const Scales*>(p.scales) + out0 * nkb + kb0;
+  const Scales* sp1 = sp0 + (size_t)8 * nkb;
+  const uint4* xp = reinterpret_cast<const uint4*>(
+      p.x + ((size_t)(q.row0 + min(q.gq, q.live - 1)) * p.groups + q.g) * p.K + (size_t)kb0 * 128 + 8 * q.t);
+  float acc[1][4] = {{0.f, 0.f, 0.f, 0.f}};
+  // this lane's 16 bytes of outputs g and g + 8 in each stage
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + q.warp * (kDepth * kStageBytes) + q.lane * 16;
+  int left = kb1 - kb0;
+  auto ask = [&](uint32_t at) {
+    cp_async_16(at, cp0);
+    cp_async_16(at + 512, cp1);
+    cp0 += 64;
+    cp1 += 64;
+  };
+#pragma unroll
+  for (int d = 0; d < kDepth; ++d) {
+    if (d < left) ask(ring + d * kStageBytes);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  Scales s0n = __ldg(sp0), s1n = __ldg(sp1);
+  uint4 xb[4], xc[4];                          // 32 inputs are four 16-byte words
+#pragma unroll
+  for (int i = 0; i < 4; ++i) xb[i] = __ldg(xp + 4 * i);
+  uint32_t stage = ring;
+  // one block of 128 inputs; `now` holds its x, `then` takes the next block's
+  auto block = [&](uint4 (&now)[4], uint4 (&then)[4]) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+    const uint4 lo = lds128(stage), hi = lds128(stage + 512);
+    if (left > kDepth) ask(stage);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    stage = ring + ((stage + kStageBytes - ring) & (kDepth * kStageBytes - 1));
+    const Scales slo = s0n, shi = s1n;
+    xp += 16;
+    if (left > 1) {
+      s0n = __ldg(++sp0);
+      s1n = __ldg(++sp1);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) then[c] = __ldg(xp + 4 * c);
+    }
+    float part[2][1][4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      w4_chunk<1, 2>(part, word_of(lo, c), word_of(hi, c), &now[c], c % kFold == 0);
+      if ((c + 1) % kFold == 0) w4_fold<1, 2>(acc, part, scale_of(slo, c / kFold), scale_of(shi, c / kFold));
+    }
+    --left;
+  };
+#pragma unroll 1
+  while (left > 1) {
+    block(xb, xc);
+    block(xc, xb);
+  }
+  if (left > 0) block(xb, xc);
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();                              // every ring is read: partial sums take its place
+  w4_finish<1>(p, q, acc, smem);
+}
+
+constexpr int kRowWarps = 8;
+
+__host__ __device__ __forceinline__ uint32_t w4_stage_bytes(int ks, int tok) {
+  return (uint32_t)(ks * tok * 256) + kRowWarps * kStageBytes;
+}
+
+// More than eight rows: NT tiles of 8 at a time.
+template <int NT, int kFold, int kStages>
+__global__ void __launch_bounds__(kRowWarps * 32, 2) w4_rows_kernel(const W4Args p) {
+  constexpr int kTok = NT * 8;
+  typedef typename ScaleWord<kFold>::type Scales;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const W4Part q = w4_part(p, kTok);
+  const int nkb = p.K >> 7;
+  // blocks of 128 inputs of this warp's part of the inputs; every part takes
+  // `steps` steps of the shared ring
+  const int steps = (nkb + q.ks - 1) >> p.log_ks;
+  const int kb0 = q.kw * steps, mine = min(steps, nkb - kb0);
+  const size_t out0 = (size_t)q.g * p.N + q.n0 + q.rw * 16 + q.gq;
+  const size_t kbytes = (size_t)p.K >> 1;
+  const uint8_t* cp0 = p.codes + out0 * kbytes + (size_t)kb0 * 64 + q.t * 16;
+  const uint8_t* cp1 = cp0 + 8 * kbytes;
+  const Scales* sp0 = reinterpret_cast<const Scales*>(p.scales) + out0 * nkb + kb0;
+  const Scales* sp1 = sp0 + (size_t)8 * nkb;
+  const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem), stage_bytes = w4_stage_bytes(q.ks, kTok);
+  const uint32_t xt = q.kw * kTok * 256;                             // this part's x within a stage
+  const uint32_t ct = q.ks * kTok * 256 + q.warp * kStageBytes + q.lane * 16;
+  // x: the part's warps copy 16-byte units, unit u of a row at u ^ 4 in odd rows
+  const int filler = q.rw * 32 + q.lane, fillers = (kRowWarps * 32) >> p.log_ks;
+  const int fu = filler & 15, ft = filler >> 4;
+  const bf16* x0 = p.x + ((size_t)q.row0 * p.groups + q.g) * p.K + (size_t)kb0 * 128 + fu * 8;
+  const size_t xrow = (size_t)p.groups * p.K;
+  const uint32_t xdst = xt + ft * 256 + ((fu ^ ((ft & 1) << 2)) << 4);      // rows step by an even number
+  auto ask = [&](int step) {
+    if (step < mine) {
+      const uint32_t at = base + (step % kStages) * stage_bytes;
+      cp_async_16(at + ct, cp0 + (size_t)step * 64);
+      cp_async_16(at + ct + 512, cp1 + (size_t)step * 64);
+      for (int tok = ft; tok < kTok; tok += fillers >> 4)
+        cp_async_16(at + xdst + (tok - ft) * 256, x0 + min(tok, q.live - 1) * xrow + step * 128);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  float acc[NT][4];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+  for (int i = 0; i < kStages - 1; ++i) ask(i);
+  Scales s0n = {}, s1n = {};
+  if (mine > 0) {
+    s0n = __ldg(sp0);
+    s1n = __ldg(sp1);
+  }
+#pragma unroll 1
+  for (int i = 0; i < steps; ++i) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    __syncthreads();                            // step i has landed, step i - 1 is read
+    ask(i + kStages - 1);
+    if (i >= mine) continue;
+    const uint32_t at = base + (i % kStages) * stage_bytes;
+    const uint4 lo = lds128(at + ct), hi = lds128(at + ct + 512);
+    const Scales slo = s0n, shi = s1n;
+    if (i + 1 < mine) {
+      s0n = __ldg(sp0 + i + 1);
+      s1n = __ldg(sp1 + i + 1);
+    }
+    float part[1][NT][4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint4 x[NT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        x[j] = lds128(at + xt + (8 * j + q.gq) * 256 + ((c ^ (q.gq & 1)) << 6) + (q.t << 4));
+      w4_chunk<NT, 1>(part, word_of(lo, c), word_of(hi, c), x, c % kFold == 0);
+      if ((c + 1) % kFold == 0) w4_fold<NT, 1>(acc, part, scale_of(slo, c / kFold), scale_of(shi, c / kFold));
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+  w4_finish<NT>(p, q, acc, smem);
+}
+
+// Largest of the ring and what w4_finish puts in its place.
+size_t w4_smem(size_t ring, int ks, int cta_rows, int tok) {
+  const size_t fin = (size_t)(ks * (cta_rows + 4) + kMaxCluster) * tok * 4;
+  return ring > fin ? ring : fin;
+}
+
+template <typename Kernel>
+cudaError_t w4_go(Kernel kern, OncePerDevice& once, size_t most, size_t smem, int tok, int threads, W4Args p, int ks,
+                  int cta_rows, cudaStream_t st) {
+  cudaError_t e =
+      once.run([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most); });
   if (e != cudaSuccess) return e;
-  const int nkb = p.K / 128;
-  const long long tiles = (long long)p.N / (16 * RT) * p.groups;      // warps without a split of the inputs
-  // split the inputs until about twelve warps an SM stream codes
-  p.ks = 1;
-  while (p.ks < 4 && tiles * p.ks < 1824 && nkb >= 4 * p.ks) p.ks *= 2;
-  // a norm's blocks take 64 outputs (eight blocks cover 512); without one a
-  // block is four warps
-  const int rt = p.norm_dim > 0 ? 4 / RT : (p.ks < 4 ? 4 / p.ks : 1);
-  p.cta_rows = 16 * RT * rt;
-  while (p.N % p.cta_rows) p.cta_rows /= 2;
+  p.log_ks = ks == 1 ? 0 : ks == 2 ? 1 : 2;
+  p.log_rows = cta_rows == 128 ? 7 : cta_rows == 64 ? 6 : cta_rows == 32 ? 5 : 4;
   cudaLaunchConfig_t cfg = {};
-  cfg.dynamicSmemBytes = (size_t)p.ks * p.cta_rows * NT * 8 * 4 + kMaxCluster * NT * 8 * 4;
-  cfg.gridDim = dim3(p.N / p.cta_rows, p.groups, (unsigned)((p.rows + NT * 8 - 1) / (NT * 8)));
-  cfg.blockDim = dim3(32 * p.ks * (p.cta_rows / (16 * RT)));
+  cfg.dynamicSmemBytes = smem;
+  cfg.gridDim = dim3(p.N / cta_rows, p.groups, (unsigned)((p.rows + tok - 1) / tok));
+  cfg.blockDim = dim3(threads);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
-  if (p.norm_dim > p.cta_rows) {
+  if (p.norm_dim > cta_rows) {
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = p.norm_dim / p.cta_rows;
+    at[0].val.clusterDim.x = p.norm_dim / cta_rows;
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
   }
-  e = cudaLaunchKernelEx(&cfg, w4_kernel<NT, RT, kDepth, kFold>, (const W4Args)p);
+  e = cudaLaunchKernelEx(&cfg, kern, (const W4Args)p);
   if (e != cudaSuccess) return e;
   note_launch();
   return cudaGetLastError();
 }
 
-template <int NT, int RT, int kDepth>
-cudaError_t w4_launch(const W4Args& p, cudaStream_t st) {
-  if (p.gs == 32) return w4_launch_fold<NT, RT, kDepth, 1>(p, st);
-  if (p.gs == 64) return w4_launch_fold<NT, RT, kDepth, 2>(p, st);
-  return w4_launch_fold<NT, RT, kDepth, 4>(p, st);
+template <int kFold>
+cudaError_t w4_few(const W4Args& p, cudaStream_t st) {
+  static OncePerDevice once;
+  const int nkb = p.K / 128;
+  const long long tiles = (long long)p.N / 16 * p.groups;             // warps without a split of the inputs
+  // split the inputs until about twelve warps an SM stream codes, each with a
+  // few blocks to itself
+  int ks = 1;
+  while (ks < 4 && tiles * ks < 1824 && nkb >= 4 * ks) ks *= 2;
+  // a norm's blocks take 64 outputs (eight blocks cover 512); without one a
+  // block is four warps
+  const int cta_rows = 16 * (p.norm_dim > 0 ? 4 : (ks < 4 ? 4 / ks : 1));
+  const int warps = ks * (cta_rows / 16);
+  constexpr size_t most = 16 * kDepth * kStageBytes + kMaxCluster * 8 * 4;
+  return w4_go(w4_few_kernel<kFold>, once, most, w4_smem((size_t)warps * kDepth * kStageBytes, ks, cta_rows, 8), 8,
+               32 * warps, p, ks, cta_rows, st);
+}
+
+template <int NT, int kFold, int kStages>
+cudaError_t w4_rows_go(const W4Args& p, int ks, int cta_rows, cudaStream_t st) {
+  static OncePerDevice once;
+  constexpr int kTok = NT * 8;
+  constexpr size_t most = 116 * 1024;                                 // two blocks an SM
+  const size_t smem = w4_smem((size_t)kStages * w4_stage_bytes(ks, kTok), ks, cta_rows, kTok);
+  return w4_go(w4_rows_kernel<NT, kFold, kStages>, once, most, smem, kTok, kRowWarps * 32, p, ks, cta_rows, st);
+}
+
+template <int NT, int kFold>
+cudaError_t w4_rows(const W4Args& p, cudaStream_t st) {
+  const int nkb = p.K / 128;
+  // A block takes 128 outputs; fewer, with the inputs split, while there are
+  // not two blocks for each SM (or N is an odd number of 64): two warps on a
+  // scheduler leave it idle two cycles of three (8 x 4096 x 1024, 24 rows:
+  // 29.4 / 16.6 us unsplit and split in two).  The norm needs 64 outputs a block
+  // and 64 rows of x the room of two stages.
+  int ks = p.N % 128 ? 2 : 1;
+  const int most = p.norm_dim > 0 || NT == 8 ? 2 : 4;
+  while (ks < most && (long long)p.N / 128 * ks * p.groups < 228 && nkb >= 4 * ks) ks *= 2;
+  if (p.norm_dim == 64) ks = 2;
+  const int cta_rows = 128 / ks;
+  // as many stages as leave room for a second block
+  if (ks * NT >= 16) return w4_rows_go<NT, kFold, 2>(p, ks, cta_rows, st);
+  if (ks * NT >= 8) return w4_rows_go<NT, kFold, 3>(p, ks, cta_rows, st);
+  return w4_rows_go<NT, kFold, 4>(p, ks, cta_rows, st);
+}
+
+template <int kFold>
+cudaError_t w4_by_rows(const W4Args& p, cudaStream_t st) {
+  if (p.rows <= 8) return w4_few<kFold>(p, st);
+  if (p.rows <= 16) return w4_rows<2, kFold>(p, st);
+  if (p.rows <= 32) return w4_rows<4, kFold>(p, st);
+  return w4_rows<8, kFold>(p, st);
 }
 
 }  // namespace
@@ -394,11 +563,10 @@ cudaError_t launch_w4_proj(const void* x, long long rows, int groups, int K, int
   p.gs = gs;
   p.norm_dim = norm_dim;
   p.eps = eps;
-  p.ks = p.cta_rows = 0;
-  if (rows <= 8) return w4_launch<1, 1, 4>(p, st);
-  if (rows <= 16) return w4_launch<2, 1, 4>(p, st);
-  if (rows <= 32) return w4_launch<4, 2, 2>(p, st);
-  return w4_launch<8, 2, 2>(p, st);
+  p.log_ks = p.log_rows = 0;
+  if (gs == 32) return w4_by_rows<1>(p, st);
+  if (gs == 64) return w4_by_rows<2>(p, st);
+  return w4_by_rows<4>(p, st);
 }
 
 }  // namespace v4
