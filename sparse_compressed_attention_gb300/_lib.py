@@ -378,9 +378,11 @@ def _current(t, name):
 
 def _shaped(t, name, shape, dtype, dev):
     """Pointer of a dense tensor of exactly this shape on device `dev` (the current one)."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev \
-            and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _ptr(t, name, dtype)
     if t.get_device() != dev:
         raise ValueError("%s is on %s, the current device is cuda:%d" % (name, t.device, dev))
@@ -485,41 +487,55 @@ def alloc_tree_workspace(cfg, n_rows, device=None):
     return torch.empty(max(v4_tree_workspace_size(cfg, n_rows), 256), dtype=torch.uint8, device=device or "cuda")
 
 
-def _paged(inputs, kind, used, D, B, dt, dev):
+def _paged(cache, table, kind, D, B, dt, dev):
     """Cache pointer, table pointer, slots, blocks, page size of one paged cache."""
-    if not used:
-        return None, None, 0, 0, 0
-    cache, table = inputs.get(kind + "_cache"), inputs.get(kind + "_table")
+    try:
+        pages, page, width = cache.shape
+        blocks = table.shape[1]
+        if width == D and cache.dtype is dt and cache.get_device() == dev and cache.is_contiguous():
+            return (cache.data_ptr(), _shaped(table, kind + "_table", (B, blocks), torch.int32, dev), pages * page, blocks,
+                    page)
+    except (AttributeError, ValueError, IndexError):
+        pass
     if not isinstance(cache, torch.Tensor) or cache.dim() != 3 or cache.shape[2] != D:
         raise ValueError("%s_cache must be a tensor [pages, page_size, %d]" % (kind, D))
+    _shaped(cache, kind + "_cache", cache.shape, dt, dev)
     if not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise ValueError("%s_table must be a tensor [batch, blocks]" % kind)
-    shape, blocks = cache.shape, table.shape[1]
-    return (_shaped(cache, kind + "_cache", shape, dt, dev),
-            _shaped(table, kind + "_table", (B, blocks), torch.int32, dev), shape[0] * shape[1], blocks, shape[1])
+    _shaped(table, kind + "_table", (B, table.shape[1]), torch.int32, dev)
+    raise ValueError("%s_cache and %s_table cannot be used" % (kind, kind))
 
 
 def v4_tree_mqa_fwd(cfg, inputs, o, lse, workspace, stream=None):
     """Attention of planned rows over paged caches.  inputs: a dict keyed like v4_tree_inputs' pointers, with
     tok_cache / ent_cache [pages, page_size, D] and tok_table / ent_table [B, blocks]."""
-    dt, i32, f32 = _storage(cfg), torch.int32, torch.float32
-    q, sink, half = inputs["q"], inputs.get("sink"), cfg.rope_dim // 2
+    i32, f32 = torch.int32, torch.float32
+    get = inputs.get
+    q, sink = inputs["q"], get("sink")
     dev = _current(q, "q")
-    n, H, D, B, r, K = q.shape[0], cfg.n_heads, cfg.head_dim, cfg.batch, cfg.ratio, cfg.topk
-    tc, tt, ts, tb, tp = _paged(inputs, "tok", cfg.window != 0, D, B, dt, dev)
-    ec, et, es, eb, ep = _paged(inputs, "ent", r > 0, D, B, dt, dev)
+    H, D, B, r, K, half, dt = cfg.n_heads, cfg.head_dim, cfg.batch, cfg.ratio, cfg.topk, cfg.rope_dim // 2, _storage(cfg)
+    n = q.shape[0]
     shape = (n, H, D)
+    tc = tt = ec = et = el = ix = None
+    ts = tb = tp = es = eb = ep = 0
+    if cfg.window:
+        tc, tt, ts, tb, tp = _paged(get("tok_cache"), get("tok_table"), "tok", D, B, dt, dev)
+    if r > 0:
+        ec, et, es, eb, ep = _paged(get("ent_cache"), get("ent_table"), "ent", D, B, dt, dev)
+        el = _shaped(get("ent_len"), "ent_len", (B,), i32, dev)
+        if K > 0:
+            ix = _shaped(get("idx"), "idx", (n, K), i32, dev)
     vin = v4_tree_inputs(
-        _shaped(q, "q", shape, dt, dev), _shaped(inputs["plan"], "plan", (n, 8), i32, dev), tc, tt, ec, et,
-        _shaped(inputs.get("ent_len"), "ent_len", (B,), i32, dev) if r > 0 else None,
-        _shaped(inputs.get("idx"), "idx", (n, K), i32, dev) if K > 0 else None,
+        _shaped(q, "q", shape, dt, dev), _shaped(inputs["plan"], "plan", (n, 8), i32, dev), tc, tt, ec, et, el, ix,
         None if sink is None else _shaped(sink, "sink", (H,), f32, dev),
-        _shaped(inputs.get("inv_freq"), "inv_freq", (half,), f32, dev) if half else None,
-        ts, es, n, tb, tp, eb, ep)
-    _check(lib().v4_tree_mqa_fwd(C.byref(cfg), C.byref(vin), _shaped(o, "o", shape, dt, dev),
-                                 None if lse is None else _shaped(lse, "lse", (n, H), f32, dev),
-                                 _shaped(workspace, "workspace", workspace.shape, torch.uint8, dev), workspace.numel(),
-                                 _stream_on(stream, dev)))
+        _shaped(get("inv_freq"), "inv_freq", (half,), f32, dev) if half else None, ts, es, n, tb, tp, eb, ep)
+    size = workspace.numel()
+    st = lib().v4_tree_mqa_fwd(cfg, vin, _shaped(o, "o", shape, dt, dev),
+                               None if lse is None else _shaped(lse, "lse", (n, H), f32, dev),
+                               _shaped(workspace, "workspace", (size,), torch.uint8, dev), size,
+                               _stream_on(stream, dev))
+    if st:
+        _check(st)
     return o
 
 

@@ -51,6 +51,7 @@ constexpr int kSoftWarps = kSoftThreads / 32;
 constexpr int kGatherWarps = 4;                   // 32 key rows each
 constexpr int kTile = 128;
 constexpr int kSlots = 8;                         // K-blocks of 64 dims: one tile
+constexpr int kPairs = kSlots / 2;
 constexpr uint32_t kSlotBytes = kTile * 128;
 constexpr uint32_t kQBlockBytes = kH * 128;
 constexpr uint32_t kPBytes = kTile * kH * 2;
@@ -64,15 +65,17 @@ constexpr uint32_t OFF_P = OFF_SLOT + kSlots * kSlotBytes;        // 204800
 constexpr uint32_t OFF_CTL = OFF_P + kPBytes;                     // 221184
 
 // A block's piece of an item.
-struct Piece {
-  int row, hs, tile0, tiles, done;
+struct alignas(16) Piece {               // two 16-byte words: it is copied through shared memory
+  int row, hs, tile0, tiles;
+  int done;
   int dense;                             // leading tiles that arrive as whole page runs (TMA)
   int part;                              // workspace part of a cut item, -1: the item is whole
+  int seq;
 };
 
 struct Ctl {
-  uint64_t full_g[kSlots], full_t[kSlots];   // gathered / page-run K-blocks landed
-  uint64_t empty[kSlots / 2];                // pairs of K-blocks released (one M-block of O)
+  // K-blocks go in pairs, as an M-block of O releases them
+  uint64_t full_g[kPairs], full_t[kPairs], empty[kPairs];   // gathered / page-run pair landed, pair released
   uint64_t valid_full[2];
   uint64_t q_full, q_ready, q_empty;
   uint64_t s_full[2], p_ready[2];
@@ -133,7 +136,11 @@ __device__ __forceinline__ int nth_node(const int4 w, int i) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int n = __popc(m[k]);
-    if (i < n) return 32 * k + (int)__fns(m[k], 0, i + 1);
+    if (i < n) {
+      uint32_t b = m[k];
+      for (; i > 0; --i) b &= b - 1;
+      return 32 * k + __ffs(b) - 1;
+    }
     i -= n;
   }
   return -1;
@@ -245,10 +252,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     return;
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kSlots; ++i) {
+    for (int i = 0; i < kPairs; ++i) {
       mbar_init(&c->full_g[i], 32 * kGatherWarps);
       mbar_init(&c->full_t[i], 1);
-      if (i < kSlots / 2) mbar_init(&c->empty[i], 1);
+      mbar_init(&c->empty[i], 1);
     }
     mbar_init(&c->q_full, 1);
     mbar_init(&c->q_ready, kSoftWarps);
@@ -324,8 +331,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     bool ok = true;
     int2 cut = make_int2(-1, -1);                // the item that begins here and ends in a later block
     auto next_piece = [&]() -> Piece {
-      Piece pc;
-      pc.done = 1;
+      Piece pc = {0, 0, 0, 0, 1, 0, -1, 0};
       while (item < p.items && unit < s1) {
         int dense = 0;
         const int n = tree_tiles(p, item / p.HS, &dense);
@@ -340,6 +346,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
           pc.dense = min(max(dense - pc.tile0, 0), pc.tiles);
           // a share that begins behind tile 0 leaves its part in the block's
           // first place, one that begins with it in the second
+          pc.seq = a.plan[(size_t)pc.row * kPlanWords];
           pc.part = pc.tiles == n ? -1 : 2 * (int)blockIdx.x + (lo > base ? 0 : 1);
           if (pc.part >= 0 && lo == base) cut = make_int2(item, (base + n - 1) / share);
         }
@@ -377,9 +384,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
       if (lane < 8)
         tma_load_2d(smem + OFF_Q + lane * kQBlockBytes, &map_q, 64 * lane, pc.row * a.H + kH * pc.hs, &c->q_full);
       // the next piece is described while this one's tiles load
-      const int seq = a.plan[(size_t)pc.row * kPlanWords];
-      Piece nxt;
-      nxt.done = 1;
+      Piece nxt = {0, 0, 0, 0, 1, 0, -1, 0};
       if (pc.dense == 0) {
         nxt = next_piece();
         publish(nxt, qc + 1);
@@ -391,7 +396,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         if (box < boxes) {
           const long long at = (long long)(pc.tile0 + j) * kTile + box * p.box;
           const long long blk = at / page;
-          const int pg = blk < blocks ? table[(size_t)seq * blocks + blk] : -1;
+          const int pg = blk < blocks ? table[(size_t)pc.seq * blocks + blk] : -1;
           const long long r = (long long)pg * page + (at - blk * page);
           if (pg >= 0 && r < slots) y = (int)r;
         }
@@ -399,9 +404,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
           const int kb = 2 * m + odd;
           if (g >= 1) ok = mbar_wait(&c->empty[m], (g - 1) & 1, &c->abort, a.status);
           if (!ok) break;
-          if (box == 0) mbar_expect_tx(&c->full_t[kb], kSlotBytes);
+          if (lane == 0) mbar_expect_tx(&c->full_t[m], 2 * kSlotBytes);
           if (box < boxes)
-            tma_load_2d(smem + OFF_SLOT + kb * kSlotBytes + box * p.box * 128, &map_pages, 64 * kb, y, &c->full_t[kb]);
+            tma_load_2d(smem + OFF_SLOT + kb * kSlotBytes + box * p.box * 128, &map_pages, 64 * kb, y, &c->full_t[m]);
         }
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -414,7 +419,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
       // gathered tiles: their slot releases are awaited too, a parity wait being
       // unambiguous one phase ahead only
       for (int j = pc.dense; j < pc.tiles && ok; ++j) {
-        for (int m = 0; m < kSlots / 2 && ok; ++m)
+        for (int m = 0; m < kPairs && ok; ++m)
           if (g >= 1) ok = warp_wait(&c->empty[m], (g - 1) & 1, c, a.status);
         ++g;
       }
@@ -454,8 +459,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
           const uint32_t par = (dense ? gt : gg) & 1;
 #pragma unroll
           for (int kb = 0; kb < kSlots; kb += 2) {
-            ok = ok && mbar_wait(&full[kb], par, &c->abort, a.status) &&
-                 mbar_wait(&full[kb + 1], par, &c->abort, a.status);
+            ok = ok && mbar_wait(&full[kb / 2], par, &c->abort, a.status);
             if (!dense) fence_proxy_async_smem();     // cp.async writes -> tensor-core reads
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
@@ -531,19 +535,21 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         for (int i = 0; i < 8; ++i)
           rows[i] = reinterpret_cast<const bf16*>(
               __shfl_sync(0xffffffffu, (unsigned long long)src, 4 * i + (lane >> 3)));
-        for (int kb = 0; kb < kSlots; ++kb) {
-          if (g >= 1 && !(kb & 1)) ok = warp_wait(&c->empty[kb / 2], (g - 1) & 1, c, a.status);
+        for (int m = 0; m < kPairs; ++m) {
+          if (g >= 1) ok = warp_wait(&c->empty[m], (g - 1) & 1, c, a.status);
           if (!ok) break;
           if (j < pc.dense) continue;               // arrives as page runs
-          const uint32_t d0 = smem_u32(smem + OFF_SLOT + kb * kSlotBytes);
+          const uint32_t d0 = smem_u32(smem + OFF_SLOT + 2 * m * kSlotBytes);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int row = 32 * gw + 4 * i + (lane >> 3);
             const bool key = rows[i] != nullptr;
-            const bf16* from = key ? rows[i] + kb * 64 + chunk * 8 : reinterpret_cast<const bf16*>(a.q);
-            cp_async_16_or_zero(d0 + row * 128 + ((chunk ^ (row & 7)) << 4), from, key);
+            const bf16* from = key ? rows[i] + m * 128 + chunk * 8 : reinterpret_cast<const bf16*>(a.q);
+            const uint32_t to = d0 + row * 128 + ((chunk ^ (row & 7)) << 4);
+            cp_async_16_or_zero(to, from, key);
+            cp_async_16_or_zero(to + kSlotBytes, from + (key ? 64 : 0), key);
           }
-          cp_async_mbar_arrive(&c->full_g[kb]);
+          cp_async_mbar_arrive(&c->full_g[m]);
         }
         ask(j + 1);
         ++g;
@@ -747,7 +753,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
       }
       warp_wait(&c->o_full, par, c, a.status);
       tc_fence_after();
-      bf16* obase = reinterpret_cast<bf16*>(a.o) + (orow + h0) * kD + krow;
+      bf16* opair = reinterpret_cast<bf16*>(a.o) + (orow + h0 + (lane & 1)) * kD + (krow & ~1);
       for (int m = 0; m < 4; ++m) {
         float v[32];
         tmem_ld32(tmem + lane_base + 128 + 64 * m + h0, v);
@@ -772,8 +778,16 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             v[i] = odd ? v[i] * cs.x - other * cs.y : v[i] * cs.x + other * cs.y;
           }
         }
+        // two heads at a time: lanes of a pair of dims exchange, the even one
+        // stores both dims of the first head, the odd one of the second (half
+        // the stores, and packed conversions)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) obase[(size_t)i * kD + 128 * m] = __float2bfloat16_rn(v[i]);
+        for (int i = 0; i < 32; i += 2) {
+          const uint32_t own = pack_bf16x2(v[i], v[i + 1]);
+          const uint32_t oth = __shfl_xor_sync(0xffffffffu, own, 1);
+          *reinterpret_cast<uint32_t*>(opair + (size_t)i * kD + 128 * m) =
+              (lane & 1) ? __byte_perm(oth, own, 0x7632) : __byte_perm(own, oth, 0x5410);
+        }
       }
       named_bar_sync(1, kSoftThreads);            // this piece's shifts and factors are read
       ++qc;
