@@ -436,6 +436,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
       const uint64_t dQ = smem_desc(smem_u32(smem + OFF_Q), 16, 1024, kLayoutSW128);
       const uint64_t dA2 = smem_desc(smem_u32(smem + OFF_SLOT), kSlotBytes, 1024, kLayoutSW128);
       const uint64_t dP = smem_desc(smem_u32(smem + OFF_P), 128, 2048, kLayoutNone);
+      const uint32_t hA1 = (uint32_t)(dA1 >> 32), hQ = (uint32_t)(dQ >> 32), hA2 = (uint32_t)(dA2 >> 32),
+                     hP = (uint32_t)(dP >> 32);
+      const auto desc = [](uint32_t hi, uint32_t lo) { return ((uint64_t)hi << 32) | lo; };
       int qc = 0, g = 0, gg = 0, gt = 0;            // all tiles, gathered ones, page runs
       bool ok = true;
       while (ok) {
@@ -450,6 +453,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         for (int j = 0; j < pc.tiles && ok; ++j) {
           const int sb = g & 1;
           const uint32_t s_tmem = tmem + 64 * sb;
+          // descriptors are affine in the start address (low word); opaque copies
+          // keep the sums of base and offset out of registers that would hold
+          // them across tiles (and be spilled)
+          uint32_t a1 = (uint32_t)dA1, q1 = (uint32_t)dQ, a2 = (uint32_t)dA2, p2 = (uint32_t)dP;
+          asm volatile("" : "+r"(a1), "+r"(q1), "+r"(a2), "+r"(p2));
           // K-blocks as they land, two at a time (the O products release them in
           // pairs); TMA writes need no proxy fence.  Products are unrolled with
           // constant descriptor offsets: in rolled loops 32 O products took
@@ -463,15 +471,15 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             if (!dense) fence_proxy_async_smem();     // cp.async writes -> tensor-core reads
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
-              umma_f16_ss(s_tmem, dA1 + (uint64_t)(((kb + ks / 4) * kSlotBytes + 32 * (ks & 3)) >> 4),
-                          dQ + (uint64_t)(((kb + ks / 4) * kQBlockBytes + 32 * (ks & 3)) >> 4), id1, (kb | ks) != 0);
+              umma_f16_ss(s_tmem, desc(hA1, a1 + (((kb + ks / 4) * kSlotBytes + 32 * (ks & 3)) >> 4)),
+                          desc(hQ, q1 + (((kb + ks / 4) * kQBlockBytes + 32 * (ks & 3)) >> 4)), id1, (kb | ks) != 0);
           }
           if (dense) ++gt; else ++gg;
           // the rotated dims once more, against q's low part
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            umma_f16_ss(s_tmem, dA1 + (uint64_t)((7 * kSlotBytes + 32 * ks) >> 4),
-                        dQ + (uint64_t)((8 * kQBlockBytes + 32 * ks) >> 4), id1, 1u);
+            umma_f16_ss(s_tmem, desc(hA1, a1 + ((7 * kSlotBytes + 32 * ks) >> 4)),
+                        desc(hQ, q1 + ((8 * kQBlockBytes + 32 * ks) >> 4)), id1, 1u);
           umma_commit(&c->s_full[sb]);
           if (j == pc.tiles - 1) umma_commit(&c->q_empty);
           if (!ok) break;
@@ -482,8 +490,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
           for (int m = 0; m < 4; ++m) {
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
-              umma_f16_ss(tmem + 128 + 64 * m, dA2 + (uint64_t)((2 * m * kSlotBytes + 2048 * ks) >> 4),
-                          dP + (uint64_t)((256 * ks) >> 4), id2, (j > 0 || ks > 0) ? 1u : 0u);
+              umma_f16_ss(tmem + 128 + 64 * m, desc(hA2, a2 + ((2 * m * kSlotBytes + 2048 * ks) >> 4)),
+                          desc(hP, p2 + ((256 * ks) >> 4)), id2, (j > 0 || ks > 0) ? 1u : 0u);
             umma_commit(&c->empty[m]);
           }
           ++g;
