@@ -115,7 +115,7 @@ struct Args {
   int dense_tok;                         // the runs are token pages (else entry pages)
   int ask;                               // next tile's rows are asked into L2
   char* parts;
-  int2* cuts;                            // per block: the item cut at its end (or -1) and that item's last block
+  int4* cuts;                            // per block: the item that goes on behind its end (or -1), that item's first and last block
 };
 
 // Tiles of a row's key list; *dense: how many leading ones are whole page runs.
@@ -307,7 +307,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
   const int share = share_of(total, gridDim.x);
   const int s0 = min(blockIdx.x * share, total), s1 = min(s0 + share, total);
   if (s0 >= s1) {                                // nothing for this block
-    if (threadIdx.x == 0) p.cuts[blockIdx.x] = make_int2(-1, -1);
+    if (threadIdx.x == 0) p.cuts[blockIdx.x] = make_int4(-1, -1, -1, 0);
     return;
   }
   if (before <= s0 && s0 < before + mine) {
@@ -336,7 +336,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     // ------------------------------------------------------------ shares and query rows
     int item = c->start_item, unit = c->start_unit, qc = 0, g = 0;
     bool ok = true;
-    int2 cut = make_int2(-1, -1);                // the item that begins here and ends in a later block
+    int4 cut = make_int4(-1, -1, -1, 0);         // the item that goes on in the next block
     auto next_piece = [&]() -> Piece {
       Piece pc = {0, 0, 0, 0, 1, 0, -1, 0};
       while (item < p.items && unit < s1) {
@@ -355,7 +355,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
           // first place, one that begins with it in the second
           pc.seq = a.plan[(size_t)pc.row * kPlanWords];
           pc.part = pc.tiles == n ? -1 : 2 * (int)blockIdx.x + (lo > base ? 0 : 1);
-          if (pc.part >= 0 && lo == base) cut = make_int2(item, (base + n - 1) / share);
+          if (base + n > s1) cut = make_int4(item, base / share, (base + n - 1) / share, 0);
         }
         unit += n ? n + 1 : 0;
         ++item;
@@ -829,75 +829,128 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
 }
 
 // ---------------------------------------------------------------------------
-// Join of cut items, each found under the block that holds its tile 0: block
-// (that block, eight heads), a warp for each head with 16 dims a lane.
-// sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s over the item's parts.
+// Join of cut items: sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s over an item's
+// parts.  An item in few parts is taken by the thread blocks (its first block,
+// eight heads), a warp for each head with 16 dims a lane.  One in more than
+// kJoinSerial parts has as many blocks behind its first that own nothing else:
+// the first eight of them take one head each, a warp every eighth part, and add
+// up in shared memory: one row over 131072 tokens, 152 parts, takes 62 us in both
+// kernels, 100 with a block for eight heads of any item; 16 ragged rows over all
+// their tokens 92 against 95.  Eight parts is where the two ways cross (four: 94).
 // Launched while the attention kernel drains (programmatic dependence) and
 // waits for its end before it reads anything.
 // ---------------------------------------------------------------------------
-constexpr int kJoinHeads = 8;
+constexpr int kJoinHeads = 8, kJoinSerial = 8;
 
 __global__ void __launch_bounds__(kJoinHeads * 32) tree_join_kernel(const Args p) {
+  __shared__ float4 s_o[kJoinHeads][kD / 4];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const TreeArgs& a = p.t;
-  const int first = blockIdx.x;
-  const int2 found = p.cuts[first];
-  if (found.x < 0) return;
-  const int item = found.x, last = found.y, row = item / p.HS, hs = item % p.HS;
-  const int h = blockIdx.y * kJoinHeads + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int4 cut = p.cuts[blockIdx.x];
+  const int item = cut.x, first = cut.y, last = cut.z, which = blockIdx.x - first;
+  if (item < 0) return;
+  const bool serial = last - first < kJoinSerial;
+  if (which >= (serial ? 1 : kJoinHeads)) return;
+  const int row = item / p.HS, hs = item % p.HS;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = a.plan[(size_t)row * kPlanWords + 2];
   // the first block holds the item from tile 0 (its second place), the others
   // begin inside it (their first place)
   auto place = [&](int cta) { return p.parts + (size_t)(2 * cta + (cta == first ? 1 : 0)) * kPartBytes; };
-  float m = -INFINITY;
-  for (int s = first; s <= last; ++s)
-    m = fmaxf(m, reinterpret_cast<const PartHead*>(place(s) + kPartFloats * 4)->m[h]);
-  float l = 0.f;
-  if (a.sink != nullptr) {
-    const float s2 = a.sink[kH * hs + h] * kLog2e;
-    m = fmaxf(m, s2);
-    if (s2 > -INFINITY) l = ex2_approx(s2 - m);
-  }
-  float o[16];
+  auto head = [&](int cta) { return reinterpret_cast<const PartHead*>(place(cta) + kPartFloats * 4); };
+  // one pair of dims, divided by l: the rotated ones turned back
+  auto finish = [&](float x0, float x1, int dim) {
+    if (dim >= kD - kR) {
+      float cs, sn;
+      turn_cos_sin(t, turn_fraction(a.inv_freq[(dim - (kD - kR)) / 2]), &cs, &sn);
+      rot_pair(x0, x1, cs, -sn);
+    }
+    return pack_bf16x2(x0, x1);
+  };
+  if (serial) {
+    const int h = blockIdx.y * kJoinHeads + warp;
+    const size_t orow = (size_t)row * a.H + kH * hs + h;
+    const float s2 = a.sink != nullptr ? a.sink[kH * hs + h] * kLog2e : -INFINITY;
+    float m = s2;
+    for (int s = first; s <= last; ++s) m = fmaxf(m, head(s)->m[h]);
+    float l = s2 > -INFINITY ? ex2_approx(s2 - m) : 0.f;
+    float o[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) o[i] = 0.f;
-  for (int s = first; s <= last; ++s) {
-    const char* at = place(s);
-    const PartHead* hd = reinterpret_cast<const PartHead*>(at + kPartFloats * 4);
-    const float ms = hd->m[h];
+    for (int i = 0; i < 16; ++i) o[i] = 0.f;
+    for (int s = first; s <= last; ++s) {
+      const float ms = head(s)->m[h];
+      const float f = ms == m ? 1.f : ex2_approx(ms - m);
+      l = fmaf(head(s)->l[h], f, l);
+      const float4* src =
+          reinterpret_cast<const float4*>(reinterpret_cast<const float*>(place(s)) + (size_t)h * kD) + lane;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 v = src[32 * i];
+        o[4 * i] = fmaf(v.x, f, o[4 * i]);
+        o[4 * i + 1] = fmaf(v.y, f, o[4 * i + 1]);
+        o[4 * i + 2] = fmaf(v.z, f, o[4 * i + 2]);
+        o[4 * i + 3] = fmaf(v.w, f, o[4 * i + 3]);
+      }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (a.lse && lane == 0) a.lse[orow] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int dim = 128 * i + 4 * lane;
+      uint2 u;
+      u.x = finish(o[4 * i] * inv, o[4 * i + 1] * inv, dim);
+      u.y = finish(o[4 * i + 2] * inv, o[4 * i + 3] * inv, dim + 2);
+      *reinterpret_cast<uint2*>(reinterpret_cast<bf16*>(a.o) + orow * kD + dim) = u;
+    }
+    return;
+  }
+  const int h = blockIdx.y * kJoinHeads + which;
+  const size_t orow = (size_t)row * a.H + kH * hs + h;
+  const float s2 = a.sink != nullptr ? a.sink[kH * hs + h] * kLog2e : -INFINITY;
+  float m = s2;
+  for (int s = first + lane; s <= last; s += 32) m = fmaxf(m, head(s)->m[h]);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  float l = 0.f;
+  for (int s = first + lane; s <= last; s += 32) {
+    const float ms = head(s)->m[h];
+    l = fmaf(head(s)->l[h], ms == m ? 1.f : ex2_approx(ms - m), l);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+  if (s2 > -INFINITY) l += ex2_approx(s2 - m);
+  float4 o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int s = first + warp; s <= last; s += kJoinHeads) {
+    const float ms = head(s)->m[h];
     const float f = ms == m ? 1.f : ex2_approx(ms - m);
-    l = fmaf(hd->l[h], f, l);
-    const float4* src = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(at) + (size_t)h * kD) + lane;
+    const float4* src =
+        reinterpret_cast<const float4*>(reinterpret_cast<const float*>(place(s)) + (size_t)h * kD) + lane;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float4 v = src[32 * i];
-      o[4 * i] = fmaf(v.x, f, o[4 * i]);
-      o[4 * i + 1] = fmaf(v.y, f, o[4 * i + 1]);
-      o[4 * i + 2] = fmaf(v.z, f, o[4 * i + 2]);
-      o[4 * i + 3] = fmaf(v.w, f, o[4 * i + 3]);
+      o[i].x = fmaf(v.x, f, o[i].x);
+      o[i].y = fmaf(v.y, f, o[i].y);
+      o[i].z = fmaf(v.z, f, o[i].z);
+      o[i].w = fmaf(v.w, f, o[i].w);
     }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s_o[warp][32 * i + lane] = o[i];
+  __syncthreads();
+  float2 x = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < kJoinHeads; ++w) {
+    const float2 v = reinterpret_cast<const float2*>(s_o[w])[threadIdx.x];
+    x.x += v.x;
+    x.y += v.y;
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  const size_t orow = (size_t)row * a.H + kH * hs + h;
-  if (a.lse && lane == 0) a.lse[orow] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
-  bf16* dst = reinterpret_cast<bf16*>(a.o) + orow * kD + 4 * lane;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float x[4] = {o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv};
-    const int dim = 128 * i + 4 * lane;
-    if (dim >= kD - kR) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float cs, sn;
-        turn_cos_sin(t, turn_fraction(a.inv_freq[(dim - (kD - kR)) / 2 + e]), &cs, &sn);
-        rot_pair(x[2 * e], x[2 * e + 1], cs, -sn);
-      }
-    }
-    uint2 u;
-    u.x = pack_bf16x2(x[0], x[1]);
-    u.y = pack_bf16x2(x[2], x[3]);
-    *reinterpret_cast<uint2*>(dst + 128 * i) = u;
-  }
+  if (a.lse && threadIdx.x == 0) a.lse[orow] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+  const int dim = 2 * threadIdx.x;
+  *reinterpret_cast<uint32_t*>(reinterpret_cast<bf16*>(a.o) + orow * kD + dim) = finish(x.x * inv, x.y * inv, dim);
 }
 
 }  // namespace
@@ -908,7 +961,7 @@ bool tree_tc_supported(const v4_config& c) {
 }
 
 size_t tree_tc_workspace() {
-  return (size_t)2 * kMaxCtas * kPartBytes + ((kMaxCtas * sizeof(int2) + 255) & ~(size_t)255);
+  return (size_t)2 * kMaxCtas * kPartBytes + ((kMaxCtas * sizeof(int4) + 255) & ~(size_t)255);
 }
 
 cudaError_t launch_tree_tc(const TreeArgs& a, void* workspace, cudaStream_t st) {
@@ -929,7 +982,7 @@ cudaError_t launch_tree_tc(const TreeArgs& a, void* workspace, cudaStream_t st) 
     if (box >= 8) p.box = box;
   }
   p.parts = (char*)workspace;
-  p.cuts = (int2*)((char*)workspace + (size_t)2 * kMaxCtas * kPartBytes);
+  p.cuts = (int4*)((char*)workspace + (size_t)2 * kMaxCtas * kPartBytes);
   // One or two rows a sequence read their keys from HBM, where asking ahead
   // pays (16 ragged sequences over all their tokens: 107 against 113 us); more
   // rows share theirs through L2, where the asking costs (16 rows a sequence:
