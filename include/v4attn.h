@@ -468,8 +468,9 @@ v4_status v4_cache_append(const void* x, int64_t rows, int32_t dim, int64_t x_ro
  * depth(j), depth 0 for a child of the last committed token.
  *
  * v4_tree_plan describes the rows once for all layers of a step:
- *   node_begin  : [B+1] int32, ascending, node_begin[B] <= n_rows.  Rows
- *                 before the first sequence and behind the last are padding.
+ *   node_begin  : [B+1] int32, ascending, node_begin[B] <= n_rows <= 2^24.
+ *                 Rows before the first sequence and behind the last are
+ *                 padding.
  *   seq_len     : [B] int32 >= 0.
  *   parent      : [n_rows] int32, the parent's node number within the
  *                 sequence, -1 = a child of the last committed token; NULL =
@@ -532,9 +533,12 @@ typedef struct v4_tree_inputs {
  *   cfg  : batch, n_heads, head_dim, rope_dim, ratio, window, topk,
  *          softmax_scale, dtype and path are used; seqlen need not bound the
  *          positions.  q_begin must be 0.
- *   o    : [n_rows, H, D] out.    lse : [n_rows, H] fp32 out, nullable.
+ *   o    : [n_rows, H, D] out, must not overlap q.
+ *   lse  : [n_rows, H] fp32 out, nullable.
  * Tensor-core path: bf16, H a multiple of 64 up to 512, D = 512, R = 64;
- * every other shape runs on CUDA cores.  Workspace: v4_tree_workspace_size
+ * every other shape runs on CUDA cores.  It counts tiles of 128 keys in 32
+ * bits: n_rows * H/64 * (longest key list that the tables allow / 128 + 2)
+ * above 2^30 returns V4_ERR_UNSUPPORTED.  Workspace: v4_tree_workspace_size
  * bytes, 256-byte aligned; calls that may overlap need one each.  Results do
  * not depend on what the workspace held, and repeat bit for bit on the same
  * inputs.
@@ -550,7 +554,8 @@ v4_status v4_tree_mqa_fwd(const v4_config* cfg, const v4_tree_inputs* in, void* 
  *   y[t, g, n] = sum_k x[t, g, k] * (code[g, n, k] - 8) * scale[g, n, k / gs]
  * and with norm_dim > 0 every block of norm_dim outputs is RMS-normalised:
  * y / sqrt(mean(y^2) + eps) * norm_w (norm_w [norm_dim] fp32, NULL = ones).
- *   x      : [rows, groups, K] bf16.      y : [rows, groups, N] bf16 out.
+ *   x      : [rows, groups, K] bf16.      y : [rows, groups, N] bf16 out, must
+ *            not overlap x.
  *   codes  : [groups, N, K/2] bytes.  Each 64-byte block holds 128 inputs:
  *            its little-endian 32-bit word 4 t + c (t, c = 0..3) holds inputs
  *            32 c + 8 t .. + 7 of the block, from the lowest nibble in the

@@ -71,6 +71,14 @@ static v4_status check_stride(int64_t s, int es, const char* name) {
   return V4_OK;
 }
 
+// Rows of a call: far above what memory holds, low enough for 32-bit row loops.
+constexpr int32_t kMaxRows = 1 << 24;
+
+static v4_status check_rows(int32_t n_rows) {
+  if (n_rows < 0 || n_rows > kMaxRows) return bad("n_rows must be in [0, 2^24]");
+  return V4_OK;
+}
+
 static bool tree_on_tc(const v4_config& c) { return tree_tc_supported(c) && c.path != V4_PATH_SIMT; }
 
 }  // namespace v4
@@ -185,7 +193,7 @@ v4_status v4_tree_plan(int32_t batch, int32_t n_rows, const int32_t* node_begin,
                        const int32_t* parent, const int32_t* block_table, int32_t max_blocks, int32_t page_size,
                        int64_t n_slots, int32_t* plan, int32_t* pos, int32_t* slot, void* stream) {
   if (batch < 1 || batch > (1 << 24)) return bad("batch must be in [1, 2^24]");
-  if (n_rows < 0) return bad("n_rows must be >= 0");
+  TRY(check_rows(n_rows));
   if (slot) {
     TRY(check_ptr(block_table, "block_table"));
     if (max_blocks < 1) return bad("max_blocks must be >= 1");
@@ -210,7 +218,7 @@ v4_status v4_tree_plan(int32_t batch, int32_t n_rows, const int32_t* node_begin,
 v4_status v4_tree_workspace_size(const v4_config* cfg, int32_t n_rows, size_t* bytes) {
   TRY(validate_config(cfg));
   if (!bytes) return bad("bytes is NULL");
-  if (n_rows < 0) return bad("n_rows must be >= 0");
+  TRY(check_rows(n_rows));
   *bytes = tree_on_tc(*cfg) ? tree_tc_workspace() : 0;
   return V4_OK;
 }
@@ -221,7 +229,7 @@ v4_status v4_tree_mqa_fwd(const v4_config* cfg, const v4_tree_inputs* in, void* 
   if (!in) return bad("inputs struct is NULL");
   const v4_config& c = *cfg;
   if (c.q_begin != 0) return set_error(V4_ERR_UNSUPPORTED, "the tree attention needs q_begin = 0");
-  if (in->n_rows < 0) return bad("n_rows must be >= 0");
+  TRY(check_rows(in->n_rows));
   const bool tc = tree_on_tc(c);
   if (c.path == V4_PATH_TC && !tc)
     return set_error(V4_ERR_UNSUPPORTED, "tensor-core tree attention needs bf16, H a multiple of 64 up to 512, D=512, R=64");
@@ -255,6 +263,17 @@ v4_status v4_tree_mqa_fwd(const v4_config* cfg, const v4_tree_inputs* in, void* 
   }
   if (need > 0 && !workspace) return set_error(V4_ERR_WORKSPACE, "workspace is NULL");
   if ((uintptr_t)workspace & 255u) return set_error(V4_ERR_WORKSPACE, "workspace not 256-byte aligned");
+  const int64_t out_bytes = (int64_t)in->n_rows * c.n_heads * c.head_dim * (c.dtype == V4_BF16 ? 2 : 4);
+  if (overlap(in->q, out_bytes, o, out_bytes)) return bad("q and o overlap");
+  if (tc) {
+    // the kernel counts tiles of 128 keys in 32 bits
+    const int64_t tok = (int64_t)in->tok_blocks * in->tok_page, ent = (int64_t)in->ent_blocks * in->ent_page;
+    const int64_t keys = (c.ratio == 0 ? 0 : c.topk > 0 ? c.topk : ent) +
+                         (c.window == 0 ? 0 : c.window < 0 || c.window > tok ? tok : c.window) + V4_TREE_MAX_NODES;
+    if (keys > (int64_t)1 << 36 || (keys / 128 + 2) * in->n_rows * (c.n_heads / 64) > (int64_t)1 << 30)
+      return set_error(V4_ERR_UNSUPPORTED,
+                       "n_rows times the longest key list that the tables allow is above 2^30 tiles of 128 keys");
+  }
   int* status = device_status_ptr();
   if (!status) return set_error(V4_ERR_CUDA, "device status word unavailable");
   TreeArgs a;
@@ -326,6 +345,7 @@ v4_status v4_w4_proj(const void* x, int64_t rows, int32_t groups, int32_t K, int
   TRY(check_ptr(scales, "scales"));
   TRY(check_ptr(norm_w, "norm_w", false));
   TRY(check_ptr(y, "y"));
+  if (overlap(x, rows * groups * K * 2, y, rows * groups * N * 2)) return bad("x and y overlap");
   StageTiming ps(19, (cudaStream_t)stream);
   return cuda_result(launch_w4_proj(x, rows, groups, K, N, group_size, codes, scales, norm_dim, eps,
                                     norm_dim > 0 ? norm_w : nullptr, y, (cudaStream_t)stream),

@@ -152,6 +152,63 @@ def test_many_rows():
     c.check(*c.run())
 
 
+@pytest.mark.parametrize("page", [8, 20, 24, 96, 100, 256])
+@pytest.mark.parametrize("over", ["tokens", "entries"])
+def test_whole_page_runs_of_any_page_size(page, over):
+    """Every token, or every entry: leading tiles come page by page where the page has a power of two from 8 in it."""
+    if over == "tokens":
+        c = Case([700, 257, 3], [2, 1, 4], window=-1, tok_page=page, seed=13)
+    else:
+        c = Case([3000, 1030, 9], [2, 1, 4], window=64, ratio=4, ent_page=page, seed=14)
+    c.check(*c.run())
+
+
+def test_more_items_than_threads_of_a_block():
+    rng = np.random.default_rng(2)
+    lens = [int(v) for v in rng.integers(0, 300, 70)]
+    nodes = [int(v) for v in rng.integers(1, 7, 70)]
+    c = Case(lens, nodes, H=192, ratio=4, K=24, window=16, seed=15, pad=(2, 5))
+    assert c.n * 3 > 448
+    c.check(*c.run())
+
+
+def test_long_rows_of_several_head_slices():
+    """Items in few and in many parts in one call, with sinks."""
+    c = Case([9000, 40, 2500], [1, 2, 1], H=128, window=-1, tok_page=16, sink=True, seed=16)
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32_tiny"])
+def test_call_of_padding_alone_writes_nothing(kind):
+    kw = dict(H=4, D=64, R=16, dt=torch.float32) if kind == "f32_tiny" else {}
+    c = Case([50], [1], seed=17, **kw)
+    x = c.device_inputs()
+    x["plan"].zero_()
+    x["plan"][:, 0] = -1
+    o = torch.full((c.n, c.H, c.D), 3.0, dtype=c.dt, device="cuda")
+    lse = torch.full((c.n, c.H), 3.0, device="cuda")
+    V.v4_tree_mqa_fwd(c.cfg, x, o, lse, V.alloc_tree_workspace(c.cfg, c.n))
+    assert (o == 3).all() and (lse == 3).all()
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with its own workspace."""
+    cases = [Case([9000, 30], [2, 3], window=-1, seed=18), Case([5000, 700], [4, 1], ratio=4, seed=19)]
+    ins = [c.device_inputs() for c in cases]
+    want = [c.run(x) for c, x in zip(cases, ins)]
+    ws = [V.alloc_tree_workspace(c.cfg, c.n) for c in cases]
+    outs = [(torch.empty_like(o), torch.empty_like(s)) for o, s in want]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for c, x, w, (o, s), st in zip(cases, ins, ws, outs, streams):
+            V.v4_tree_mqa_fwd(c.cfg, x, o, s, w, stream=st)
+    torch.cuda.synchronize()
+    live = [torch.from_numpy(c.plan_ref[:, 0] >= 0).cuda() for c in cases]
+    for (o, s), (wo, wl), m in zip(outs, want, live):
+        assert torch.equal(o[m], wo[m]) and torch.equal(s[m], wl[m])
+
+
 def test_repeats_bit_for_bit_and_replays():
     c = Case([700, 1900, 20], [3, 4, 1], ratio=4, K=128, sink=True, seed=11, pool=60)
     x = c.device_inputs()

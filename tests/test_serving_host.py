@@ -194,6 +194,24 @@ def test_codes_of_the_oracle_round_trip():
         assert int(word >> np.uint32(4 * at)) & 15 == int(w[0, k, 0]) + 8
 
 
+def test_tree_refuses_overlaps_and_counts_beyond_32_bits(lib):
+    refused(lib, tree(lib), L.V4_ERR_INVALID_ARG, "overlap")
+    refused(lib, tree(lib, o=16 + 3 * 64 * 512), L.V4_ERR_INVALID_ARG, "overlap")
+    big = dict(o=1 << 40)
+    cfg = L.make_config(2, 1, 64, 512, 64, window=-1)
+    refused(lib, tree(lib, cfg, n_rows=1 << 18, tok_blocks=16384, **big), L.V4_ERR_UNSUPPORTED, "2^30 tiles")
+    refused(lib, tree(lib, cfg, n_rows=1, tok_blocks=1 << 30, tok_page=1 << 30, **big), L.V4_ERR_UNSUPPORTED, "2^30 tiles")
+    refused(lib, tree(lib, n_rows=(1 << 24) + 1, **big), L.V4_ERR_INVALID_ARG, "n_rows")
+    with pytest.raises(L.V4Error, match="n_rows"):
+        L.v4_tree_workspace_size(cfg, (1 << 24) + 1)
+    refused(lib, lib.v4_tree_plan(2, 1 << 30, 16, 16, 16, 16, 4, 16, 64, 16, 16, 16, None), L.V4_ERR_INVALID_ARG, "n_rows")
+
+
+def test_w4_refuses_overlap(lib):
+    refused(lib, w4(lib), L.V4_ERR_INVALID_ARG, "overlap")
+    refused(lib, w4(lib, y=16 + 3 * 2 * 256 * 2 - 16), L.V4_ERR_INVALID_ARG, "overlap")
+
+
 @pytest.mark.parametrize("swap", ["sign", "window", "order"])
 def test_planted_mistakes_are_seen(swap):
     """The comparisons of this file tell a wrong oracle from a right one."""
