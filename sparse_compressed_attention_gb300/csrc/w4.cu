@@ -106,6 +106,7 @@ struct W4Args {
   bf16* y;
   long long rows;
   int groups, K, N, gs, norm_dim, log_ks, log_rows;      // warps an output's inputs are split over, outputs of a block
+  int sq_at;                                              // shared memory offset of the cluster's sums of squares
   float eps;
 };
 
@@ -193,16 +194,18 @@ __device__ __forceinline__ W4Part w4_part(const W4Args& p, int tokens) {
   return q;
 }
 
-// Partial sums of every warp -> outputs.  `smem` (all of it free) takes
-// [ks][tokens][cta_rows + 4] sums and the cluster's sums of squares behind them:
-// outputs run along the rows, so that sums are stored without bank conflicts
-// (the pitch is 4 modulo 16 words) and leave in 16-byte words.
+// Partial sums of every warp -> outputs.  The ring (free by now) takes
+// [ks][tokens][cta_rows + 4] sums: outputs run along the rows, so that sums
+// are stored without bank conflicts (the pitch is 4 modulo 16 words) and leave
+// in 16-byte words.  The cluster's sums of squares have a place of their own
+// behind the ring: a block that is done writes them to the others while those may
+// still be streaming codes through theirs.
 template <int NT>
 __device__ __forceinline__ void w4_finish(const W4Args& p, const W4Part& q, float (&acc)[NT][4], uint8_t* smem) {
   constexpr int kTok = NT * 8;
   const int threads = blockDim.x, pitch = q.cta_rows + 4, part = kTok * pitch;
   float* red = reinterpret_cast<float*>(smem);
-  auto s_sq = reinterpret_cast<float(*)[kTok]>(red + q.ks * part);
+  auto s_sq = reinterpret_cast<float(*)[kTok]>(smem + p.sq_at);
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     float* at = red + q.kw * part + (8 * j + 2 * q.t) * pitch + q.rw * 16 + q.gq;
@@ -449,22 +452,24 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) w4_rows_kernel(const W4Args
   w4_finish<NT>(p, q, acc, smem);
 }
 
-// Largest of the ring and what w4_finish puts in its place.
-size_t w4_smem(size_t ring, int ks, int cta_rows, int tok) {
-  const size_t fin = (size_t)(ks * (cta_rows + 4) + kMaxCluster) * tok * 4;
+// Larger of the ring and the sums that w4_finish puts in its place; the sums of
+// squares follow.
+size_t w4_ring(size_t ring, int ks, int cta_rows, int tok) {
+  const size_t fin = (size_t)ks * (cta_rows + 4) * tok * 4;
   return ring > fin ? ring : fin;
 }
 
 template <typename Kernel>
-cudaError_t w4_go(Kernel kern, OncePerDevice& once, size_t most, size_t smem, int tok, int threads, W4Args p, int ks,
+cudaError_t w4_go(Kernel kern, OncePerDevice& once, size_t most, size_t ring, int tok, int threads, W4Args p, int ks,
                   int cta_rows, cudaStream_t st) {
   cudaError_t e =
       once.run([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most); });
   if (e != cudaSuccess) return e;
   p.log_ks = ks == 1 ? 0 : ks == 2 ? 1 : 2;
   p.log_rows = cta_rows == 128 ? 7 : cta_rows == 64 ? 6 : cta_rows == 32 ? 5 : 4;
+  p.sq_at = (int)ring;
   cudaLaunchConfig_t cfg = {};
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = ring + (size_t)kMaxCluster * tok * 4;
   cfg.gridDim = dim3(p.N / cta_rows, p.groups, (unsigned)((p.rows + tok - 1) / tok));
   cfg.blockDim = dim3(threads);
   cfg.stream = st;
@@ -497,7 +502,7 @@ cudaError_t w4_few(const W4Args& p, cudaStream_t st) {
   const int cta_rows = 16 * (p.norm_dim > 0 ? 4 : (ks < 4 ? 4 / ks : 1));
   const int warps = ks * (cta_rows / 16);
   constexpr size_t most = 16 * kDepth * kStageBytes + kMaxCluster * 8 * 4;
-  return w4_go(w4_few_kernel<kFold>, once, most, w4_smem((size_t)warps * kDepth * kStageBytes, ks, cta_rows, 8), 8,
+  return w4_go(w4_few_kernel<kFold>, once, most, w4_ring((size_t)warps * kDepth * kStageBytes, ks, cta_rows, 8), 8,
                32 * warps, p, ks, cta_rows, st);
 }
 
@@ -506,8 +511,8 @@ cudaError_t w4_rows_go(const W4Args& p, int ks, int cta_rows, cudaStream_t st) {
   static OncePerDevice once;
   constexpr int kTok = NT * 8;
   constexpr size_t most = 116 * 1024;                                 // two blocks an SM
-  const size_t smem = w4_smem((size_t)kStages * w4_stage_bytes(ks, kTok), ks, cta_rows, kTok);
-  return w4_go(w4_rows_kernel<NT, kFold, kStages>, once, most, smem, kTok, kRowWarps * 32, p, ks, cta_rows, st);
+  const size_t ring = w4_ring((size_t)kStages * w4_stage_bytes(ks, kTok), ks, cta_rows, kTok);
+  return w4_go(w4_rows_kernel<NT, kFold, kStages>, once, most, ring, kTok, kRowWarps * 32, p, ks, cta_rows, st);
 }
 
 template <int NT, int kFold>
@@ -563,7 +568,7 @@ cudaError_t launch_w4_proj(const void* x, long long rows, int groups, int K, int
   p.gs = gs;
   p.norm_dim = norm_dim;
   p.eps = eps;
-  p.log_ks = p.log_rows = 0;
+  p.log_ks = p.log_rows = p.sq_at = 0;
   if (gs == 32) return w4_by_rows<1>(p, st);
   if (gs == 64) return w4_by_rows<2>(p, st);
   return w4_by_rows<4>(p, st);

@@ -55,6 +55,22 @@ def test_projection_with_norm(rows, N, norm, weighted):
     check(y, x, codes, scales, 64, norm, 1e-5, w)
 
 
+@pytest.mark.parametrize("rows,K,N", [(1, 1024, 32768), (8, 512, 16384), (20, 1024, 8192)])
+def test_norm_over_blocks_that_finish_apart(rows, K, N):
+    """A norm's blocks exchange sums while others still stream their codes, some from a cold cache."""
+    x, codes, scales = operands(rows, 1, K, N, 128, seed=rows)
+    y = torch.empty(rows, 1, N, dtype=torch.bfloat16, device="cuda")
+    V.v4_w4_proj(x, codes, scales, y, norm_dim=512)
+    check(y, x, codes, scales, 128, 512)
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    again = torch.empty_like(y)
+    for i in range(40):
+        if i % 2:
+            flush.fill_(i)
+        V.v4_w4_proj(x, codes, scales, again, norm_dim=512)
+        assert torch.equal(y, again), i
+
+
 @pytest.mark.parametrize("rows", [65, 130])
 def test_more_rows_than_a_slice(rows):
     x, codes, scales = operands(rows, 1, 256, 512, 128, seed=rows)
