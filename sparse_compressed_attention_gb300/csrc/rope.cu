@@ -18,8 +18,18 @@ namespace v4 {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
-constexpr int kUnitsPerThread = 4;
+// Small blocks: a block's first loads wait for nothing, its angles do, and the
+// more blocks an SM holds the less of it stands still (256 threads against 128:
+// 10.0 and 9.0 us for 16384 cache rows of 512, 82 and 83 us for 4096 x 64 heads).
+constexpr int kRopeThreads = 128;
+// Units that a thread has in flight.  A unit of the half layout in fp32 is 64
+// bytes; four of them take 109 registers (5003 x 64 heads of 128: 56 us with
+// four, 53 with two), while a bf16 unit is 16 (4096 x 64 heads of 512: 83 us with
+// four, 90 with two).
+template <typename T, bool kHalf>
+constexpr int rope_units() {
+  return sizeof(T) == 4 && kHalf ? 2 : 4;
+}
 constexpr int kMaxAngles = 1024;                 // (row, pair) angles of a tile
 
 // Division by a run-time constant below 2^31: n / d for n < 2^31.
@@ -77,16 +87,17 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs p) {
   const int nh = min(p.hb, p.heads - head0);
   const int n = nr * p.hb * p.units;
   const int half = p.R >> 1;
+  constexpr int kUnits = rope_units<T, kHalf>();
   const T* x = reinterpret_cast<const T*>(p.x) + row0 * p.xr + (long long)head0 * p.xh;
   T* out = reinterpret_cast<T*>(p.out) + (long long)head0 * p.yh;
 
   bool angles = p.pos == nullptr;                 // formed once the first loads are in flight
-  for (int base = 0; base < n; base += kRopeThreads * kUnitsPerThread) {
-    Raw<T> a[kUnitsPerThread], b[kHalf ? kUnitsPerThread : 1];
-    int where[kUnitsPerThread];                   // first angle of a rotated unit, -1: a copied one
-    T* dst[kUnitsPerThread];                      // null: nothing to do
+  for (int base = 0; base < n; base += kRopeThreads * kUnits) {
+    Raw<T> a[kUnits], b[kHalf ? kUnits : 1];
+    int where[kUnits];                            // first angle of a rotated unit, -1: a copied one
+    T* dst[kUnits];                               // null: nothing to do
 #pragma unroll
-    for (int k = 0; k < kUnitsPerThread; ++k) {
+    for (int k = 0; k < kUnits; ++k) {
       const int i = base + k * kRopeThreads + (int)threadIdx.x;
       dst[k] = nullptr;
       if (i >= n) continue;
@@ -127,7 +138,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs p) {
       __syncthreads();
     }
 #pragma unroll
-    for (int k = 0; k < kUnitsPerThread; ++k) {
+    for (int k = 0; k < kUnits; ++k) {
       if (dst[k] == nullptr) continue;
       if (where[k] >= 0) {
         const float2* cs = s_cs + where[k];
@@ -178,11 +189,11 @@ cudaError_t launch_rope(const RopeCall& c, int* status, cudaStream_t st) {
   const bool in_place = c.x == c.out && c.slot == nullptr;
   p.units = p.rot_units + (in_place ? 0 : (c.dim - p.R) / 8);
   if (p.units == 0) return cudaSuccess;          // in place with nothing rotated
-  // Tile: up to kUnitsPerThread units a thread, heads first (they share the
+  // Tile: up to rope_units() units a thread, heads first (they share the
   // row's angles), then rows as far as the angle table reaches; fewer while
   // the tiles would not give every SM one.
   const long long all = c.rows * c.heads * p.units;
-  int want = kRopeThreads * kUnitsPerThread;
+  int want = kRopeThreads * (c.dtype == V4_F32 && by_half ? rope_units<float, true>() : rope_units<bf16, false>());
   while (want > kRopeThreads && all / want < 304) want /= 2;
   const int per_row = c.heads * p.units;
   p.hb = per_row <= want ? c.heads : (want / p.units > 1 ? want / p.units : 1);
