@@ -521,24 +521,30 @@ cudaError_t w4_rows(const W4Args& p, cudaStream_t st) {
   // A block takes 128 outputs; fewer, with the inputs split, while there are
   // not two blocks for each SM (or N is an odd number of 64): two warps on a
   // scheduler leave it idle two cycles of three (8 x 4096 x 1024, 24 rows:
-  // 29.4 / 16.6 us unsplit and split in two).  The norm needs 64 outputs a block
-  // and 64 rows of x the room of two stages.
+  // 13.9 us split in two, 12.5 in four).  The norm needs 64 outputs a block and
+  // more than 32 rows of x the room of two stages.
   int ks = p.N % 128 ? 2 : 1;
-  const int most = p.norm_dim > 0 || NT == 8 ? 2 : 4;
+  const int most = p.norm_dim > 0 || NT > 4 ? 2 : 4;
   while (ks < most && (long long)p.N / 128 * ks * p.groups < 228 && nkb >= 4 * ks) ks *= 2;
   if (p.norm_dim == 64) ks = 2;
   const int cta_rows = 128 / ks;
-  // as many stages as leave room for a second block
-  if (ks * NT >= 16) return w4_rows_go<NT, kFold, 2>(p, ks, cta_rows, st);
-  if (ks * NT >= 8) return w4_rows_go<NT, kFold, 3>(p, ks, cta_rows, st);
+  // as many stages as leave room for a second block and for L1 (48 rows of
+  // 8 x 4096 x 1024, ks 2: 31.1 us with three, 21.4 with two)
+  if (ks * NT > 8) return w4_rows_go<NT, kFold, 2>(p, ks, cta_rows, st);
+  if (ks * NT == 8) return w4_rows_go<NT, kFold, 3>(p, ks, cta_rows, st);
   return w4_rows_go<NT, kFold, 4>(p, ks, cta_rows, st);
 }
 
 template <int kFold>
 cudaError_t w4_by_rows(const W4Args& p, cudaStream_t st) {
+  // As few tiles of eight rows as hold them, where it shows: products and sums are
+  // what bounds the larger counts (24 rows of 8 x 4096 x 1024: 15.2 us in four
+  // tiles, 12.5 in three; 48 rows: 26.5 in eight, 21.4 in six).
   if (p.rows <= 8) return w4_few<kFold>(p, st);
   if (p.rows <= 16) return w4_rows<2, kFold>(p, st);
+  if (p.rows <= 24) return w4_rows<3, kFold>(p, st);
   if (p.rows <= 32) return w4_rows<4, kFold>(p, st);
+  if (p.rows <= 48) return w4_rows<6, kFold>(p, st);
   return w4_rows<8, kFold>(p, st);
 }
 
