@@ -80,15 +80,19 @@ w4_pack_kernel(const bf16* __restrict__ w, int K, int N, int gs, uint32_t* __res
 // loop body).  After that the instructions count (306 a warp and block in the
 // first streaming version, 96 of them unpacking and products: 9.5 us), so
 // pointers are incremented, rows of x beyond the last read the last one (their
-// columns are never stored), and a scale group's first product starts from
-// zero by itself.
+// columns are never stored), a scale group's first product starts from zero by
+// itself and its sums are folded two an instruction.  One row of 1024 x 32768
+// with the norm: 8.7 us (2.1 TB/s of codes; 2 us of it a launch, 1.5 the
+// cluster's exchange), 15 from a cold cache.
 //
 // More rows (w4_rows_kernel): there the rows of x, read again for every 16
 // outputs, are the larger traffic (24 rows: eight times the codes; 18 us for
-// 8 x 4096 x 1024 with the kernel above).  Eight warps share each 128-input
-// block of x through a ring of stages in shared memory, one block barrier a
-// stage; rows lie 256 bytes apart with the halves of odd rows exchanged, so
-// that a fragment read touches every bank once.
+// 8 x 4096 x 1024 with the kernel above, 12.2 with this one).  Eight warps share
+// each 128-input block of x through a ring of stages in shared memory, one
+// block barrier a stage; rows lie 256 bytes apart with the halves of odd rows
+// exchanged, so that a fragment read touches every bank once.  What bounds it
+// now is the issue of instructions (a warp was ready in two cycles of three,
+// the tensor pipe busy in a quarter).
 //
 // `ks` warps share an output's inputs and meet in shared memory.  With a norm,
 // the blocks of a norm_dim run form a cluster and exchange their sums of
@@ -288,15 +292,26 @@ __device__ __forceinline__ void w4_chunk(float (&part)[kParts][NT][4], uint32_t 
   }
 }
 
+// acc += part * scale, two sums an instruction.
+__device__ __forceinline__ void w4_fma2(float& a0, float& a1, float p0, float p1, float s) {
+  asm("{\n\t.reg .b64 a, p, s;\n\t"
+      "mov.b64 a, {%0, %1};\n\tmov.b64 p, {%2, %3};\n\tmov.b64 s, {%4, %4};\n\t"
+      "fma.rn.f32x2 a, p, s, a;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(p0), "f"(p1), "f"(s));
+}
+
 template <int NT, int kParts>
 __device__ __forceinline__ void w4_fold(float (&acc)[NT][4], const float (&part)[kParts][NT][4], float s0, float s1) {
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
+  for (int j = 0; j < NT; ++j) {
+    float v[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float v = kParts == 1 ? part[0][j][e] : part[0][j][e] + part[kParts - 1][j][e];
-      acc[j][e] = fmaf(v, e < 2 ? s0 : s1, acc[j][e]);
-    }
+    for (int e = 0; e < 4; ++e) v[e] = kParts == 1 ? part[0][j][e] : part[0][j][e] + part[kParts - 1][j][e];
+    w4_fma2(acc[j][0], acc[j][1], v[0], v[1], s0);
+    w4_fma2(acc[j][2], acc[j][3], v[2], v[3], s1);
+  }
 }
 
 // Up to eight rows.  kFold chunks of 32 inputs in a scale group.
@@ -530,9 +545,11 @@ cudaError_t w4_rows(const W4Args& p, cudaStream_t st) {
   const int cta_rows = 128 / ks;
   // as many stages as leave room for a second block and for L1 (48 rows of
   // 8 x 4096 x 1024, ks 2: 31.1 us with three, 21.4 with two)
-  if (ks * NT > 8) return w4_rows_go<NT, kFold, 2>(p, ks, cta_rows, st);
-  if (ks * NT == 8) return w4_rows_go<NT, kFold, 3>(p, ks, cta_rows, st);
-  return w4_rows_go<NT, kFold, 4>(p, ks, cta_rows, st);
+  if constexpr (NT > 2)
+    if (ks * NT > 8) return w4_rows_go<NT, kFold, 2>(p, ks, cta_rows, st);
+  if constexpr (8 % NT == 0)
+    if (ks * NT == 8) return w4_rows_go<NT, kFold, 3>(p, ks, cta_rows, st);
+  return w4_rows_go<NT, kFold, NT < 8 ? 4 : 3>(p, ks, cta_rows, st);
 }
 
 template <int kFold>
