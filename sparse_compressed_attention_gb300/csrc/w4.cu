@@ -90,9 +90,9 @@ w4_pack_kernel(const bf16* __restrict__ w, int K, int N, int gs, uint32_t* __res
 // 8 x 4096 x 1024 with the kernel above, 12.2 with this one).  Eight warps share
 // each 128-input block of x through a ring of stages in shared memory, one
 // block barrier a stage; rows lie 256 bytes apart with the halves of odd rows
-// exchanged, so that a fragment read touches every bank once.  What bounds it
-// now is the issue of instructions (a warp was ready in two cycles of three,
-// the tensor pipe busy in a quarter).
+// exchanged, so that a fragment read touches every bank once.  The issue slots
+// are half busy and the tensor pipe a quarter; what is left is the latency of
+// a stage, with 13 warps on an SM to cover it.
 //
 // `ks` warps share an output's inputs and meet in shared memory.  With a norm,
 // the blocks of a norm_dim run form a cluster and exchange their sums of
