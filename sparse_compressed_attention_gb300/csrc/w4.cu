@@ -82,8 +82,8 @@ w4_pack_kernel(const bf16* __restrict__ w, int K, int N, int gs, uint32_t* __res
 // pointers are incremented, rows of x beyond the last read the last one (their
 // columns are never stored), a scale group's first product starts from zero by
 // itself and its sums are folded two an instruction.  One row of 1024 x 32768
-// with the norm: 8.7 us (2.1 TB/s of codes; 2 us of it a launch, 1.5 the
-// cluster's exchange), 15 from a cold cache.
+// with the norm: 7.7 us (2.2 TB/s of codes; 2 us of it a launch, about 1 the
+// cluster's exchange), 8.5 with the codes out of HBM.
 //
 // More rows (w4_rows_kernel): there the rows of x, read again for every 16
 // outputs, are the larger traffic (24 rows: eight times the codes; 18 us for
@@ -99,7 +99,7 @@ w4_pack_kernel(const bf16* __restrict__ w, int K, int N, int gs, uint32_t* __res
 // squares through distributed shared memory.
 // ---------------------------------------------------------------------------
 constexpr int kMaxCluster = 8;
-constexpr int kDepth = 4;                    // blocks in flight (a power of two; eight measured 0.5 us slower: less L1)
+constexpr int kDepth = 2;                    // blocks in flight, a power of two (four: 1 to 9% slower, less L1)
 constexpr uint32_t kStageBytes = 1024;       // codes of 16 outputs x 128 inputs
 
 struct W4Args {
@@ -480,7 +480,8 @@ cudaError_t w4_go(Kernel kern, OncePerDevice& once, size_t most, size_t ring, in
   cudaError_t e =
       once.run([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most); });
   if (e != cudaSuccess) return e;
-  p.log_ks = ks == 1 ? 0 : ks == 2 ? 1 : 2;
+  p.log_ks = 0;
+  while (1 << p.log_ks < ks) ++p.log_ks;
   p.log_rows = cta_rows == 128 ? 7 : cta_rows == 64 ? 6 : cta_rows == 32 ? 5 : 4;
   p.sq_at = (int)ring;
   cudaLaunchConfig_t cfg = {};
@@ -509,12 +510,18 @@ cudaError_t w4_few(const W4Args& p, cudaStream_t st) {
   const int nkb = p.K / 128;
   const long long tiles = (long long)p.N / 16 * p.groups;             // warps without a split of the inputs
   // split the inputs until about twelve warps an SM stream codes, each with a
-  // few blocks to itself
+  // few blocks to itself (up to 16 of them for 16 outputs: 8192 x 1024 7.1 us split
+  // in four, 4.5 in 16).  With a norm a split in four takes an SM for each block; of
+  // clusters of eight such blocks 12 run at once, 16 do not (1024 x 8192 with a
+  // norm of 512: 7.4 us in four, 5.3 in two; 1024 x 4096: 4.2 and 5.3).
+  const int most_ks = p.norm_dim == 0 ? 16 : p.norm_dim > 256 && tiles > 4 * 96 ? 2 : 4;
   int ks = 1;
-  while (ks < 4 && tiles * ks < 1824 && nkb >= 4 * ks) ks *= 2;
-  // a norm's blocks take 64 outputs (eight blocks cover 512); without one a
-  // block is four warps
-  const int cta_rows = 16 * (p.norm_dim > 0 ? 4 : (ks < 4 ? 4 / ks : 1));
+  while (ks < most_ks && tiles * ks < 1824 && nkb >= 4 * ks) ks *= 2;
+  // without a norm a block is four warps; with one it takes 64 outputs, or 128
+  // where the norm covers them and the block stays within 16 warps: smaller clusters
+  // (1024 x 32768 with a norm of 512: 8.3 us in clusters of eight, 7.6 of four)
+  const int wide = p.norm_dim >= 128 && ks <= 2 ? 8 : 4;
+  const int cta_rows = 16 * (p.norm_dim > 0 ? wide : (ks < 4 ? 4 / ks : 1));
   const int warps = ks * (cta_rows / 16);
   constexpr size_t most = 16 * kDepth * kStageBytes + kMaxCluster * 8 * 4;
   return w4_go(w4_few_kernel<kFold>, once, most, w4_ring((size_t)warps * kDepth * kStageBytes, ks, cta_rows, 8), 8,

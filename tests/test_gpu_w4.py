@@ -55,6 +55,17 @@ def test_projection_with_norm(rows, N, norm, weighted):
     check(y, x, codes, scales, 64, norm, 1e-5, w)
 
 
+@pytest.mark.parametrize("rows,G,K,N,gs,norm", [
+    (1, 1, 8192, 64, 128, 0), (8, 2, 4096, 192, 32, 0), (3, 1, 2048, 256, 64, 0),              # inputs split in 16 and 8
+    (2, 1, 1024, 8192, 128, 512), (2, 1, 1024, 16384, 64, 128), (2, 1, 512, 4096, 32, 256),    # norms of wide and narrow blocks
+    (24, 8, 512, 128, 32, 0), (40, 1, 1024, 256, 64, 0), (48, 1, 384, 1024, 128, 512)])        # three and six tiles of rows
+def test_projection_at_every_split(rows, G, K, N, gs, norm):
+    x, codes, scales = operands(rows, G, K, N, gs, seed=K + rows)
+    y = torch.full((rows, G, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    V.v4_w4_proj(x, codes, scales, y, norm_dim=norm)
+    check(y, x, codes, scales, gs, norm)
+
+
 @pytest.mark.parametrize("rows,K,N", [(1, 1024, 32768), (8, 512, 16384), (20, 1024, 8192)])
 def test_norm_over_blocks_that_finish_apart(rows, K, N):
     """A norm's blocks exchange sums while others still stream their codes, some from a cold cache."""
