@@ -113,7 +113,6 @@ struct Args {
   int HS, items;
   int box;                               // rows of a page run that one TMA box takes, 0: gather everything
   int dense_tok;                         // the runs are token pages (else entry pages)
-  int ask;                               // next tile's rows are asked into L2
   char* parts;
   int4* cuts;                            // per block: the item that goes on behind its end (or -1), that item's first and last block
 };
@@ -538,16 +537,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
       auto look_up = [&](int j) {
         return key_row(a, r, bits, pc.row, (long long)(pc.tile0 + j) * kTile + 32 * gw + lane);
       };
-      // Only one tile fits in shared memory, too few bytes in flight to cover
-      // the latency of HBM: rows of the next tile are asked into L2.
-      auto ask = [&](int j) {
-        const bf16* src = j < pc.tiles && p.ask ? look_up(j) : nullptr;
-        if (src != nullptr)
-          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(kD * 2) : "memory");
-      };
+      const bf16* next = look_up(0);
       for (int j = 0; j < pc.tiles && ok; ++j) {
-        // this runs while the tile before is still in use
-        const bf16* src = look_up(j);
+        const bf16* src = next;
         const uint32_t live = __ballot_sync(0xffffffffu, src != nullptr);
         if (lane == 0) {
           // tile g - 2's bits have been read: its O products completed before
@@ -576,7 +568,15 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
           }
           cp_async_mbar_arrive(&c->full_g[m]);
         }
-        ask(j + 1);
+        // Rows of the next tile are looked up while this one is in use, and asked
+        // into L2: only one tile fits in shared memory, too few bytes in flight to
+        // cover the latency of HBM (16 ragged rows over all their tokens: 105 us
+        // without, 93 with).
+        if (j + 1 < pc.tiles) {
+          next = look_up(j + 1);
+          if (next != nullptr)
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(next), "r"(kD * 2) : "memory");
+        }
         ++g;
       }
       ++qc;
@@ -983,11 +983,6 @@ cudaError_t launch_tree_tc(const TreeArgs& a, void* workspace, cudaStream_t st) 
   }
   p.parts = (char*)workspace;
   p.cuts = (int4*)((char*)workspace + (size_t)2 * kMaxCtas * kPartBytes);
-  // One or two rows a sequence read their keys from HBM, where asking ahead
-  // pays (16 ragged sequences over all their tokens: 107 against 113 us); more
-  // rows share theirs through L2, where the asking costs (16 rows a sequence:
-  // 442 against 433 us).
-  p.ask = a.n_rows <= 2 * a.B;
   CUtensorMap mq, mp;
   if (make_tmap_bf16_2d(&mq, a.q, kD, (uint64_t)a.n_rows * a.H, 64, 64, true)) return cudaErrorInvalidValue;
   mp = mq;
