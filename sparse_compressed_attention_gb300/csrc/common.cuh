@@ -98,4 +98,12 @@ __device__ __forceinline__ int n_visible(long long t, int ratio) {
   return ratio > 0 ? (int)((t + 1) / ratio) : 0;
 }
 
+// Waits for the kernels before this one in the stream, whose writes are then
+// visible, and lets the next one's blocks start (they wait here in turn).  Every
+// thread of every block calls it first.
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 }  // namespace v4

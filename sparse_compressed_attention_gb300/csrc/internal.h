@@ -62,6 +62,25 @@ class OncePerDevice {
   std::atomic<bool> done_[kDevices] = {};
 };
 
+// Launch of a short kernel whose blocks may start while the kernel before it in
+// the stream drains (programmatic dependence): 0.2 to 0.5 us a call (16 rotated
+// rows 2.1 -> 1.9 us, one token's tree attention 17.1 -> 16.6).  The kernel calls
+// after_previous() before it touches global memory.
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 // Workspace carve-up for one configuration (Sq = q_rows).  Offsets are
 // 256-byte aligned.
 struct Workspace {

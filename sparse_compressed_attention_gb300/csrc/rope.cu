@@ -7,10 +7,10 @@
 // it in units of eight elements: a thread's loads are all in flight, as raw
 // bits (most units of a partly rotated head are copies and are never
 // converted), while the block forms the tile's (row, pair) angles once in
-// shared memory for all heads.  4096 rows of 64 heads of 512 in bf16 take 82.7 us
-// (6.5 TB/s), the gradient of 5003 rows of 64 heads of 128 in fp32 52.7 us
-// (6.2 TB/s), 16384 cache rows 8.7 us (3.9 TB/s, 2 us of it the launch), one
-// decode step of 16 rows 2.1 us.
+// shared memory for all heads.  4096 rows of 64 heads of 512 in bf16 take 82.0 us
+// (6.5 TB/s), the gradient of 5003 rows of 64 heads of 128 in fp32 52.0 us
+// (6.3 TB/s), 16384 cache rows 8.3 us (4.1 TB/s, nearly 2 us of it the launch),
+// one decode step of 16 rows 1.9 us.
 #include <math.h>
 
 #include "common.cuh"
@@ -84,6 +84,7 @@ struct Raw {
 template <typename T, bool kHalf>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs p) {
   __shared__ float2 s_cs[kMaxAngles];
+  after_previous();
   const long long row0 = (long long)blockIdx.x * p.rb;
   const int head0 = blockIdx.y * p.hb;
   const int nr = (int)min((long long)p.rb, p.rows - row0);
@@ -218,13 +219,10 @@ cudaError_t launch_rope(const RopeCall& c, int* status, cudaStream_t st) {
   p.by_head.set((uint32_t)p.hb);
   const long long gx = (c.rows + rb - 1) / rb;
   const dim3 grid((unsigned)gx, (unsigned)((c.heads + p.hb - 1) / p.hb));
-  if (c.dtype == V4_BF16) {
-    if (by_half) rope_kernel<bf16, true><<<grid, kRopeThreads, 0, st>>>(p);
-    else rope_kernel<bf16, false><<<grid, kRopeThreads, 0, st>>>(p);
-  } else {
-    if (by_half) rope_kernel<float, true><<<grid, kRopeThreads, 0, st>>>(p);
-    else rope_kernel<float, false><<<grid, kRopeThreads, 0, st>>>(p);
-  }
+  auto kern = c.dtype == V4_BF16 ? (by_half ? rope_kernel<bf16, true> : rope_kernel<bf16, false>)
+                                 : (by_half ? rope_kernel<float, true> : rope_kernel<float, false>);
+  const cudaError_t e = launch_overlapped(kern, grid, dim3(kRopeThreads), 0, st, p);
+  if (e != cudaSuccess) return e;
   note_launch();
   return cudaGetLastError();
 }

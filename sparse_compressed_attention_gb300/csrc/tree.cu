@@ -23,7 +23,7 @@ namespace {
 // nearest path members (itself among them) and points 2^s up, so seven
 // rounds cover 128 nodes, against a walk of up to 127 dependent steps.
 // Block B marks the rows of no sequence.  A few kilobytes in and out: the launch
-// bounds it (1.6 us for one node, 2.3 for 32 trees of 8, 9.7 for 256 of 128).
+// bounds it (1.4 us for one node, 2.1 for 32 trees of 8, 9.4 for 256 of 128).
 // ---------------------------------------------------------------------------
 struct PlanArgs {
   const int32_t *node_begin, *seq_len, *parent, *table;
@@ -45,6 +45,7 @@ __global__ void __launch_bounds__(V4_TREE_MAX_NODES) tree_plan_kernel(const Plan
   __shared__ uint4 s_bits[V4_TREE_MAX_NODES];
   __shared__ int s_up[V4_TREE_MAX_NODES], s_depth[V4_TREE_MAX_NODES];
   const int b = blockIdx.x, j = threadIdx.x;
+  after_previous();
   if (b == p.B) {
     const int first = p.node_begin[0], last = p.node_begin[p.B];
     for (int row = j; row < p.n_rows; row += blockDim.x)
@@ -294,7 +295,8 @@ cudaError_t launch_tree_plan(int B, int n_rows, const int32_t* node_begin, const
   p.n_rows = n_rows;
   p.max_blocks = max_blocks;
   p.page = page;
-  tree_plan_kernel<<<B + 1, V4_TREE_MAX_NODES, 0, st>>>(p);
+  const cudaError_t e = launch_overlapped(tree_plan_kernel, dim3(B + 1), dim3(V4_TREE_MAX_NODES), 0, st, p);
+  if (e != cudaSuccess) return e;
   note_launch();
   return cudaGetLastError();
 }

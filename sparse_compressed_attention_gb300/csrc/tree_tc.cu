@@ -37,10 +37,10 @@
 // is filled during the softmax, which makes 2.9 us a tile.  The CUDA-core
 // kernel's times are in brackets:
 //   1 row, 512 selected entries + window        17 us     [246]
-//   32 x up to 8 nodes, selected                52.5 us   [2196]
-//   8 x 8 nodes over 7812 entries each          102 us    [9681]
-//   16 rows over all of up to 49152 tokens      93 us     [19127]
-//   4 x 16 nodes over 32768 tokens              365 us    [40543], 35% tensor pipe
+//   32 x up to 8 nodes, selected                52.3 us   [2196]
+//   8 x 8 nodes over 7812 entries each          103 us    [9681]
+//   16 rows over all of up to 49152 tokens      92 us     [19127]
+//   4 x 16 nodes over 32768 tokens              363 us    [40543], 35% tensor pipe
 // About 5 us of each are the shares, the look-ups and the first tile, 4 to 12 the
 // joined parts.  Tried and not faster: 16 softmax warps, another split of the
 // registers, the softmax in paired fp32 operations or with its exponentials ahead
@@ -270,6 +270,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
   const TreeArgs& a = p.t;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if ((smem_u32(smem) & 1023u) != 0) {          // swizzled operands need 1 KB alignment
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (threadIdx.x == 0) set_status(a.status, V4_ERR_UNSUPPORTED);
     return;
   }
@@ -297,6 +298,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     prefetch_tmap(&map_q);
     prefetch_tmap(&map_pages);
   }
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");      // nothing of global memory is read before
 
   // ---- this block's share: prefix sum of the items' units
   const int per = (p.items + kThreads - 1) / kThreads;
@@ -860,7 +863,7 @@ constexpr int kJoinHeads = 8, kJoinSerial = 8;
 
 __global__ void __launch_bounds__(kJoinHeads * 32) tree_join_kernel(const Args p) {
   __shared__ float4 s_o[kJoinHeads][kD / 4];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  after_previous();
   const TreeArgs& a = p.t;
   const int4 cut = p.cuts[blockIdx.x];
   const int item = cut.x, first = cut.y, last = cut.z, which = blockIdx.x - first;
@@ -1021,7 +1024,8 @@ cudaError_t launch_tree_tc(const TreeArgs& a, void* workspace, cudaStream_t st) 
   if (e != cudaSuccess) return e;
   const int sms = sm_count[dev].load(std::memory_order_relaxed);
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
-  tree_tc_kernel<<<grid, kThreads, kSmemBytes, st>>>(mq, mp, p);
+  e = launch_overlapped(tree_tc_kernel, dim3(grid), dim3(kThreads), kSmemBytes, st, mq, mp, p);
+  if (e != cudaSuccess) return e;
   note_launch();
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;

@@ -84,12 +84,12 @@ w4_pack_kernel(const bf16* __restrict__ w, int K, int N, int gs, uint32_t* __res
 // pointers are incremented, rows of x beyond the last read the last one (their
 // columns are never stored), a scale group's first product starts from zero by
 // itself and its sums are folded two an instruction.  One row of 1024 x 32768
-// with the norm: 7.7 us (2.2 TB/s of codes; 2 us of it a launch, about 1 the
+// with the norm: 8.3 us (2.0 TB/s of codes; 2 us of it a launch, about 1 the
 // cluster's exchange), 8.5 with the codes out of HBM.
 //
 // More rows (w4_rows_kernel): there the rows of x, read again for every 16
 // outputs, are the larger traffic (24 rows: eight times the codes; 18 us for
-// 8 x 4096 x 1024 with the kernel above, 12.2 with this one).  Eight warps share
+// 8 x 4096 x 1024 with the kernel above, 12.0 with this one).  Eight warps share
 // each 128-input block of x through a ring of stages in shared memory, one
 // block barrier a stage; rows lie 256 bytes apart with the halves of odd rows
 // exchanged, so that a fragment read touches every bank once.  The issue slots
@@ -181,6 +181,7 @@ struct W4Part {
 
 __device__ __forceinline__ W4Part w4_part(const W4Args& p, int tokens) {
   W4Part q;
+  after_previous();
   q.warp = threadIdx.x >> 5;
   q.lane = threadIdx.x & 31;
   q.gq = q.lane >> 2;
@@ -492,13 +493,18 @@ cudaError_t w4_go(Kernel kern, OncePerDevice& once, size_t most, size_t ring, in
   cfg.blockDim = dim3(threads);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
   if (p.norm_dim > cta_rows) {
+    // clusters that start early keep the running ones' peers from being placed
+    // (1024 x 32768 with a norm of 512: 10.1 us, 8.4 without)
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = p.norm_dim / cta_rows;
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
+  } else {
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
   }
   e = cudaLaunchKernelEx(&cfg, kern, (const W4Args)p);
   if (e != cudaSuccess) return e;

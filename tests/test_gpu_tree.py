@@ -191,6 +191,84 @@ def test_call_of_padding_alone_writes_nothing(kind):
     assert (o == 3).all() and (lse == 3).all()
 
 
+def test_chain_of_calls_in_a_forked_graph():
+    """Every call starts while the one before drains, and waits for what it reads: a chain of short calls that feed one
+    another, in one stream and over two streams of one captured graph, against the same chain with a wait after each."""
+    g = torch.Generator().manual_seed(33)
+    c = Case([300, 77, 5000], [3, 2, 1], ratio=4, K=48, sink=True, seed=20)
+    x = c.device_inputs()
+    n, H = c.n, 64
+    w = (torch.randn(1, 512, 64 * 512, generator=g) * 0.05).to(torch.bfloat16).cuda()
+    codes, scales = torch.empty(1, 64 * 512, 256, dtype=torch.uint8, device="cuda"), torch.empty(
+        1, 64 * 512, 4, dtype=torch.bfloat16, device="cuda")
+    V.v4_w4_pack(w, 128, codes, scales)
+    lat = torch.randn(n, 1, 512, generator=g).to(torch.bfloat16).cuda()
+    kv = torch.randn(n, 512, generator=g).to(torch.bfloat16).cuda()
+    begin = torch.from_numpy(c.begin.astype(np.int32)).cuda()
+    lens, par = torch.tensor(c.lens, dtype=torch.int32).cuda(), torch.from_numpy(c.parent).cuda()
+    table = x["tok_table"]
+    ws = V.alloc_tree_workspace(c.cfg, n)
+    q, o = (torch.empty(n, H, 512, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    lse = torch.empty(n, H, device="cuda")
+
+    def layer(norm, wait, side=None):
+        here = torch.cuda.current_stream()
+        V.v4_tree_plan(begin, lens, par, x["plan"], pos=c.pos, slot=c.slot, block_table=table, page_size=c.tok_page,
+                       n_slots=c.tok.shape[0] * c.tok_page)
+        wait()
+        if side is not None:
+            side.wait_stream(here)
+        with torch.cuda.stream(side or here):
+            V.v4_cache_append(kv, c.pos, x["inv_freq"], c.slot, x["tok_cache"])
+            wait()
+        V.v4_w4_proj(lat, codes, scales, q.view(n, 1, -1), norm_dim=norm)
+        wait()
+        V.v4_rope(q, c.pos, x["inv_freq"], q, inverse=True)
+        wait()
+        if side is not None:
+            here.wait_stream(side)
+        V.v4_tree_mqa_fwd(c.cfg, dict(x, q=q), o, lse, ws)
+        wait()
+        lat.copy_(o[:, 3][:, None])                    # a kernel of another library in the chain
+        V.v4_rope(o, c.pos, x["inv_freq"], o)
+        wait()
+        kv.copy_(o[:, 7])
+
+    def run(wait, side=None):
+        for norm in (512, 64, 0, 512):
+            layer(norm, wait, side)
+
+    start = [t.clone() for t in (lat, kv, x["tok_cache"])]
+
+    def reset():
+        for t, s in zip((lat, kv, x["tok_cache"]), start):
+            t.copy_(s)
+        torch.cuda.synchronize()
+
+    live = torch.from_numpy(c.plan_ref[:, 0] >= 0).cuda()
+    outs = []
+    run(torch.cuda.synchronize)
+    outs.append((o[live].clone(), lse[live].clone(), x["tok_cache"].clone()))
+    side, main = torch.cuda.Stream(), torch.cuda.Stream()
+    for other in (None, side):
+        reset()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=main):
+            run(lambda: None, other)
+        for _ in range(3):
+            reset()
+            graph.replay()
+            torch.cuda.synchronize()
+            outs.append((o[live].clone(), lse[live].clone(), x["tok_cache"].clone()))
+    reset()
+    run(lambda: None)
+    torch.cuda.synchronize()
+    outs.append((o[live].clone(), lse[live].clone(), x["tok_cache"].clone()))
+    for got in outs[1:]:
+        assert all(torch.equal(u, v) for u, v in zip(got, outs[0]))
+    assert V.v4_get_device_status() == 0
+
+
 def test_two_calls_at_once():
     """Calls on two streams, each with its own workspace."""
     cases = [Case([9000, 30], [2, 3], window=-1, seed=18), Case([5000, 700], [4, 1], ratio=4, seed=19)]
