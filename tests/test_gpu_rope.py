@@ -91,6 +91,35 @@ def test_strided_views_in_place_and_head_major():
     check(before[:, 4:8, :128].contiguous(), before[:, 0:4, :128].contiguous(), pos, f, 64)
 
 
+@pytest.mark.parametrize("order", ["rows", "heads"])
+def test_strides_beyond_32_bits(order):
+    """Rows, or heads, 2^30 elements apart: a tile of them does not fit 32-bit offsets."""
+    f = freqs(16)
+    x, pos = draw(4, 3, 64, torch.bfloat16, seed=9)
+    shape, far = (4, 3, 64), 1 << 30
+    stride = (far, 64, 1) if order == "rows" else (64, far, 1)
+    big = torch.empty(5 * far, dtype=torch.bfloat16, device="cuda")
+    src = big.as_strided(shape, stride)
+    src.copy_(x)
+    out = torch.empty(shape, dtype=torch.bfloat16, device="cuda")
+    V.v4_rope(src, pos, torch.from_numpy(f).cuda(), out)
+    check(out, x, pos, f, 48)
+    V.v4_rope(x, pos, torch.from_numpy(f).cuda(), src)
+    check(src, x, pos, f, 48)
+    V.v4_rope(src, pos, torch.from_numpy(f).cuda(), src, inverse=True)
+    check(src, out, pos, f, 48, inverse=True)
+
+
+def test_cache_write_beyond_32_bits():
+    f = freqs(64)
+    x, pos = draw(70, 1, 512, torch.bfloat16, seed=10)
+    n = (1 << 23) + 200
+    cache = torch.empty(n // 8, 8, 512, dtype=torch.bfloat16, device="cuda")
+    slot = (torch.randperm(100)[:70] + (1 << 23) + 50).to(torch.int32).cuda()
+    V.v4_cache_append(x[:, 0], pos, torch.from_numpy(f).cuda(), slot, cache)
+    check(cache.view(-1, 512)[slot.long()][:, None], x, pos, f, 448)
+
+
 @pytest.mark.parametrize("half", [False, True])
 def test_gradient_is_the_inverse_call(half):
     """Against central differences of sum(dout * rope(x)) in fp32 (the map is linear: the difference quotient is exact up

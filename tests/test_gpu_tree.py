@@ -269,6 +269,23 @@ def test_chain_of_calls_in_a_forked_graph():
     assert V.v4_get_device_status() == 0
 
 
+@pytest.mark.parametrize("over", ["selected", "tokens", "entries"])
+def test_offsets_beyond_32_bits(over):
+    """Pages more than 2^32 bytes (and 2^32 elements) into their caches, gathered and as page runs."""
+    c = {"selected": lambda: Case([300, 77], [3, 2], ratio=4, K=48, seed=22),
+         "tokens": lambda: Case([700, 257], [2, 1], window=-1, seed=23),
+         "entries": lambda: Case([3000, 1030], [2, 1], window=64, ratio=4, ent_page=64, seed=24)}[over]()
+    x = c.device_inputs()
+    for kind in ("tok", "ent") if c.ratio else ("tok",):
+        small, table = x[kind + "_cache"], x[kind + "_table"]
+        pages, page, D = small.shape
+        far = (1 << 32) // (page * D) + 5
+        big = torch.empty(far + pages, page, D, dtype=small.dtype, device="cuda")
+        big[far:] = small
+        x[kind + "_cache"], x[kind + "_table"] = big, torch.where(table < 0, table, table + far)
+    c.check(*c.run(x))
+
+
 def test_two_calls_at_once():
     """Calls on two streams, each with its own workspace."""
     cases = [Case([9000, 30], [2, 3], window=-1, seed=18), Case([5000, 700], [4, 1], ratio=4, seed=19)]
