@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(V4_TREE_MAX_NODES) tree_plan_kernel(const Plan
 // memory, lane j scores key j, the running maximum and denominator are kept
 // in fp32, and each lane accumulates channels lane, lane + 32, ...  The fallback:
 // bound by its fp32 products out of shared memory (one row of 64 heads over 641
-// keys 246 us, where the tensor-core kernel takes 17).
+// keys 246 us, where the tensor-core kernel takes 16).
 // ---------------------------------------------------------------------------
 constexpr int kHG = 8, kKT = 32, kSimtThreads = kHG * 32;
 

@@ -36,8 +36,8 @@
 // released pair by pair by the O products and filled again meanwhile, but nothing
 // is filled during the softmax, which makes 2.9 us a tile.  The CUDA-core
 // kernel's times are in brackets:
-//   1 row, 512 selected entries + window        17 us     [246]
-//   32 x up to 8 nodes, selected                52.3 us   [2196]
+//   1 row, 512 selected entries + window        16.2 us   [246]
+//   32 x up to 8 nodes, selected                52 us     [2196]
 //   8 x 8 nodes over 7812 entries each          103 us    [9681]
 //   16 rows over all of up to 49152 tokens      92 us     [19127]
 //   4 x 16 nodes over 32768 tokens              363 us    [40543], 35% tensor pipe
@@ -80,6 +80,13 @@ constexpr uint32_t OFF_SLOT = OFF_Q + 9 * kQBlockBytes;           // 73728
 constexpr uint32_t OFF_P = OFF_SLOT + kSlots * kSlotBytes;        // 204800
 constexpr uint32_t OFF_CTL = OFF_P + kPBytes;                     // 221184
 
+// A row's key list in tiles.
+struct Tiles {
+  int n;                                 // all of them, 0: the row is not live
+  int dense;                             // leading ones that are whole page runs
+  int seq;
+};
+
 // A block's piece of an item.
 struct alignas(16) Piece {               // two 16-byte words: it is copied through shared memory
   int row, hs, tile0, tiles;
@@ -107,7 +114,8 @@ struct Ctl {
   float part_l[4][kH];
   float inv[kH];
   int scan[kThreads / 32];
-  int start_item, start_unit, total;     // where this block's share begins
+  int start_item, start_unit;            // where this block's share begins
+  Tiles start_tiles;
   uint32_t tmem_base;
   int abort;
   int decision;
@@ -133,16 +141,15 @@ struct Args {
   int4* cuts;                            // per block: the item that goes on behind its end (or -1), that item's first and last block
 };
 
-// Tiles of a row's key list; *dense: how many leading ones are whole page runs.
-__device__ __forceinline__ int tree_tiles(const Args& p, int row, int* dense = nullptr) {
+// Tiles of a row.
+__device__ __forceinline__ Tiles tree_tiles(const Args& p, int row) {
   const TreeArgs& a = p.t;
   const TreeRow r = tree_row(a, row);
-  if (!r.live) return 0;
-  if (dense) *dense = p.box ? (p.dense_tok ? r.nw : r.ne) / kTile : 0;
+  if (!r.live) return Tiles{0, 0, 0};
   const int4 w = *reinterpret_cast<const int4*>(a.plan + (size_t)row * kPlanWords + 4);
   const int nd = a.window == 0 ? 0 : __popc(w.x) + __popc(w.y) + __popc(w.z) + __popc(w.w);
   const long long nk = (long long)r.ne + r.nw + nd;
-  return nk == 0 ? 1 : (int)((nk + kTile - 1) / kTile);
+  return Tiles{nk == 0 ? 1 : (int)((nk + kTile - 1) / kTile), p.box ? (p.dense_tok ? r.nw : r.ne) / kTile : 0, r.b};
 }
 
 // Node of the i-th set bit.
@@ -305,9 +312,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
   const int per = (p.items + kThreads - 1) / kThreads;
   const int i0 = threadIdx.x * per, i1 = min(i0 + per, p.items);
   int mine = 0;
+  Tiles first = {0, 0, 0};
   for (int i = i0; i < i1; ++i) {
-    const int n = tree_tiles(p, i / p.HS);
-    mine += n ? n + 1 : 0;
+    const Tiles t = tree_tiles(p, i / p.HS);
+    if (i == i0) first = t;
+    mine += t.n ? t.n + 1 : 0;
   }
   int upto = mine;
 #pragma unroll
@@ -331,11 +340,12 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
   if (before <= s0 && s0 < before + mine) {
     int at = before;
     for (int i = i0; i < i1; ++i) {
-      const int n = tree_tiles(p, i / p.HS);
-      const int u = n ? n + 1 : 0;
+      const Tiles t = i == i0 ? first : tree_tiles(p, i / p.HS);
+      const int u = t.n ? t.n + 1 : 0;
       if (s0 < at + u) {
         c->start_item = i;
         c->start_unit = at;
+        c->start_tiles = t;
         break;
       }
       at += u;
@@ -358,8 +368,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     auto next_piece = [&]() -> Piece {
       Piece pc = {0, 0, 0, 0, 1, 0, -1, 0};
       while (item < p.items && unit < s1) {
-        int dense = 0;
-        const int n = tree_tiles(p, item / p.HS, &dense);
+        const Tiles t = item == c->start_item ? c->start_tiles : tree_tiles(p, item / p.HS);
+        const int n = t.n;
         const int base = unit + 1;               // unit of the item's tile 0
         const int lo = max(s0, base), hi = min(s1, base + n);
         if (n > 0 && lo < hi) {
@@ -368,10 +378,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
           pc.hs = item % p.HS;
           pc.tile0 = lo - base;
           pc.tiles = hi - lo;
-          pc.dense = min(max(dense - pc.tile0, 0), pc.tiles);
+          pc.dense = min(max(t.dense - pc.tile0, 0), pc.tiles);
           // a share that begins behind tile 0 leaves its part in the block's
           // first place, one that begins with it in the second
-          pc.seq = a.plan[(size_t)pc.row * kPlanWords];
+          pc.seq = t.seq;
           pc.part = pc.tiles == n ? -1 : 2 * (int)blockIdx.x + (lo > base ? 0 : 1);
           if (base + n > s1) cut = make_int4(item, base / share, (base + n - 1) / share, 0);
         }
