@@ -98,12 +98,14 @@ __device__ __forceinline__ int n_visible(long long t, int ratio) {
   return ratio > 0 ? (int)((t + 1) / ratio) : 0;
 }
 
-// Waits for the kernels before this one in the stream, whose writes are then
-// visible, and lets the next one's blocks start (they wait here in turn).  Every
-// thread of every block calls it first.
+// wait_previous: the kernels before this one in the stream have ended and their
+// writes are visible; every thread of every block calls it before it touches
+// global memory.  start_next: the next kernel's blocks may start (and wait in turn).
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void start_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void after_previous() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_previous();
+  start_next();
 }
 
 }  // namespace v4

@@ -277,7 +277,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
   const TreeArgs& a = p.t;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if ((smem_u32(smem) & 1023u) != 0) {          // swizzled operands need 1 KB alignment
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_previous();
     if (threadIdx.x == 0) set_status(a.status, V4_ERR_UNSUPPORTED);
     return;
   }
@@ -306,7 +306,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     prefetch_tmap(&map_pages);
   }
 
-  asm volatile("griddepcontrol.wait;" ::: "memory");      // nothing of global memory is read before
+  wait_previous();                              // nothing of global memory is read before
 
   // ---- this block's share: prefix sum of the items' units
   const int per = (p.items + kThreads - 1) / kThreads;
@@ -849,7 +849,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
   }
 
   tc_fence_before();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  start_next();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();

@@ -84,8 +84,8 @@ w4_pack_kernel(const bf16* __restrict__ w, int K, int N, int gs, uint32_t* __res
 // pointers are incremented, rows of x beyond the last read the last one (their
 // columns are never stored), a scale group's first product starts from zero by
 // itself and its sums are folded two an instruction.  One row of 1024 x 32768
-// with the norm: 8.3 us (2.0 TB/s of codes; 2 us of it a launch, about 1 the
-// cluster's exchange), 8.5 with the codes out of HBM.
+// with the norm: 8.0 us (2.1 TB/s of codes; nearly 2 us of it a launch, about 1
+// the cluster's exchange).
 //
 // More rows (w4_rows_kernel): there the rows of x, read again for every 16
 // outputs, are the larger traffic (24 rows: eight times the codes; 18 us for
@@ -181,7 +181,11 @@ struct W4Part {
 
 __device__ __forceinline__ W4Part w4_part(const W4Args& p, int tokens) {
   W4Part q;
-  after_previous();
+  // The next kernel's blocks may come at once, but clusters that come early keep
+  // the running one's from being placed: those wait for the sums (1024 x 32768
+  // with a norm of 512: 10.1 us at once, 8.0 before the exchange, 8.7 after it).
+  wait_previous();
+  if (p.norm_dim <= (1 << p.log_rows)) start_next();
   q.warp = threadIdx.x >> 5;
   q.lane = threadIdx.x & 31;
   q.gq = q.lane >> 2;
@@ -384,6 +388,7 @@ __global__ void __launch_bounds__(512) w4_few_kernel(const W4Args p) {
   if (left > 0) block(xb, xc);
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();                              // every ring is read: partial sums take its place
+  if (q.peers > 1) start_next();
   w4_finish<1>(p, q, acc, smem);
 }
 
@@ -467,6 +472,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) w4_rows_kernel(const W4Args
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
+  if (q.peers > 1) start_next();
   w4_finish<NT>(p, q, acc, smem);
 }
 
@@ -492,19 +498,17 @@ cudaError_t w4_go(Kernel kern, OncePerDevice& once, size_t most, size_t ring, in
   cfg.gridDim = dim3(p.N / cta_rows, p.groups, (unsigned)((p.rows + tok - 1) / tok));
   cfg.blockDim = dim3(threads);
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
   if (p.norm_dim > cta_rows) {
-    // clusters that start early keep the running ones' peers from being placed
-    // (1024 x 32768 with a norm of 512: 10.1 us, 8.4 without)
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = p.norm_dim / cta_rows;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-  } else {
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = p.norm_dim / cta_rows;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
   }
   e = cudaLaunchKernelEx(&cfg, kern, (const W4Args)p);
   if (e != cudaSuccess) return e;
