@@ -260,10 +260,11 @@ def test_chain_of_calls_in_a_forked_graph():
             graph.replay()
             torch.cuda.synchronize()
             outs.append((o[live].clone(), lse[live].clone(), x["tok_cache"].clone()))
-    reset()
-    run(lambda: None)
-    torch.cuda.synchronize()
-    outs.append((o[live].clone(), lse[live].clone(), x["tok_cache"].clone()))
+    for other in (None, side):
+        reset()
+        run(lambda: None, other)
+        torch.cuda.synchronize()
+        outs.append((o[live].clone(), lse[live].clone(), x["tok_cache"].clone()))
     for got in outs[1:]:
         assert all(torch.equal(u, v) for u, v in zip(got, outs[0]))
     assert V.v4_get_device_status() == 0
