@@ -526,7 +526,8 @@ typedef struct v4_tree_inputs {
  *     read from token row L + j of the cache.
  * o = softmax-weighted sum (V = K) with the optional sink, de-rotated at -t;
  * lse natural log.  An empty key set yields o = 0 and lse = -inf (with a
- * sink: o = 0, lse = sink).  Rows of padding (plan sequence -1) keep their o
+ * sink: o = 0, lse = sink).  A sink of -inf is none, one of +inf takes its
+ * head whole (o = 0, lse = +inf), a NaN makes its head's o and lse NaN.  Rows of padding (plan sequence -1) keep their o
  * and lse.  Only the rows of the caches named above are read; a token or
  * entry whose page the table does not hold (a negative or too large value)
  * is skipped and flagged.

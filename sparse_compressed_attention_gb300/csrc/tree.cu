@@ -175,9 +175,14 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const TreeArgs 
   }
   const long long nk = (long long)r.ne + r.nw + nd;
   float m = -INFINITY, l = 0.f;
-  if (a.sink != nullptr && head_live && a.sink[h] > -INFINITY) {
-    m = a.sink[h];
-    l = 1.f;
+  if (a.sink != nullptr && head_live) {
+    const float s = a.sink[h];
+    if (s > -INFINITY) {
+      m = s;
+      l = 1.f;
+    } else if (s != s) {
+      l = s;                                     // a NaN sink makes the denominator one
+    }
   }
   float acc[32];
 #pragma unroll

@@ -266,6 +266,13 @@ __device__ __forceinline__ float fold_lanes(float* r, int lane, F f) {
   return r[0];
 }
 
+// What a sink (log2 units) adds to a denominator whose shift m is at least as
+// large: nothing at -inf, one where it is the shift itself (+inf among them),
+// NaN for a NaN, which the maximum has dropped.
+__device__ __forceinline__ float sink_mass(float s2, float m) {
+  return s2 == -INFINITY ? 0.f : s2 == m ? 1.f : ex2_approx(s2 - m);
+}
+
 // Units of a share: each item is one unit (its query rows and output) plus
 // its tiles.  Block c of the grid takes units [c * share, (c + 1) * share).
 __device__ __forceinline__ int share_of(int total, int ctas) { return (total + ctas - 1) / ctas; }
@@ -798,7 +805,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             const float s2 = a.sink[kH * cur.hs + ts] * kLog2e;
             m = fmaxf(m_row, s2);
             f = m_row == m ? 1.f : ex2_approx(m_row - m);
-            l = l_row * f + (s2 > -INFINITY ? ex2_approx(s2 - m) : 0.f);
+            l = l_row * f + sink_mass(s2, m);
           }
           c->inv[ts] = l == 0.f ? 0.f : f / l;
           if (a.lse) a.lse[orow + ts] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
@@ -902,7 +909,7 @@ __global__ void __launch_bounds__(kJoinHeads * 32) tree_join_kernel(const Args p
     const float s2 = a.sink != nullptr ? a.sink[kH * hs + h] * kLog2e : -INFINITY;
     float m = s2;
     for (int s = first; s <= last; ++s) m = fmaxf(m, head(s)->m[h]);
-    float l = s2 > -INFINITY ? ex2_approx(s2 - m) : 0.f;
+    float l = sink_mass(s2, m);
     float o[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[i] = 0.f;
@@ -947,7 +954,7 @@ __global__ void __launch_bounds__(kJoinHeads * 32) tree_join_kernel(const Args p
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-  if (s2 > -INFINITY) l += ex2_approx(s2 - m);
+  l += sink_mass(s2, m);
   float4 o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
