@@ -427,8 +427,10 @@ v4_status v4_attn_layer_fwd(const v4_config* cfg, const v4_layer_inputs* in,
  *   dim a multiple of 8 up to 8192; rope_dim a multiple of 8 (16 for
  *   V4_ROPE_HALF), <= 1024; rope_begin a multiple of 8, rope_begin +
  *   rope_dim <= dim.  rows = 0 is valid.  dtype: a v4_dtype.
- * Angles are formed from a 64-bit fraction of a turn (any int32 position);
- * the rotation is fp32 with one rounding to the storage type.
+ * Angles are formed from a 64-bit fraction of a turn, for any int32 position:
+ * within |pos| (1 + |inv_freq| / 8) 2^-64 + 2^-32 turns, and another 2^-28 for
+ * the fp32 remainder that is left of them; the rotation is fp32 with one
+ * rounding to the storage type.
  * --------------------------------------------------------------------*/
 typedef enum { V4_ROPE_INTERLEAVED = 0, V4_ROPE_HALF = 1 } v4_rope_layout;
 v4_status v4_rope(const void* x, int64_t rows, int32_t heads, int32_t dim, int64_t x_row_stride,

@@ -37,8 +37,8 @@ def rope(x, pos, inv_freq, begin, half=False, inverse=False, mscale=1.0):
 def rope_error(x, inv_freq, begin, half=False, mscale=1.0):
     """Bound of the fp32 rotation's error before the final rounding, per element.
 
-    Angle: at most pi 2^-25 from its fp32 fraction of a half turn and 1.5e-9 from
-    the dropped bits; sine and cosine 2^-23; a scale, two products and a sum 2^-24 each:
+    Angle: at most pi 2^-25 from an fp32 fraction of a half turn (pi 2^-27 from one of
+    an eighth of a turn) and 1.5e-9 from the dropped bits; sine and cosine 2^-23; a scale, two products and a sum 2^-24 each:
     below 2^-21 (|a| + |b|) in all."""
     e = np.zeros(np.shape(x), F64)
     R = 2 * len(inv_freq)

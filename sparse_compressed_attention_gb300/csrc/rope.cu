@@ -62,7 +62,7 @@ struct RopeArgs {
   int heads, R, begin, inverse;
   int rot_units, units;        // units of a (row, head): rotated ones first, then copied ones
   int rb, hb;                  // rows and heads of a tile
-  FastDiv by_unit, by_head;
+  FastDiv by_unit, by_head, by_half;
 };
 
 // Eight elements as raw 16-byte words: one for bf16, two for float.
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs p) {
     if (!angles) {
       angles = true;
       for (int j = threadIdx.x; j < nr * half; j += kRopeThreads) {
-        const int r = j / half, c = j - r * half;
+        const int r = (int)p.by_half.div((uint32_t)j), c = j - r * half;
         float cs, sn;
         turn_cos_sin(p.pos[row0 + r], turn_fraction(p.inv_freq[c]), &cs, &sn);
         s_cs[j] = make_float2(cs * p.mscale, (p.inverse ? -sn : sn) * p.mscale);
@@ -217,6 +217,7 @@ cudaError_t launch_rope(const RopeCall& c, int* status, cudaStream_t st) {
   p.tyh = p.hb > 1 ? (int)p.yh : 0;
   p.by_unit.set((uint32_t)p.units);
   p.by_head.set((uint32_t)p.hb);
+  p.by_half.set((uint32_t)(half > 0 ? half : 1));
   const long long gx = (c.rows + rb - 1) / rb;
   const dim3 grid((unsigned)gx, (unsigned)((c.heads + p.hb - 1) / p.hb));
   auto kern = c.dtype == V4_BF16 ? (by_half ? rope_kernel<bf16, true> : rope_kernel<bf16, false>)

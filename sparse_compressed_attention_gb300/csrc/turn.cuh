@@ -5,9 +5,14 @@
 // 2^-64 units, F = f / (2 pi) mod 1, and the angle of a position is the
 // 64-bit product pos * F, which wraps at whole turns by itself.  f = m * 2^e
 // with a 24-bit m, so F = m * (2^66 / (2 pi)) * 2^(e-2) needs one 64 x 24
-// bit product; the constant is good to 2^-64 relative, which leaves an angle
-// error below 2^-31 turns for |pos| < 2^31 and f <= 1.  The top 32 bits go to
-// sincospif.  No fp64: this part's fp64 rate is low.
+// bit product; the constant is rounded to 64 bits and F cut off behind its last,
+// which leaves F within (1 + |f| / 8) 2^-64 and the angle within |pos| times that
+// many turns: 2^-32 at the farthest positions for |f| <= 1.  The top 32 bits
+// are split, still as integers, into quarter turns and a remainder of at most an
+// eighth of a turn to either side, since fp32 holds 24 bits: sincospif gets the
+// remainder to 2^-28 turns (the whole angle would come to 2^-26, the largest
+// term in the error of an fp32 rotation), and the quarter turns only exchange and
+// negate its results.  No fp64: this part's fp64 rate is low.
 #pragma once
 
 #include <stdint.h>
@@ -34,9 +39,15 @@ __device__ __forceinline__ uint64_t turn_fraction(float f) {
 
 // cos and sin of pos * F turns.
 __device__ __forceinline__ void turn_cos_sin(int pos, uint64_t F, float* c, float* s) {
-  const uint64_t a = (uint64_t)(long long)pos * F;
-  const int hi = (int)(a >> 32);                    // signed: half a turn is -2^31
-  sincospif((float)hi * 4.656612873077393e-10f, s, c);      // 2^-31: half turns
+  const uint32_t a = (uint32_t)(((uint64_t)(long long)pos * F) >> 32);
+  const uint32_t quarters = (a + 0x20000000u) >> 30;        // modulo four
+  const int rest = (int)(a - (quarters << 30));             // within 2^29 of zero
+  float sr, cr;
+  sincospif((float)rest * 4.656612873077393e-10f, &sr, &cr);      // 2^-31: half turns
+  const bool swap = quarters & 1u;
+  const float x = swap ? sr : cr, y = swap ? cr : sr;
+  *c = (quarters + 1u) & 2u ? -x : x;
+  *s = quarters & 2u ? -y : y;
 }
 
 }  // namespace v4

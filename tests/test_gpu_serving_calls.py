@@ -1,8 +1,11 @@
 """Calls of the serving operators that a program may make and the other files do not."""
+import numpy as np
 import pytest
 import torch
 
 import sparse_compressed_attention_gb300 as V
+from oracle import serving_oracle as S
+from tests.helpers import np64
 from tests.tree_cases import Case
 
 pytestmark = pytest.mark.gpu
@@ -31,3 +34,30 @@ def test_sinks_that_are_no_numbers(kind):
     none = c.run({k: v for k, v in x.items() if k != "sink"})
     assert torch.equal(o[:, 6], none[0][:, 6]) and torch.equal(lse[:, 6], none[1][:, 6])
     assert V.v4_get_device_status() == 0
+
+
+@pytest.mark.parametrize("half", [False, True])
+def test_angles_keep_their_precision_at_every_part_of_a_turn(half):
+    """Rows of ones and zeros come out as the cosines and sines themselves.
+
+    The angle reaches sincospif within an eighth of a turn of a quarter, in half turns below 1/4: half a step of fp32 is
+    2^-27 of them, pi 2^-27 as an angle.  The 64-bit fraction of a turn behind it is off by less than 2^-31 turns for
+    tables up to 1.  sincospif is within one step (2^-23 relative at most), products with one and zero are exact."""
+    rows, R = 4096, 64
+    rng = np.random.default_rng(5)
+    f = (10.0 ** rng.uniform(-6, 0, R // 2)).astype(np.float32)
+    pos = rng.integers(-2 ** 31, 2 ** 31, rows).astype(np.int32)
+    pos[:1024] = rng.integers(0, 4096, 1024)
+    x = torch.zeros(rows, 1, R, device="cuda")
+    out = torch.empty_like(x)
+    first = slice(0, R // 2) if half else slice(0, R, 2)
+    second = slice(R // 2, R) if half else slice(1, R, 2)
+    x[..., first] = 1.0
+    V.v4_rope(x, torch.from_numpy(pos).cuda(), torch.from_numpy(f).cuda(), out,
+              layout=V.V4_ROPE_HALF if half else V.V4_ROPE_INTERLEAVED)
+    phi = S.angles(pos, f)
+    got = np64(out)[:, 0]
+    for part, ref in ((first, np.cos(phi)), (second, np.sin(phi))):
+        err = np.abs(got[:, part] - ref)
+        allow = 2.0 ** -23 * np.abs(ref) + np.pi * 2.0 ** -27 + 2 * np.pi * 2.0 ** -31
+        assert np.all(err <= allow), float((err / allow).max())
