@@ -285,7 +285,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if ((smem_u32(smem) & 1023u) != 0) {          // swizzled operands need 1 KB alignment
     wait_previous();
-    if (threadIdx.x == 0) set_status(a.status, V4_ERR_UNSUPPORTED);
+    if (threadIdx.x == 0) {
+      set_status(a.status, V4_ERR_UNSUPPORTED);
+      p.cuts[blockIdx.x] = make_int4(-1, -1, -1, 0);        // nothing for the join
+    }
     return;
   }
   if (threadIdx.x == 0) {
