@@ -118,7 +118,6 @@ struct Ctl {
   Tiles start_tiles;
   uint32_t tmem_base;
   int abort;
-  int decision;
 };
 constexpr uint32_t kSmemBytes = OFF_CTL + sizeof(Ctl);
 static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -405,8 +404,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
       if (lane == 0) {
         const int is = q & 1;
         if (q >= 2) ok = mbar_wait(&c->info_empty[is], ((q >> 1) - 1) & 1, &c->abort, a.status);
-        c->info[is] = pc;
-        mbar_arrive(&c->info_full[is]);
+        if (ok) {
+          c->info[is] = pc;
+          mbar_arrive(&c->info_full[is]);
+        }
       }
       ok = __shfl_sync(0xffffffffu, (int)ok, 0);
     };
@@ -634,21 +635,20 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     const auto fmax2 = [](float x, float y) { return fmaxf(x, y); };
     const auto fadd2 = [](float x, float y) { return x + y; };
 
+    // The next piece, unless a warp's wait for it gave up: what that one has read
+    // is none, and addresses nothing.
     auto next_piece = [&](int qc, Piece& pc) -> bool {
       const int is = qc & 1;
-      warp_wait(&c->info_full[is], (qc >> 1) & 1, c, a.status);
+      const bool ok = warp_wait(&c->info_full[is], (qc >> 1) & 1, c, a.status);
       pc = c->info[is];
+      const bool last = !ok || pc.done;
       warp_arrive(&c->info_empty[is], lane);
-      if (ts == 0) c->decision = (c->abort || pc.done) ? 1 : 0;
-      if (!pc.done && ts < kR / 2) {
+      if (!last && ts < kR / 2) {
         float cs, sn;
         turn_cos_sin(a.plan[(size_t)pc.row * kPlanWords + 2], F, &cs, &sn);
         c->cs[is][ts] = make_float2(cs, sn);
       }
-      named_bar_sync(1, kSoftThreads);
-      const bool more = c->decision == 0;
-      named_bar_sync(1, kSoftThreads);
-      return more;
+      return !bar_any(1, kSoftThreads, last);
     };
     // Rotate the last 64 dims of each head (four threads a head), as a high
     // and a low bf16 term.
@@ -861,6 +861,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
   tc_fence_before();
   start_next();
   __syncthreads();
+  if (c->abort && threadIdx.x == 0) {           // bulk copies that were asked for land before the block goes
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 200000) {
+    }
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
