@@ -62,6 +62,22 @@ class OncePerDevice {
   std::atomic<bool> done_[kDevices] = {};
 };
 
+// Lets a kernel take what dynamic shared memory a block can have beside its static
+// part.  Once: the limit belongs to the process, and one that follows each call's
+// own size is taken away by another host thread's smaller call before the launch.
+template <typename Kernel>
+cudaError_t allow_shared(Kernel kern, OncePerDevice& once) {
+  return once.run([&] {
+    int dev = 0, most = 0;
+    cudaFuncAttributes at;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, kern);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most - (int)at.sharedSizeBytes);
+  });
+}
+
 // Launch of a short kernel whose blocks may start while the kernel before it in
 // the stream drains (programmatic dependence): 0.2 to 0.5 us a call (16 rotated
 // rows 2.1 -> 1.9 us, one token's tree attention 17.1 -> 16.6).  The kernel calls

@@ -273,7 +273,8 @@ template <typename T>
 cudaError_t tree_simt_t(const TreeArgs& a, cudaStream_t st) {
   const size_t smem = (size_t)(kHG * a.D + kKT * (a.D + 1) + kHG * kKT) * sizeof(float);
   auto kern = tree_simt_kernel<T>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static OncePerDevice once;
+  const cudaError_t e = allow_shared(kern, once);
   if (e != cudaSuccess) return e;
   const dim3 grid(a.n_rows, (a.H + kHG - 1) / kHG);
   kern<<<grid, kSimtThreads, smem, st>>>(a);

@@ -1,10 +1,13 @@
 """Calls of the serving operators that a program may make and the other files do not."""
+import threading
+
 import numpy as np
 import pytest
 import torch
 
 import sparse_compressed_attention_gb300 as V
 from oracle import serving_oracle as S
+from sparse_compressed_attention_gb300 import _lib
 from tests.helpers import np64
 from tests.tree_cases import Case
 
@@ -61,3 +64,65 @@ def test_angles_keep_their_precision_at_every_part_of_a_turn(half):
         err = np.abs(got[:, part] - ref)
         allow = 2.0 ** -23 * np.abs(ref) + np.pi * 2.0 ** -27 + 2 * np.pi * 2.0 ** -31
         assert np.all(err <= allow), float((err / allow).max())
+
+
+def library_call(call, stream):
+    """The library function and the arguments of the last call that `call` makes on `stream`."""
+    real, made = _lib.lib(), []
+
+    class Spy:
+        def __getattr__(self, name):
+            fn = getattr(real, name)
+
+            def go(*args):
+                made.append((fn, args))
+                return fn(*args)
+            return go
+
+    _lib._lib = Spy()
+    try:
+        call(stream)
+    finally:
+        _lib._lib = real
+    return made[-1]
+
+
+def at_once(*calls, times=20000):
+    """Each call `times` times in a host thread and on a stream of its own, through the library alone; what was refused."""
+    made, refused, done = [library_call(c, torch.cuda.Stream()) for c in calls], [], []
+    gate = threading.Barrier(len(calls))
+
+    def work(fn, args):
+        torch.cuda.set_device(0)
+        gate.wait()
+        for _ in range(times):
+            if fn(*args) != 0:
+                refused.append(_lib.lib().v4_last_error().decode())
+                return
+        done.append(fn)
+
+    threads = [threading.Thread(target=work, args=m) for m in made]
+    torch.cuda.synchronize()
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert len(done) + len(refused) == len(calls)
+    return refused
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_tree_calls_of_two_host_threads_with_other_widths(dt):
+    cases = [Case([9], [1], H=3, D=512, R=64, dt=dt, seed=1), Case([5], [1], H=2, D=32, R=16, dt=dt, seed=2)]
+    ins = [c.device_inputs() for c in cases]
+    want = [c.run(x) for c, x in zip(cases, ins)]
+    outs = [(torch.empty_like(o), torch.empty_like(s)) for o, s in want]
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+
+    def call(c, x, o, s):
+        return lambda stream: V.v4_tree_mqa_fwd(c.cfg, x, o, s, ws, stream=stream)
+
+    assert at_once(*(call(c, x, o, s) for c, x, (o, s) in zip(cases, ins, outs))) == []
+    for (o, s), (wo, wl) in zip(outs, want):
+        assert torch.equal(o, wo) and torch.equal(s, wl)
