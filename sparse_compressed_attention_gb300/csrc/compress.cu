@@ -582,7 +582,8 @@ cudaError_t compress_t(const v4_config& c, const void* ckv, const void* cscore, 
   const int nms = threads / ncv;
   const size_t smem = (size_t)(3 * nms * dim + dim) * sizeof(float);
   auto kern = G >= 32 ? compress_kernel<T, true> : compress_kernel<T, false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static OncePerDevice once[2];
+  const cudaError_t e = allow_shared(kern, once[G >= 32]);
   if (e != cudaSuccess) return e;
   dim3 grid(N, c.batch);
   kern<<<grid, threads, smem, st>>>((const T*)ckv, (const T*)cscore, ape, norm_w, inv_freq, cs_table,

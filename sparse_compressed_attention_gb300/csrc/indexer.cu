@@ -331,7 +331,8 @@ cudaError_t scores_t(const v4_config& c, const void* iqp, const void* ikey, cons
   const int N = c.seqlen / c.ratio;
   const size_t smem = (size_t)(c.idx_heads * c.idx_dim + c.idx_heads) * sizeof(float);
   auto kern = indexer_scores_kernel<T>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static OncePerDevice once;
+  const cudaError_t e = allow_shared(kern, once);
   if (e != cudaSuccess) return e;
   const float wscale = 1.0f / sqrtf((float)c.idx_heads) / sqrtf((float)c.idx_dim);
   dim3 grid(q_rows(c), c.batch);
@@ -357,7 +358,8 @@ cudaError_t launch_topk(const v4_config& c, const float* scores, int32_t* idx, f
   // (measured faster at 16384 keys than staging 64 KB per row)
   const int cap = N < 4096 ? N : 4096;
   const size_t smem = (size_t)((cap + 3) & ~3) * sizeof(uint32_t);      // whole 4-key chunks
-  cudaError_t e = cudaFuncSetAttribute(topk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static OncePerDevice once;
+  const cudaError_t e = allow_shared(topk_kernel, once);
   if (e != cudaSuccess) return e;
   dim3 grid(q_rows(c), c.batch);
   topk_kernel<<<grid, kTopkThreads, smem, st>>>(scores, idx, iscore, q_rows(c), c.q_begin, N, c.topk, c.ratio,

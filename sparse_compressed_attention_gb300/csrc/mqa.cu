@@ -204,7 +204,8 @@ cudaError_t mqa_t(const v4_config& c, const void* q, const void* kv_rot, const v
   const int D = c.head_dim;
   const size_t smem = (size_t)(kHG * D + kKT * (D + 1) + kHG * kKT) * sizeof(float);
   auto kern = mqa_simt_kernel<T>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static OncePerDevice once;
+  const cudaError_t e = allow_shared(kern, once);
   if (e != cudaSuccess) return e;
   const int N = c.ratio > 0 ? c.seqlen / c.ratio : 0;
   const float scale = c.softmax_scale > 0.f ? c.softmax_scale : 1.0f / sqrtf((float)D);

@@ -126,3 +126,43 @@ def test_tree_calls_of_two_host_threads_with_other_widths(dt):
     assert at_once(*(call(c, x, o, s) for c, x, (o, s) in zip(cases, ins, outs))) == []
     for (o, s), (wo, wl) in zip(outs, want):
         assert torch.equal(o, wo) and torch.equal(s, wl)
+
+
+def sequence_call(op, big):
+    """One call of an operator over a short sequence whose kernel takes much (or little) shared memory."""
+    g = torch.Generator().manual_seed(int(big))
+    f32 = lambda *shape: torch.randn(*shape, generator=g).cuda()        # noqa: E731
+    D, R = (512, 64) if big else (32, 16)
+    if op == "attention":
+        cfg = V.make_config(1, 4, 2, D, R, window=4, dtype="f32", path=V.V4_PATH_SIMT)
+        q, kv, f, o = f32(1, 4, 2, D), f32(1, 4, D), f32(R // 2).abs(), torch.empty(1, 4, 2, D, device="cuda")
+        return lambda ws, s: V.v4_sparse_mqa_fwd(cfg, q, kv, None, None, None, f, o, None, ws, stream=s), cfg, o
+    if op == "compressor":
+        cfg = V.make_config(1, 64, 2, D, R, ratio=32, dtype="f32", path=V.V4_PATH_SIMT)
+        kv, sc, ape, f = f32(1, 64, D), f32(1, 64, D), f32(32, D), f32(R // 2).abs()
+        o = torch.empty(1, 2, D, device="cuda")
+        return lambda ws, s: V.v4_compress(cfg, kv, sc, ape, None, f, D, 0, o, stream=s), cfg, o
+    Hi, Di, n = (64, 128, 64) if big else (1, 16, 8)
+    n = 400 if big else n
+    cfg = V.make_config(1, n, 2, 32, 16, ratio=4, topk=4, Hi=Hi, Di=Di, dtype="f32", path=V.V4_PATH_SIMT)
+    iq, ik, w, f = f32(1, n, Hi, Di), f32(1, n // 4, Di), f32(1, n, Hi), f32(8).abs()
+    o = torch.empty(1, n, 4, dtype=torch.int32, device="cuda")
+    return lambda ws, s: V.v4_indexer_topk(cfg, iq, 1, ik, w, f, o, None, ws, stream=s), cfg, o
+
+
+@pytest.mark.parametrize("op", ["attention", "compressor", "indexer"])
+def test_sequence_calls_of_two_host_threads_with_other_widths(op):
+    made = [sequence_call(op, big) for big in (True, False)]
+    ws = [V.alloc_workspace(cfg) for _, cfg, _ in made]
+    want = []
+    for (call, _, o), w in zip(made, ws):
+        call(w, None)
+        want.append(o.clone())
+        o.zero_()
+
+    def bound(call, w):
+        return lambda stream: call(w, stream)
+
+    assert at_once(*(bound(call, w) for (call, _, _), w in zip(made, ws))) == []
+    for (_, _, o), wo in zip(made, want):
+        assert torch.equal(o, wo)
