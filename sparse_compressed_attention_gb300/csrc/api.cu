@@ -29,6 +29,8 @@ static v4_status fail(v4_status st, const char* fmt, ...) {
   vsnprintf(buf, sizeof(buf), fmt, ap);
   va_end(ap);
   g_err = buf;
+  // reported here, so not left behind for the next launch's check
+  if (st == V4_ERR_CUDA) cudaGetLastError();
   return st;
 }
 

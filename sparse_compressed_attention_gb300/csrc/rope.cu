@@ -223,9 +223,8 @@ cudaError_t launch_rope(const RopeCall& c, int* status, cudaStream_t st) {
   auto kern = c.dtype == V4_BF16 ? (by_half ? rope_kernel<bf16, true> : rope_kernel<bf16, false>)
                                  : (by_half ? rope_kernel<float, true> : rope_kernel<float, false>);
   const cudaError_t e = launch_overlapped(kern, grid, dim3(kRopeThreads), 0, st, p);
-  if (e != cudaSuccess) return e;
-  note_launch();
-  return cudaGetLastError();
+  if (e == cudaSuccess) note_launch();
+  return e;
 }
 
 }  // namespace v4

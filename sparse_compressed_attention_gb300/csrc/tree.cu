@@ -302,9 +302,8 @@ cudaError_t launch_tree_plan(int B, int n_rows, const int32_t* node_begin, const
   p.max_blocks = max_blocks;
   p.page = page;
   const cudaError_t e = launch_overlapped(tree_plan_kernel, dim3(B + 1), dim3(V4_TREE_MAX_NODES), 0, st, p);
-  if (e != cudaSuccess) return e;
-  note_launch();
-  return cudaGetLastError();
+  if (e == cudaSuccess) note_launch();
+  return e;
 }
 
 cudaError_t launch_tree_simt(const TreeArgs& a, int dtype, cudaStream_t st) {

@@ -516,9 +516,8 @@ cudaError_t w4_go(Kernel kern, OncePerDevice& once, size_t most, size_t ring, in
     cfg.numAttrs = 2;
   }
   e = cudaLaunchKernelEx(&cfg, kern, (const W4Args)p);
-  if (e != cudaSuccess) return e;
-  note_launch();
-  return cudaGetLastError();
+  if (e == cudaSuccess) note_launch();
+  return e;
 }
 
 template <int kFold>

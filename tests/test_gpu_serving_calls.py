@@ -1,4 +1,5 @@
 """Calls of the serving operators that a program may make and the other files do not."""
+import ctypes
 import threading
 
 import numpy as np
@@ -166,3 +167,26 @@ def test_sequence_calls_of_two_host_threads_with_other_widths(op):
     assert at_once(*(bound(call, w) for (call, _, _), w in zip(made, ws))) == []
     for (_, _, o), wo in zip(made, want):
         assert torch.equal(o, wo)
+
+
+def test_a_call_after_one_that_could_not_be_launched():
+    """A launch that the runtime refuses (the legacy stream, while a blocking stream is captured) is reported by its own call
+    and by no later one."""
+    rt = ctypes.CDLL("libcudart.so.13")
+    x = torch.randn(4, 2, 64).cuda()
+    pos, f = torch.arange(4, dtype=torch.int32).cuda(), torch.rand(8).cuda()
+    out, want = torch.empty_like(x), torch.empty_like(x)
+    V.v4_rope(x, pos, f, want)
+    torch.cuda.synchronize()
+    stream, graph = ctypes.c_void_p(), ctypes.c_void_p()
+    assert rt.cudaStreamCreate(ctypes.byref(stream)) == 0
+    try:
+        assert rt.cudaStreamBeginCapture(stream, 0) == 0
+        with pytest.raises(V.V4Error, match="rotation kernel"):
+            V.v4_rope(x, pos, f, out, stream=0)
+    finally:
+        rt.cudaStreamEndCapture(stream, ctypes.byref(graph))
+        rt.cudaStreamDestroy(stream)
+        rt.cudaGetLastError()
+    V.v4_rope(x, pos, f, out)
+    assert torch.equal(out, want)
