@@ -306,7 +306,6 @@ v4_status v4_tree_mqa_fwd(const v4_config* cfg, const v4_tree_inputs* in, void* 
   a.K = c.ratio > 0 ? c.topk : 0;
   a.scale = c.softmax_scale > 0.f ? c.softmax_scale : 1.0f / sqrtf((float)c.head_dim);
   cudaStream_t st = (cudaStream_t)stream;
-  StageTiming ps(16, st);
   return cuda_result(tc ? launch_tree_tc(a, workspace, st) : launch_tree_simt(a, c.dtype, st), "tree attention kernel");
 }
 

@@ -277,6 +277,7 @@ cudaError_t tree_simt_t(const TreeArgs& a, cudaStream_t st) {
   const cudaError_t e = allow_shared(kern, once);
   if (e != cudaSuccess) return e;
   const dim3 grid(a.n_rows, (a.H + kHG - 1) / kHG);
+  StageTiming ps(16, st);
   kern<<<grid, kSimtThreads, smem, st>>>(a);
   note_launch();
   return cudaGetLastError();

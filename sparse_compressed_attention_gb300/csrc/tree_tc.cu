@@ -1049,9 +1049,12 @@ cudaError_t launch_tree_tc(const TreeArgs& a, void* workspace, cudaStream_t st) 
   if (e != cudaSuccess) return e;
   const int sms = sm_count[dev].load(std::memory_order_relaxed);
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
-  e = launch_overlapped(tree_tc_kernel, dim3(grid), dim3(kThreads), kSmemBytes, st, mq, mp, p);
-  if (e != cudaSuccess) return e;
-  note_launch();
+  {
+    StageTiming ps(16, st);
+    e = launch_overlapped(tree_tc_kernel, dim3(grid), dim3(kThreads), kSmemBytes, st, mq, mp, p);
+    if (e != cudaSuccess) return e;
+    note_launch();
+  }
   {
     StageTiming ps(17, st);
     cudaLaunchConfig_t cfg = {};

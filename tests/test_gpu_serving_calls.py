@@ -190,3 +190,22 @@ def test_a_call_after_one_that_could_not_be_launched():
         rt.cudaGetLastError()
     V.v4_rope(x, pos, f, out)
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("kind", ["tensor_cores", "cuda_cores"])
+def test_stages_of_the_tree_attention_are_apart(kind):
+    """The attention's record ends before the join's begins: records come in the order in which stages end."""
+    c = Case([5000, 3], [1, 1], window=-1, seed=3) if kind == "tensor_cores" else Case([90], [2], H=3, seed=4)
+    x = c.device_inputs()
+    c.run(x)
+    k, ms = ctypes.c_int32(), ctypes.c_float()
+    L = _lib.lib()
+    assert L.v4_profile_enable(1) == 0
+    c.run(x)
+    assert L.v4_profile_enable(0) == 0
+    n = L.v4_profile_count()
+    kinds = []
+    for i in range(n):
+        assert L.v4_profile_get(i, ctypes.byref(k), ctypes.byref(ms)) == 0 and ms.value > 0
+        kinds.append(_lib.PROFILE_KINDS[k.value])
+    assert kinds == (["tree_attention", "tree_join"] if kind == "tensor_cores" else ["tree_attention"])
