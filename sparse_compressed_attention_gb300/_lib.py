@@ -508,7 +508,8 @@ def _paged(cache, table, kind, D, B, dt, dev):
 
 def v4_tree_mqa_fwd(cfg, inputs, o, lse, workspace, stream=None):
     """Attention of planned rows over paged caches.  inputs: a dict keyed like v4_tree_inputs' pointers, with
-    tok_cache / ent_cache [pages, page_size, D] and tok_table / ent_table [B, blocks]."""
+    tok_cache / ent_cache [pages, page_size, D] and tok_table / ent_table [B, blocks].  workspace may be None where
+    v4_tree_workspace_size is 0."""
     i32, f32 = torch.int32, torch.float32
     get = inputs.get
     q, sink = inputs["q"], get("sink")
@@ -529,11 +530,11 @@ def v4_tree_mqa_fwd(cfg, inputs, o, lse, workspace, stream=None):
         _shaped(q, "q", shape, dt, dev), _shaped(inputs["plan"], "plan", (n, 8), i32, dev), tc, tt, ec, et, el, ix,
         None if sink is None else _shaped(sink, "sink", (H,), f32, dev),
         _shaped(get("inv_freq"), "inv_freq", (half,), f32, dev) if half else None, ts, es, n, tb, tp, eb, ep)
-    size = workspace.numel()
+    size = 0 if workspace is None else workspace.numel()
     st = lib().v4_tree_mqa_fwd(cfg, vin, _shaped(o, "o", shape, dt, dev),
                                None if lse is None else _shaped(lse, "lse", (n, H), f32, dev),
-                               _shaped(workspace, "workspace", (size,), torch.uint8, dev), size,
-                               _stream_on(stream, dev))
+                               None if workspace is None else _shaped(workspace, "workspace", (size,), torch.uint8, dev),
+                               size, _stream_on(stream, dev))
     if st:
         _check(st)
     return o

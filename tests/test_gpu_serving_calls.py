@@ -209,3 +209,17 @@ def test_stages_of_the_tree_attention_are_apart(kind):
         assert L.v4_profile_get(i, ctypes.byref(k), ctypes.byref(ms)) == 0 and ms.value > 0
         kinds.append(_lib.PROFILE_KINDS[k.value])
     assert kinds == (["tree_attention", "tree_join"] if kind == "tensor_cores" else ["tree_attention"])
+
+
+def test_workspace_may_be_left_out_where_none_is_needed():
+    c = Case([90, 7], [2, 1], H=3, D=64, R=16, seed=6)
+    x = c.device_inputs()
+    o, lse = c.run(x)
+    o2, lse2 = torch.full_like(o, 3.0), torch.full_like(lse, 3.0)
+    assert V.v4_tree_workspace_size(c.cfg, c.n) == 0
+    V.v4_tree_mqa_fwd(c.cfg, x, o2, lse2, None)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    c = Case([90, 7], [2, 1], seed=6)
+    with pytest.raises(V.V4Error, match="workspace"):
+        V.v4_tree_mqa_fwd(c.cfg, c.device_inputs(), *(torch.empty(c.n, 64, *d, dtype=t, device="cuda") for d, t in
+                                                      (((512,), torch.bfloat16), ((), torch.float32))), None)
