@@ -534,8 +534,8 @@ typedef struct v4_tree_inputs {
  * entry whose page the table does not hold (a negative or too large value)
  * is skipped and flagged.
  *   cfg  : batch, n_heads, head_dim, rope_dim, ratio, window, topk,
- *          softmax_scale, dtype and path are used; seqlen need not bound the
- *          positions.  q_begin must be 0.
+ *          softmax_scale, dtype and path are used, the others may hold
+ *          anything.  q_begin must be 0.
  *   o    : [n_rows, H, D] out, must not overlap q.
  *   lse  : [n_rows, H] fp32 out, nullable.
  * Tensor-core path: bf16, H a multiple of 64 up to 512, D = 512, R = 64;

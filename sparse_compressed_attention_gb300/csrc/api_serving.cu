@@ -79,6 +79,22 @@ static v4_status check_rows(int32_t n_rows) {
   return V4_OK;
 }
 
+// The configuration as the tree attention reads it.  What it has no use for (the
+// length, the compressor's and the indexer's fields) may hold anything.
+static v4_status tree_config(const v4_config* cfg, v4_config* c) {
+  if (!cfg) return validate_config(cfg);
+  *c = *cfg;
+  c->seqlen = 1;
+  c->overlap = c->indexer_fp8 = c->q_begin = 0;
+  c->topk = 0;                                   // with one the indexer's fields are checked
+  c->rms_eps = 0.f;
+  TRY(validate_config(c));
+  if (cfg->topk < 0) return bad("topk must be >= 0");
+  if (cfg->topk > 0 && cfg->ratio < 1) return bad("topk needs ratio >= 1");
+  c->topk = cfg->topk;
+  return V4_OK;
+}
+
 static bool tree_on_tc(const v4_config& c) { return tree_tc_supported(c) && c.path != V4_PATH_SIMT; }
 
 }  // namespace v4
@@ -216,19 +232,20 @@ v4_status v4_tree_plan(int32_t batch, int32_t n_rows, const int32_t* node_begin,
 }
 
 v4_status v4_tree_workspace_size(const v4_config* cfg, int32_t n_rows, size_t* bytes) {
-  TRY(validate_config(cfg));
+  v4_config c;
+  TRY(tree_config(cfg, &c));
   if (!bytes) return bad("bytes is NULL");
   TRY(check_rows(n_rows));
-  *bytes = tree_on_tc(*cfg) ? tree_tc_workspace() : 0;
+  *bytes = tree_on_tc(c) ? tree_tc_workspace() : 0;
   return V4_OK;
 }
 
 v4_status v4_tree_mqa_fwd(const v4_config* cfg, const v4_tree_inputs* in, void* o, float* lse, void* workspace,
                           size_t ws_bytes, void* stream) {
-  TRY(validate_config(cfg));
+  v4_config c;
+  TRY(tree_config(cfg, &c));
   if (!in) return bad("inputs struct is NULL");
-  const v4_config& c = *cfg;
-  if (c.q_begin != 0) return set_error(V4_ERR_UNSUPPORTED, "the tree attention needs q_begin = 0");
+  if (cfg->q_begin != 0) return set_error(V4_ERR_UNSUPPORTED, "the tree attention needs q_begin = 0");
   TRY(check_rows(in->n_rows));
   const bool tc = tree_on_tc(c);
   if (c.path == V4_PATH_TC && !tc)
