@@ -420,8 +420,9 @@ v4_status v4_attn_layer_fwd(const v4_config* cfg, const v4_layer_inputs* in,
  *              elements; strides >= 0, multiples of 16 bytes.  x may be
  *              broadcast (a stride of 0); out's rows must not overlap
  *              (refused).  out may be x with the same strides (in place:
- *              only the rotated dims are touched); otherwise the two must not
- *              overlap.
+ *              only the rotated dims are touched), or another view of x's
+ *              buffer with the same strides and no element of x; other
+ *              tensors whose extents overlap are refused.
  *   pos      : [rows] int32, any value.   inv_freq : [rope_dim/2] fp32,
  *              finite (the table of v4_rope_inv_freq, or any other scaling).
  *   dim a multiple of 8 up to 8192; rope_dim a multiple of 8 (16 for

@@ -62,6 +62,23 @@ static bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
   return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
 }
 
+// Whether a view of no x ni runs of dim elements (nested: the inner runs of one outer
+// step end before the next) and the same view moved by `shift` elements have an
+// element in common: some difference of outer and inner steps brings a run within
+// dim of another.  The outer difference is one of the two around shift / so, since
+// what is left is smaller than so, the inner one likewise.
+static bool views_meet(int64_t shift, int64_t no, int64_t so, int64_t ni, int64_t si, int64_t dim) {
+  const int64_t moved = shift < 0 ? -shift : shift;                // the other way round it is the same
+  const int64_t o0 = no > 1 ? moved / so : 0;
+  for (int64_t o = o0; o <= o0 + 1 && o < no; ++o) {
+    const int64_t rest = moved - o * so < 0 ? o * so - moved : moved - o * so;
+    const int64_t i0 = ni > 1 ? rest / si : 0;
+    for (int64_t i = i0; i <= i0 + 1 && i < ni; ++i)
+      if (rest - i * si < dim && i * si - rest < dim) return true;
+  }
+  return false;
+}
+
 static v4_status check_stride(int64_t s, int es, const char* name) {
   char buf[128];
   if (s < 0 || s > (int64_t)1 << 40 || (s * es) % 16) {
@@ -129,14 +146,11 @@ v4_status v4_rope(const void* x, int64_t rows, int32_t heads, int32_t dim, int64
   const bool same = x == out && (rows == 1 || x_row_stride == rs) && (heads == 1 || x_head_stride == hs);
   if (!same && overlap(x, extent(rows, heads, dim, x_row_stride, x_head_stride, es), out,
                        extent(rows, heads, dim, rs, hs, es))) {
-    // two views of one buffer are apart when they step alike and their
-    // columns do not meet: whole rows of heads side by side, or parts of a head
+    // two views of one buffer that step alike, as parts of a head or runs of heads
     const int64_t step = (intptr_t)out - (intptr_t)x;
-    const int64_t gap = (step < 0 ? -step : step) / es, span = (heads - 1) * hs + dim;
     const bool alike = step % es == 0 && (rows == 1 || x_row_stride == rs) && (heads == 1 || x_head_stride == hs);
-    const bool by_row = gap >= span && (rows == 1 || gap + span <= rs);
-    const bool by_head = heads > 1 && gap >= dim && gap + dim <= hs && (rows == 1 || heads * hs <= rs);
-    const bool apart = alike && (by_row || by_head);
+    const bool apart = alike && !(rows_outer ? views_meet(step / es, rows, rs, heads, hs, dim)
+                                             : views_meet(step / es, heads, hs, rows, rs, dim));
     if (!apart) return bad("x and out overlap and are not the same tensor");
   }
   RopeCall c;

@@ -223,3 +223,37 @@ def test_workspace_may_be_left_out_where_none_is_needed():
     with pytest.raises(V.V4Error, match="workspace"):
         V.v4_tree_mqa_fwd(c.cfg, c.device_inputs(), *(torch.empty(c.n, 64, *d, dtype=t, device="cuda") for d, t in
                                                       (((512,), torch.bfloat16), ((), torch.float32))), None)
+
+
+@pytest.mark.parametrize("order", ["rows", "heads"])
+def test_views_of_one_buffer_that_do_not_meet(order):
+    """Two views that step alike are refused exactly where an element belongs to both."""
+    pos, f = torch.arange(3, dtype=torch.int32).cuda(), torch.tensor([0.5, 0.01, 1.0, 0.3]).cuda()
+    base = torch.randn(400, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    seen = [0, 0]
+    for rows in (1, 2, 3):
+        for heads in (1, 2, 3):
+            inner = rows if order == "heads" else heads
+            outer = heads if order == "heads" else rows
+            for s_in in (8, 16, 24, 32):
+                for s_out in ((inner - 1) * s_in + 8, (inner - 1) * s_in + 16, (inner - 1) * s_in + 40):
+                    span = (outer - 1) * s_out + (inner - 1) * s_in + 8
+                    st = (s_in, s_out) if order == "heads" else (s_out, s_in)
+                    at = np.array([t * st[0] + h * st[1] + c for t in range(rows) for h in range(heads) for c in range(8)])
+                    for shift in range(-64, 72, 8):
+                        if not shift or 100 + abs(shift) + span > 400 or 100 + shift < 0:
+                            continue
+                        buf = base.clone()
+                        x = buf.as_strided((rows, heads, 8), (*st, 1), 100 - 100 % 8)
+                        out = buf.as_strided((rows, heads, 8), (*st, 1), 100 - 100 % 8 + shift)
+                        meet = np.intersect1d(at, at + shift).size > 0
+                        seen[meet] += 1
+                        if meet:
+                            with pytest.raises(V.V4Error, match="overlap"):
+                                V.v4_rope(x, pos[:rows], f, out)
+                            continue
+                        want = torch.empty(rows, heads, 8, dtype=torch.bfloat16, device="cuda")
+                        V.v4_rope(x.clone(memory_format=torch.contiguous_format), pos[:rows], f, want)
+                        V.v4_rope(x, pos[:rows], f, out)
+                        assert torch.equal(out, want), (rows, heads, st, shift)
+    assert min(seen) > 100
