@@ -474,7 +474,7 @@ v4_status v4_cache_append(const void* x, int64_t rows, int32_t dim, int64_t x_ro
  *   node_begin  : [B+1] int32, ascending, node_begin[B] <= n_rows <= 2^24.
  *                 Rows before the first sequence and behind the last are
  *                 padding.
- *   seq_len     : [B] int32 >= 0.
+ *   seq_len     : [B] int32 in [0, 2^31 - 1 - V4_TREE_MAX_NODES].
  *   parent      : [n_rows] int32, the parent's node number within the
  *                 sequence, -1 = a child of the last committed token; NULL =
  *                 every sequence's nodes form a chain.
@@ -490,8 +490,9 @@ v4_status v4_cache_append(const void* x, int64_t rows, int32_t dim, int64_t x_ro
  * Bad values are flagged (V4_ERR_BAD_INDEX in the device status): a node
  * whose parent is not an earlier node is treated as a child of the last
  * committed token; a sequence with a bad range, more than V4_TREE_MAX_NODES
- * nodes or a negative length becomes padding; a slot outside the table or
- * the cache becomes -1.
+ * nodes or a length out of range becomes padding; a slot outside the table or
+ * the cache becomes -1.  Where node_begin descends, rows that two sequences
+ * then claim hold the plan of one of them or words of both.
  * After acceptance the caller appends the accepted nodes' rows again at the
  * slots of tokens seq_len[b], seq_len[b] + 1, ...
  * --------------------------------------------------------------------*/
@@ -523,7 +524,7 @@ typedef struct v4_tree_inputs {
  * (position t, sequence b, committed length L):
  *   - entries s < min((t+1)/r, ent_len[b]): every one (K = 0), or those of
  *     idx[i] (-1 = unused slot; other values outside that range are skipped
- *     and flagged);
+ *     and flagged; an entry that is named twice counts twice);
  *   - committed tokens u < L with t - W < u <= t (W = -1: all u <= t);
  *   - the nodes j of its bits with 0 <= t - t_j < W (W = -1: any t_j <= t),
  *     read from token row L + j of the cache.
@@ -539,6 +540,12 @@ typedef struct v4_tree_inputs {
  *          anything.  q_begin must be 0.
  *   o    : [n_rows, H, D] out, must not overlap q.
  *   lse  : [n_rows, H] fp32 out, nullable.
+ * idx and the entries' cache are the caller's: v4_indexer_topk selects for the
+ * rows of whole, equally long sequences and v4_compress makes the entries of
+ * whole sequences; neither takes a plan.
+ * Logits, sums and lse are fp32 on both paths.  Probabilities are rounded to
+ * bf16 on the tensor-core path, as in v4_sparse_mqa_fwd, and fp32 on CUDA
+ * cores (path = V4_PATH_SIMT, 15 to 200 times as long at 64 heads).
  * Tensor-core path: bf16, H a multiple of 64 up to 512, D = 512, R = 64;
  * every other shape runs on CUDA cores.  It counts tiles of 128 keys in 32
  * bits: n_rows * H/64 * (longest key list that the tables allow / 128 + 2)

@@ -7,10 +7,10 @@
 // it in units of eight elements: a thread's loads are all in flight, as raw
 // bits (most units of a partly rotated head are copies and are never
 // converted), while the block forms the tile's (row, pair) angles once in
-// shared memory for all heads.  4096 rows of 64 heads of 512 in bf16 take 82.0 us
-// (6.5 TB/s), the gradient of 5003 rows of 64 heads of 128 in fp32 52.0 us
-// (6.3 TB/s), 16384 cache rows 8.3 us (4.1 TB/s, nearly 2 us of it the launch),
-// one decode step of 16 rows 1.9 us.
+// shared memory for all heads.  4096 rows of 64 heads of 512 in bf16 take 81.6 us
+// (6.6 TB/s), the gradient of 5003 rows of 64 heads of 128 in fp32 52.2 us
+// (6.3 TB/s), 16384 cache rows 8.4 us (4.0 TB/s, nearly 2 us of it the launch),
+// one decode step of 16 rows 1.8 us on the device (7 from one Python call to the next).
 #include <math.h>
 
 #include "common.cuh"
@@ -196,7 +196,7 @@ cudaError_t launch_rope(const RopeCall& c, int* status, cudaStream_t st) {
   // the tiles would not give every SM one.
   const long long all = c.rows * c.heads * p.units;
   int want = kRopeThreads * (c.dtype == V4_F32 && by_half ? rope_units<float, true>() : rope_units<bf16, false>());
-  while (want > kRopeThreads && all / want < 304) want /= 2;
+  while (want > kRopeThreads && all / want < 304) want /= 2;      // two for each of 152 SMs
   const int per_row = c.heads * p.units;
   p.hb = per_row <= want ? c.heads : (want / p.units > 1 ? want / p.units : 1);
   long long rb = p.hb == c.heads ? want / per_row : 1;

@@ -23,7 +23,7 @@ namespace {
 // nearest path members (itself among them) and points 2^s up, so seven
 // rounds cover 128 nodes, against a walk of up to 127 dependent steps.
 // Block B marks the rows of no sequence.  A few kilobytes in and out: the launch
-// bounds it (1.4 us for one node, 2.1 for 32 trees of 8, 9.4 for 256 of 128).
+// bounds it (1.3 us for one node, 1.8 for 32 trees of 8, 10 for 256 of 128).
 // ---------------------------------------------------------------------------
 struct PlanArgs {
   const int32_t *node_begin, *seq_len, *parent, *table;

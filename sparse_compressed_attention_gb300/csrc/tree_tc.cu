@@ -14,7 +14,10 @@
 //
 // Per tile (one block, M = 128 keys or dims, N = 64 heads):
 //   S^T[key, head]  = K_tile . Q^T             (K = 512, + 64 for q's low part)
-//   P^T             = exp2(S^T c - m_head), bf16
+//   P^T             = exp2(S^T c - m_head), rounded to bf16 like the keys that it
+//                     multiplies: two terms would be 32 more products of 100 a tile.
+//                     The output's error grows from 1.0 to at most 1.3 roundings of
+//                     a bf16 output (selected trees 0.0017 -> 0.0021 relative)
 //   O^T[dim, head] += K_tile^T . P^T           (4 x M = 128 dims)
 // The rotated 64 dims of q are kept as two bf16 terms (high and low), so the
 // logits, and with them lse, carry no rounding of the rotation; it costs 4
@@ -30,19 +33,23 @@
 // nothing a mask hides is ever read), warps 4-11 softmax and output (two per
 // TMEM lane quarter, 32 heads each).
 //
-// What bounds it.  A tile is 128 KB and a block's shared memory takes in 71 GB/s
-// at best (bulk copies alone, from one block or from all of them), so a tile
-// costs 1.85 us to fill.  Only one fits beside the query rows: its slots are
-// released pair by pair by the O products and filled again meanwhile, but nothing
-// is filled during the softmax, which makes 2.9 us a tile.  The CUDA-core
-// kernel's times are in brackets:
-//   1 row, 512 selected entries + window        16.2 us   [246]
-//   32 x up to 8 nodes, selected                52 us     [2196]
-//   8 x 8 nodes over 7812 entries each          103 us    [9681]
-//   16 rows over all of up to 49152 tokens      92 us     [19127]
-//   4 x 16 nodes over 32768 tokens              363 us    [40543], 35% tensor pipe
-// About 5 us of each are the shares, the look-ups and the first tile, 4 to 12 the
-// joined parts.  Tried and not faster: 16 softmax warps, another split of the
+// What bounds it.  A block takes a tile in 2.8 us when the keys come out of L2,
+// in boxes or gathered (rows of 16 to 32 tiles, one to a block).  1.8 us of it are
+// the 68 products, 54.3 cycles each at N = 64; the softmax lies between the S and
+// the O products of the same tile, and only one tile fits beside the query rows,
+// so its slots are filled again as the O products release them.  Where all 152
+// blocks read keys of their own, 128 KB a tile meet HBM: 2.9 us a tile in boxes
+// (6.8 TB/s, the copy rate), 4.1 gathered.  Beside the tiles a block pays 12 us
+// for its first piece (launch, shares, look-ups, first tile, output, the empty
+// join), 4 for each further one, and a call in which rows are cut 9 for parts
+// and join.  The CUDA-core kernel's times are in brackets, tiles are a block's:
+//   1 row, 512 selected entries + window        16 us     [246]     1 tile
+//   32 x up to 8 nodes, selected                51 us     [2196]    7
+//   8 x 8 nodes over 7812 entries each          99 us     [9681]    27
+//   16 rows over all of up to 49152 tokens      91 us     [19127]   20
+//   4 x 16 nodes over 32768 tokens              358 us    [40543]   109, 35% tensor pipe
+// (the last reads 134 MB of keys, more than L2 holds: one sequence with 64 nodes
+// takes 323).  Tried and not faster: 16 softmax warps, another split of the
 // registers, the softmax in paired fp32 operations or with its exponentials ahead
 // of the vote, TMEM allocated before the shares, rows asked two tiles ahead.
 #include <cuda.h>
@@ -878,7 +885,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
 // eight heads), a warp for each head with 16 dims a lane.  One in more than
 // kJoinSerial parts has as many blocks behind its first that own nothing else:
 // the first eight of them take one head each, a warp every eighth part, and add
-// up in shared memory: one row over 131072 tokens, 152 parts, takes 62 us in both
+// up in shared memory: one row over 131072 tokens, 147 parts, takes 62 us in both
 // kernels, 100 with a block for eight heads of any item; 16 ragged rows over all
 // their tokens 92 against 95.  Eight parts is where the two ways cross (four: 94).
 // Launched while the attention kernel drains (programmatic dependence) and

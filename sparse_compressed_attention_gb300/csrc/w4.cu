@@ -23,8 +23,8 @@ __host__ __device__ constexpr int w4_nibble(int k) {
 
 // One thread packs one output's 128 inputs (threads of a warp take
 // consecutive outputs, so each row of w is read in whole lines).  Run once for
-// a weight: 70 us for 1024 x 32768 (1.2 TB/s; bound by the latency of the two
-// passes over a group's inputs).
+// a weight, and left simple: 67 us for 1024 x 32768 (1.3 TB/s, floor 12.4; bound by
+// the latency of two-byte loads and of the two passes over a group's inputs).
 __global__ void __launch_bounds__(128)
 w4_pack_kernel(const bf16* __restrict__ w, int K, int N, int gs, uint32_t* __restrict__ codes,
                bf16* __restrict__ scales) {
@@ -88,8 +88,8 @@ w4_pack_kernel(const bf16* __restrict__ w, int K, int N, int gs, uint32_t* __res
 // 2 us of it a launch, about 1 the cluster's exchange).
 //
 // More rows (w4_rows_kernel): there the rows of x, read again for every 16
-// outputs, are the larger traffic (24 rows: eight times the codes; 18 us for
-// 8 x 4096 x 1024 with the kernel above, 12.0 with this one).  Eight warps share
+// outputs, are the larger traffic (24 rows: six times the codes; 18 us for
+// 8 x 4096 x 1024 with the kernel above, 12.1 with this one, 12.7 with the codes in HBM).  Eight warps share
 // each 128-input block of x through a ring of stages in shared memory, one
 // block barrier a stage; rows lie 256 bytes apart with the halves of odd rows
 // exchanged, so that a fragment read touches every bank once.  The issue slots
@@ -101,7 +101,7 @@ w4_pack_kernel(const bf16* __restrict__ w, int K, int N, int gs, uint32_t* __res
 // squares through distributed shared memory.
 // ---------------------------------------------------------------------------
 constexpr int kMaxCluster = 8;
-constexpr int kDepth = 2;                    // blocks in flight, a power of two (four: 1 to 9% slower, less L1)
+constexpr int kDepth = 2;                    // blocks in flight, a power of two (see w4_few_kernel)
 constexpr uint32_t kStageBytes = 1024;       // codes of 16 outputs x 128 inputs
 
 struct W4Args {
@@ -184,9 +184,10 @@ __device__ __forceinline__ W4Part w4_part(const W4Args& p, int tokens) {
   // What the kernels before may have written (x; codes and scales, behind a
   // packing) is read by ordinary loads behind this wait: the read-only path wants
   // memory that nothing writes while the kernel lives, and it lives before the wait.
-  // The next kernel's blocks may come at once, but clusters that come early keep
-  // the running one's from being placed: those wait for the sums (1024 x 32768
-  // with a norm of 512: 10.1 us at once, 8.0 before the exchange, 8.7 after it).
+  // The next kernel's blocks may come at once; those of clusters when the sums are
+  // done, before the exchange, since clusters that come early can keep the running
+  // ones from being placed (clusters of eight blocks: 10.1 us at once for 1024 x 32768
+  // with a norm of 512, 8.0 before the exchange; of four, as now: 7.4 and 7.4, 7.6 after it).
   wait_previous();
   if (p.norm_dim <= (1 << p.log_rows)) start_next();
   q.warp = threadIdx.x >> 5;
@@ -324,7 +325,10 @@ __device__ __forceinline__ void w4_fold(float (&acc)[NT][4], const float (&part)
   }
 }
 
-// Up to eight rows.  kFold chunks of 32 inputs in a scale group.
+// Up to eight rows.  kFold chunks of 32 inputs in a scale group.  Two blocks of
+// codes in flight: with four, one row of 1024 x 32768 takes 8.6 us instead of 8.2 with
+// the norm and 8.5 instead of 8.3 without (codes in HBM; in L2 7.4 and 7.4, 7.6 and
+// 7.3), 8192 x 1024 4.4 instead of 4.3, but 8 x 4096 x 1024 8.4 instead of 9.4.
 template <int kFold>
 __global__ void __launch_bounds__(512) w4_few_kernel(const W4Args p) {
   typedef typename ScaleWord<kFold>::type Scales;
@@ -525,17 +529,17 @@ cudaError_t w4_few(const W4Args& p, cudaStream_t st) {
   static OncePerDevice once;
   const int nkb = p.K / 128;
   const long long tiles = (long long)p.N / 16 * p.groups;             // warps without a split of the inputs
-  // split the inputs until about twelve warps an SM stream codes, each with a
-  // few blocks to itself (up to 16 of them for 16 outputs: 8192 x 1024 7.1 us split
-  // in four, 4.5 in 16).  With a norm a split in four takes an SM for each block; of
-  // clusters of eight such blocks 12 run at once, 16 do not (1024 x 8192 with a
-  // norm of 512: 7.4 us in four, 5.3 in two; 1024 x 4096: 4.2 and 5.3).
+  // split the inputs until about twelve warps an SM (1824 on 152 SMs) stream codes,
+  // each with a few blocks to itself (up to 16 of them for 16 outputs: 8192 x 1024
+  // 5.7 us split in four, 4.4 in 16).  With a norm a split in four takes an SM for
+  // each block; of clusters of eight such blocks 12 run at once, 16 do not (1024 x
+  // 8192 with a norm of 512: 6.8 us in four, 5.0 in two; 1024 x 4096: 3.8 and 5.0).
   const int most_ks = p.norm_dim == 0 ? 16 : p.norm_dim > 256 && tiles > 4 * 96 ? 2 : 4;
   int ks = 1;
   while (ks < most_ks && tiles * ks < 1824 && nkb >= 4 * ks) ks *= 2;
   // without a norm a block is four warps; with one it takes 64 outputs, or 128
   // where the norm covers them and the block stays within 16 warps: smaller clusters
-  // (1024 x 32768 with a norm of 512: 8.3 us in clusters of eight, 7.6 of four)
+  // (1024 x 32768 with a norm of 512: 8.3 us in clusters of eight, 7.4 of four)
   const int wide = p.norm_dim >= 128 && ks <= 2 ? 8 : 4;
   const int cta_rows = 16 * (p.norm_dim > 0 ? wide : (ks < 4 ? 4 / ks : 1));
   const int warps = ks * (cta_rows / 16);
@@ -557,7 +561,7 @@ template <int NT, int kFold>
 cudaError_t w4_rows(const W4Args& p, cudaStream_t st) {
   const int nkb = p.K / 128;
   // A block takes 128 outputs; fewer, with the inputs split, while there are
-  // not two blocks for each SM (or N is an odd number of 64): two warps on a
+  // not one and a half blocks for each of 152 SMs (or N is an odd number of 64): two warps on a
   // scheduler leave it idle two cycles of three (8 x 4096 x 1024, 24 rows:
   // 13.9 us split in two, 12.5 in four).  The norm needs 64 outputs a block and
   // more than 32 rows of x the room of two stages.
