@@ -493,7 +493,7 @@ v4_status v4_cache_append(const void* x, int64_t rows, int32_t dim, int64_t x_ro
  * nodes or a length out of range becomes padding; a slot outside the table or
  * the cache becomes -1.  Where node_begin descends, rows that two sequences
  * then claim hold the plan of one of them or words of both.
- * After acceptance the caller appends the accepted nodes' rows again at the
+ * After acceptance v4_pages_compact moves the accepted nodes' rows to the
  * slots of tokens seq_len[b], seq_len[b] + 1, ...
  * --------------------------------------------------------------------*/
 #define V4_TREE_MAX_NODES 128
@@ -590,6 +590,163 @@ v4_status v4_w4_proj(const void* x, int64_t rows, int32_t groups, int32_t K, int
                      int32_t group_size, const uint8_t* codes, const void* scales,
                      int32_t norm_dim, float eps, const float* norm_w, void* y, void* stream);
 
+/* ----------------------------------------------------------------------
+ * RMS norm of each query and key head and the position rotation in one pass
+ * (no counterpart of its own on the pages: [PR] items 1 and 2 norm and rotate
+ * latents and entries, [BLOG] "The DeepSeek-V4-Flash architecture" norms the
+ * queries of each head).
+ *
+ *   u = x / sqrt(mean(x^2) + eps),  out = R(pos[t]) (w * u)
+ * over each head of dim values, R the rotation of v4_rope (mscale 1) on dims
+ * [rope_begin, rope_begin + rope_dim).  Queries and keys are two parts of one
+ * launch with their own head counts and weights; k may be NULL.  rope_dim = 0
+ * leaves the rotation out (pos and inv_freq are then not read).
+ *
+ * v4_norm_rope_bwd: with g = R(-pos) dy and r = u / x,
+ *   dw = sum over rows and heads of g * u (fp32),
+ *   out = dx = r (w g - u mean(w g u)),
+ * from x and dy alone.  (Where x was broadcast over heads or rows, the caller
+ * sums dx over the broadcast axis.)  rows = 0 is valid: dw becomes zero.
+ *
+ *   x, dy, out : element (t, h, c) at t * row_stride + h * head_stride + c, in
+ *                elements; strides >= 0, multiples of 16 bytes.  An output may
+ *                be an input of its own part with the same strides (in place);
+ *                outputs that meet themselves, each other or any other input
+ *                are refused.  Views of one fused projection may be mixed as
+ *                long as their row strides are equal.
+ *   w          : [dim] fp32, NULL = ones.
+ *   dw         : [dim] fp32 out, NULL = not wanted.
+ * dim a multiple of 8 up to 1024 (above: V4_ERR_UNSUPPORTED); rows times heads
+ * up to 2^30; rope_dim, rope_begin, layout, dtype and angles as v4_rope.
+ * Squares, sums and products are fp32, results are rounded once.  A head of
+ * zeros with eps = 0 becomes NaN.  Sums of dw have a fixed order: results repeat
+ * bit for bit on the same device.  Workspace of the gradient:
+ * v4_norm_rope_workspace_size(dim) bytes, 256-byte aligned, one for each of the
+ * calls that may overlap.
+ * --------------------------------------------------------------------*/
+typedef struct v4_norm_rope_part {
+  const void* x;
+  const float* w;            /* nullable */
+  const void* dy;            /* v4_norm_rope_bwd alone */
+  void* out;                 /* y, or dx */
+  float* dw;                 /* v4_norm_rope_bwd alone, nullable */
+  int64_t x_row_stride, x_head_stride, dy_row_stride, dy_head_stride, out_row_stride, out_head_stride;
+  int32_t heads;
+} v4_norm_rope_part;
+v4_status v4_norm_rope_fwd(const v4_norm_rope_part* q, const v4_norm_rope_part* k, int64_t rows,
+                           int32_t dim, const int32_t* pos, const float* inv_freq, int32_t rope_dim,
+                           int32_t rope_begin, int32_t layout, float eps, int32_t dtype, void* stream);
+v4_status v4_norm_rope_workspace_size(int32_t dim, size_t* bytes);
+v4_status v4_norm_rope_bwd(const v4_norm_rope_part* q, const v4_norm_rope_part* k, int64_t rows,
+                           int32_t dim, const int32_t* pos, const float* inv_freq, int32_t rope_dim,
+                           int32_t rope_begin, int32_t layout, float eps, int32_t dtype,
+                           void* workspace, size_t ws_bytes, void* stream);
+
+/* ----------------------------------------------------------------------
+ * A cache held in 4 bits: v4_cache_append and v4_tree_mqa_fwd for rows of
+ * 9/16 byte a value.
+ *
+ * A row of dim values (a multiple of 32) has v4_q4_row_bytes(dim) bytes: dim/2
+ * bytes of codes, dim/16 scale bytes, zeros up to a multiple of 16.
+ *   value[i] = (code[i] - 8) * scale[i / 16],
+ *   scale = 2^(e - 20) * (1 + m / 8) of the byte 8 e + m.
+ * The little-endian 32-bit word i of the codes holds values 8 i .. 8 i + 7, from
+ * its lowest nibble in the order 0, 2, 4, 6, 1, 3, 5, 7 (as v4_w4_pack's words).
+ * Every value is exact in bf16.
+ *
+ * v4_cache_append_q4 stores row t of x at row slot[t] of the cache, as it is
+ * (v4_norm_rope_fwd and v4_rope rotate): scale = max|x| / 7 over 16 values,
+ * rounded to the nearest scale (ties to even; at least 2^-20, at most 3840),
+ * code = 8 + clamp(round_to_even(x / scale), -8, 7).  Infinities take the
+ * largest scale and code; NaN is stored as zero.
+ * v4_cache_read_q4 makes dense rows of it, exactly: the rows that
+ * v4_sparse_mqa_fwd and v4_sparse_mqa_bwd take, for instance.  A slot of -1
+ * reads zeros.
+ *   x, out : [rows, dim], rows a stride apart (elements, a multiple of 16
+ *            bytes); out's rows must not overlap.  rows up to 2^24.
+ *   slot   : [rows] int32 as v4_cache_append's: -1 = none; others outside the
+ *            cache are skipped (read: zeros) and flagged.  Written slots must
+ *            be distinct.
+ *   cache  : [n_slots, row bytes], must not overlap x or out.
+ * --------------------------------------------------------------------*/
+v4_status v4_q4_row_bytes(int32_t dim, int32_t* bytes);
+v4_status v4_cache_append_q4(const void* x, int64_t rows, int32_t dim, int64_t x_row_stride,
+                             const int32_t* slot, int64_t n_slots, int32_t dtype, void* cache,
+                             void* stream);
+v4_status v4_cache_read_q4(const void* cache, int64_t n_slots, const int32_t* slot, int64_t rows,
+                           int32_t dim, int32_t dtype, void* out, int64_t out_row_stride, void* stream);
+
+/* ----------------------------------------------------------------------
+ * v4_tree_mqa_fwd over 4-bit caches: tok_cache and ent_cache hold rows of
+ * v4_q4_row_bytes(D) bytes, everything else (keys, masks, sinks, padding, bad
+ * indices, workspace, dtype of q and o, shapes of either path) is
+ * v4_tree_mqa_fwd's.  The values of the rows are exact in bf16, so on the same
+ * values both give the same sums but for their order.
+ * --------------------------------------------------------------------*/
+v4_status v4_tree_mqa_fwd_q4(const v4_config* cfg, const v4_tree_inputs* in, void* o, float* lse,
+                             void* workspace, size_t ws_bytes, void* stream);
+
+/* ----------------------------------------------------------------------
+ * Pages of a cache.  A block table [n, blocks] int32 names the page of each
+ * block of page_size tokens of a sequence (-1: none), as everywhere here;
+ * ref [pages] int32 counts the table entries that hold each page, and a page
+ * with ref 0 is free.  The lowest free pages are given first, in the order of
+ * sequences and blocks, so tables and counts depend on the inputs alone.
+ * Tables and counts live on the device and nothing is synchronised; one page
+ * number serves the caches of all layers.  Calls that change the same counts
+ * must follow each other (one stream, or events).
+ *
+ * v4_pages_alloc gives sequence i a page for every entry -1 among the blocks
+ *   that tokens have[i] .. need[i] - 1 need beyond those of the first have[i]
+ *   tokens (blocks ceil(have / page_size) .. ceil(need / page_size) - 1; have
+ *   NULL = 0).  Entries that hold a page keep it.
+ * v4_pages_fork makes out_table[i] a copy of the first len[i] tokens of
+ *   sequence src[i] of `table` (src -1: an empty row): whole blocks are shared
+ *   (their counts rise), a partly filled last block gets a free page, and
+ *   copies[i] = (its page, the new page, its rows), else (-1, -1, 0).  All other
+ *   entries become -1: what out_table held before is overwritten, not released.
+ *   The tables must not overlap.  An entry -1 of `table` stays one.
+ * v4_pages_free releases the entries of sequence i whose blocks hold no token
+ *   in [lo[i], hi[i]) (lo NULL = 0; hi NULL: all of them): they become -1 and
+ *   their pages' counts fall.
+ * v4_pages_copy copies the first copies[i][2] rows of page copies[i][0] to page
+ *   copies[i][1] in each layer.  A target may be named once and must be no
+ *   source.
+ * v4_pages_compact moves rows base[i] + keep[i][j] of sequence i to rows
+ *   base[i] + j (j < count[i]) in each layer: accepted nodes of a drafted tree
+ *   (base = seq_len, keep = their node numbers), or the tokens that are left
+ *   when others are given up.  keep[i] ascends; the pages written must be in
+ *   one table row alone.
+ *
+ *   lack     : int32 out, nullable: entries that got no page for want of free
+ *              ones (they stay -1).  NULL: a lack is flagged instead.
+ *   cache    : layers of [pages, page_size, row_bytes], layer_stride bytes
+ *              apart; row_bytes a multiple of 16, any contents (dense or 4-bit
+ *              rows).
+ * At most 8192 sequences for v4_pages_alloc and v4_pages_fork (else
+ * V4_ERR_UNSUPPORTED).  Bad values are flagged (V4_ERR_BAD_INDEX in the device
+ * status) and touch nothing: a length that the table does not hold or a source
+ * outside it (that row gets nothing), a page outside the pool (taken for -1), a
+ * release of a page that is free, a copy outside the pool, a kept row that is
+ * not above the one before or not held (it is not moved).
+ * --------------------------------------------------------------------*/
+v4_status v4_pages_alloc(int32_t n, int32_t* table, int32_t blocks, int32_t page_size,
+                         const int32_t* have, const int32_t* need, int32_t* ref, int32_t pages,
+                         int32_t* lack, void* stream);
+v4_status v4_pages_fork(int32_t batch, const int32_t* table, int32_t blocks, int32_t n,
+                        const int32_t* src, const int32_t* len, int32_t* out_table,
+                        int32_t out_blocks, int32_t page_size, int32_t* ref, int32_t pages,
+                        int32_t* copies, int32_t* lack, void* stream);
+v4_status v4_pages_free(int32_t n, int32_t* table, int32_t blocks, int32_t page_size,
+                        const int32_t* lo, const int32_t* hi, int32_t* ref, int32_t pages, void* stream);
+v4_status v4_pages_copy(void* cache, int32_t layers, int64_t layer_stride, int32_t pages,
+                        int32_t page_size, int32_t row_bytes, const int32_t* copies, int32_t n,
+                        void* stream);
+v4_status v4_pages_compact(void* cache, int32_t layers, int64_t layer_stride, int32_t pages,
+                           int32_t page_size, int32_t row_bytes, int32_t n, const int32_t* table,
+                           int32_t blocks, const int32_t* base, const int32_t* count,
+                           const int32_t* keep, int32_t max_keep, void* stream);
+
 /* Text of the last non-OK status returned on this host thread ("" if none). */
 const char* v4_last_error(void);
 
@@ -630,7 +787,9 @@ v4_status v4_selftest_wait_timeout(int32_t limit_us, void* stream);
  * quantisation of the indexer operands, 11 query projections, 12 indexer
  * distillation target, 13 rotary positions, 14 paged cache write, 15 tree
  * plan, 16 tree attention, 17 join of split tree attention, 18 4-bit
- * packing, 19 4-bit projection.
+ * packing, 19 4-bit projection, 20 norms with the rotation, 21 their gradient,
+ * 22 4-bit cache write, 23 4-bit cache read, 24 pages given, forked or released,
+ * 25 page copies, 26 compaction.
  * --------------------------------------------------------------------*/
 v4_status v4_profile_enable(int32_t on);
 int32_t v4_profile_count(void);

@@ -32,11 +32,15 @@ EXPORTS = ["v4_rope_inv_freq", "v4_workspace_size", "v4_compress", "v4_indexer_p
            "v4_bwd_workspace_size", "v4_sparse_mqa_bwd", "v4_quantize_e4m3", "v4_indexer_topk_e4m3",
            "v4_q_proj", "v4_indexer_kl_target", "v4_selftest_wait_timeout", "v4_build_info",
            "v4_rope", "v4_cache_append", "v4_tree_plan", "v4_tree_workspace_size", "v4_tree_mqa_fwd",
-           "v4_w4_pack", "v4_w4_proj"]
+           "v4_w4_pack", "v4_w4_proj", "v4_norm_rope_fwd", "v4_norm_rope_workspace_size", "v4_norm_rope_bwd",
+           "v4_q4_row_bytes", "v4_cache_append_q4", "v4_cache_read_q4", "v4_tree_mqa_fwd_q4", "v4_pages_alloc",
+           "v4_pages_fork", "v4_pages_free", "v4_pages_copy", "v4_pages_compact"]
 PROFILE_KINDS = {0: "compress", 1: "window_rotate", 2: "indexer_prep", 3: "indexer_scores", 4: "topk",
                  5: "attention", 6: "o_proj", 7: "bwd_prep", 8: "bwd_attention", 9: "bwd_derotate",
                  10: "indexer_quant", 11: "q_proj", 12: "kl_target", 13: "rope", 14: "cache_append",
-                 15: "tree_plan", 16: "tree_attention", 17: "tree_join", 18: "w4_pack", 19: "w4_proj"}
+                 15: "tree_plan", 16: "tree_attention", 17: "tree_join", 18: "w4_pack", 19: "w4_proj",
+                 20: "norm_rope", 21: "norm_rope_bwd", 22: "cache_append_q4", 23: "cache_read_q4", 24: "pages",
+                 25: "pages_copy", 26: "pages_compact"}
 
 
 class V4Error(RuntimeError):
@@ -63,6 +67,12 @@ class v4_layer_outputs(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in ("o", "lse", "ent", "ikey", "idx", "iscore", "y")]
 
 
+class v4_norm_rope_part(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("x", "w", "dy", "out", "dw")] + [
+        (n, C.c_int64) for n in ("x_row_stride", "x_head_stride", "dy_row_stride", "dy_head_stride", "out_row_stride",
+                                 "out_head_stride")] + [("heads", C.c_int32)]
+
+
 class v4_tree_inputs(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in (
         "q", "plan", "tok_cache", "tok_table", "ent_cache", "ent_table", "ent_len", "idx", "sink", "inv_freq")] + [
@@ -86,7 +96,7 @@ def lib(path=None):
                            "sparse_compressed_attention_gb300.build.build()" % path)
     L = C.CDLL(path)
     vp, i32, i64, f32, sz = C.c_void_p, C.c_int32, C.c_int64, C.c_float, C.c_size_t
-    cfgp = C.POINTER(v4_config)
+    cfgp, partp = C.POINTER(v4_config), C.POINTER(v4_norm_rope_part)
     sig = {
         "v4_rope_inv_freq": [f32, i32, f32, i32, f32, f32, vp],
         "v4_workspace_size": [cfgp, C.POINTER(sz)],
@@ -114,6 +124,18 @@ def lib(path=None):
         "v4_tree_workspace_size": [cfgp, i32, C.POINTER(sz)],
         "v4_tree_mqa_fwd": [cfgp, C.POINTER(v4_tree_inputs), vp, vp, vp, sz, vp],
         "v4_w4_pack": [vp, i32, i32, i32, i32, vp, vp, vp],
+        "v4_norm_rope_fwd": [partp, partp, i64, i32, vp, vp, i32, i32, i32, f32, i32, vp],
+        "v4_norm_rope_workspace_size": [i32, C.POINTER(sz)],
+        "v4_norm_rope_bwd": [partp, partp, i64, i32, vp, vp, i32, i32, i32, f32, i32, vp, sz, vp],
+        "v4_q4_row_bytes": [i32, C.POINTER(i32)],
+        "v4_cache_append_q4": [vp, i64, i32, i64, vp, i64, i32, vp, vp],
+        "v4_cache_read_q4": [vp, i64, vp, i64, i32, i32, vp, i64, vp],
+        "v4_tree_mqa_fwd_q4": [cfgp, C.POINTER(v4_tree_inputs), vp, vp, vp, sz, vp],
+        "v4_pages_alloc": [i32, vp, i32, i32, vp, vp, vp, i32, vp, vp],
+        "v4_pages_fork": [i32, vp, i32, i32, vp, vp, vp, i32, i32, vp, i32, vp, vp, vp],
+        "v4_pages_free": [i32, vp, i32, i32, vp, vp, vp, i32, vp],
+        "v4_pages_copy": [vp, i32, i64, i32, i32, i32, vp, i32, vp],
+        "v4_pages_compact": [vp, i32, i64, i32, i32, i32, i32, vp, i32, vp, vp, vp, i32, vp],
         "v4_w4_proj": [vp, i64, i32, i32, i32, i32, vp, vp, i32, f32, vp, vp, vp],
     }
     for name, args in sig.items():
@@ -488,7 +510,7 @@ def alloc_tree_workspace(cfg, n_rows, device=None):
 
 
 def _paged(cache, table, kind, D, B, dt, dev):
-    """Cache pointer, table pointer, slots, blocks, page size of one paged cache."""
+    """Cache pointer, table pointer, slots, blocks, page size of one paged cache whose rows have D elements of dt."""
     try:
         pages, page, width = cache.shape
         blocks = table.shape[1]
@@ -510,6 +532,16 @@ def v4_tree_mqa_fwd(cfg, inputs, o, lse, workspace, stream=None):
     """Attention of planned rows over paged caches.  inputs: a dict keyed like v4_tree_inputs' pointers, with
     tok_cache / ent_cache [pages, page_size, D] and tok_table / ent_table [B, blocks].  workspace may be None where
     v4_tree_workspace_size is 0."""
+    return _tree_fwd(lib().v4_tree_mqa_fwd, cfg.head_dim, _storage(cfg), cfg, inputs, o, lse, workspace, stream)
+
+
+def v4_tree_mqa_fwd_q4(cfg, inputs, o, lse, workspace, stream=None):
+    """v4_tree_mqa_fwd over 4-bit caches: tok_cache / ent_cache [pages, page_size, v4_q4_row_bytes(D)] uint8."""
+    return _tree_fwd(lib().v4_tree_mqa_fwd_q4, _q4_width(cfg.head_dim), torch.uint8, cfg, inputs, o, lse, workspace, stream)
+
+
+def _tree_fwd(call, width, ct, cfg, inputs, o, lse, workspace, stream):
+    """width, ct: elements and type of a cache row."""
     i32, f32 = torch.int32, torch.float32
     get = inputs.get
     q, sink = inputs["q"], get("sink")
@@ -520,9 +552,9 @@ def v4_tree_mqa_fwd(cfg, inputs, o, lse, workspace, stream=None):
     tc = tt = ec = et = el = ix = None
     ts = tb = tp = es = eb = ep = 0
     if cfg.window:
-        tc, tt, ts, tb, tp = _paged(get("tok_cache"), get("tok_table"), "tok", D, B, dt, dev)
+        tc, tt, ts, tb, tp = _paged(get("tok_cache"), get("tok_table"), "tok", width, B, ct, dev)
     if r > 0:
-        ec, et, es, eb, ep = _paged(get("ent_cache"), get("ent_table"), "ent", D, B, dt, dev)
+        ec, et, es, eb, ep = _paged(get("ent_cache"), get("ent_table"), "ent", width, B, ct, dev)
         el = _shaped(get("ent_len"), "ent_len", (B,), i32, dev)
         if K > 0:
             ix = _shaped(get("idx"), "idx", (n, K), i32, dev)
@@ -531,10 +563,9 @@ def v4_tree_mqa_fwd(cfg, inputs, o, lse, workspace, stream=None):
         None if sink is None else _shaped(sink, "sink", (H,), f32, dev),
         _shaped(get("inv_freq"), "inv_freq", (half,), f32, dev) if half else None, ts, es, n, tb, tp, eb, ep)
     size = 0 if workspace is None else workspace.numel()
-    st = lib().v4_tree_mqa_fwd(cfg, vin, _shaped(o, "o", shape, dt, dev),
-                               None if lse is None else _shaped(lse, "lse", (n, H), f32, dev),
-                               None if workspace is None else _shaped(workspace, "workspace", (size,), torch.uint8, dev),
-                               size, _stream_on(stream, dev))
+    st = call(cfg, vin, _shaped(o, "o", shape, dt, dev), None if lse is None else _shaped(lse, "lse", (n, H), f32, dev),
+              None if workspace is None else _shaped(workspace, "workspace", (size,), torch.uint8, dev), size,
+              _stream_on(stream, dev))
     if st:
         _check(st)
     return o
@@ -570,6 +601,210 @@ def v4_w4_proj(x, codes, scales, y, norm_dim=0, eps=1e-6, norm_w=None, stream=No
                             _shaped(norm_w, "norm_w", (norm_dim,), torch.float32, dev) if norm_w is not None and norm_dim
                             else None, py, _stream_on(stream, dev)))
     return y
+
+
+def _norm_part(dev, name, x, out, w, dy, dw):
+    """One part's struct; dy None: forward."""
+    px, sx = _strided(x, name, 3, dev)
+    po, so = _strided(out, name + "'s output", 3, dev)
+    shape, dt = x.shape, x.dtype
+    if out.shape != shape or out.dtype is not dt:
+        raise ValueError("%s's output must have its shape and type" % name)
+    pg, sg = None, (0, 0)
+    if dy is not None:
+        pg, sg = _strided(dy, name + "'s output gradient", 3, dev)
+        if dy.shape != shape or dy.dtype is not dt:
+            raise ValueError("%s's output gradient must have its shape and type" % name)
+    return v4_norm_rope_part(
+        px, None if w is None else _shaped(w, name + "_w", shape[2:], torch.float32, dev), pg, po,
+        None if dw is None else _shaped(dw, "d" + name + "_w", shape[2:], torch.float32, dev), sx[0], sx[1], sg[0], sg[1],
+        so[0], so[1], shape[1])
+
+
+def _norm_common(q, k, pos, inv_freq, rope_begin, dev):
+    rows, _, dim = q.shape
+    if k is not None and (k.dim() != 3 or k.shape[0] != rows or k.shape[2] != dim or k.dtype is not q.dtype):
+        raise ValueError("k must be [%d, heads, %d] of q's type" % (rows, dim))
+    half = 0 if inv_freq is None else inv_freq.numel()
+    pp = _shaped(pos, "pos", (rows,), torch.int32, dev) if half and rows else None
+    pf = _shaped(inv_freq, "inv_freq", (half,), torch.float32, dev) if half else None
+    return rows, dim, pp, pf, 2 * half, dim - 2 * half if rope_begin is None else rope_begin
+
+
+def v4_norm_rope_fwd(q, k, pos, inv_freq, q_out, k_out=None, q_w=None, k_w=None, eps=1e-6, rope_begin=None,
+                     layout=V4_ROPE_INTERLEAVED, stream=None):
+    """RMS norm (weights q_w, k_w [dim] fp32, None: ones) of every head of q [rows, heads, dim] and k [rows, heads, dim]
+    or None, rotated at pos [rows] on dims [rope_begin, rope_begin + R), into q_out and k_out (or in place).
+
+    R = 2 * len(inv_freq) (None: no rotation); rope_begin defaults to the last R dims."""
+    dev = _current(q, "q")
+    pq = _norm_part(dev, "q", q, q_out, q_w, None, None)
+    pk = None if k is None else _norm_part(dev, "k", k, k_out, k_w, None, None)
+    rows, dim, pp, pf, R, begin = _norm_common(q, k, pos, inv_freq, rope_begin, dev)
+    if rows:
+        _check(lib().v4_norm_rope_fwd(pq, pk, rows, dim, pp, pf, R, begin, layout, eps, _STORAGE_CODE[q.dtype],
+                                      _stream_on(stream, dev)))
+    return q_out, k_out
+
+
+def v4_norm_rope_workspace_size(dim):
+    n = C.c_size_t(0)
+    _check(lib().v4_norm_rope_workspace_size(int(dim), C.byref(n)))
+    return n.value
+
+
+def alloc_norm_rope_workspace(dim, device=None):
+    return torch.empty(v4_norm_rope_workspace_size(dim), dtype=torch.uint8, device=device or "cuda")
+
+
+def v4_norm_rope_bwd(q, k, dq_out, dk_out, pos, inv_freq, dq, dk=None, q_w=None, k_w=None, dq_w=None, dk_w=None, eps=1e-6,
+                     rope_begin=None, layout=V4_ROPE_INTERLEAVED, workspace=None, stream=None):
+    """Gradients of v4_norm_rope_fwd: from its inputs and the gradients dq_out, dk_out of its outputs, dq and dk (of q's
+    type) and the weights' dq_w, dk_w [dim] fp32 (None: not wanted) are written.  workspace: alloc_norm_rope_workspace."""
+    dev = _current(q, "q")
+    _current(dq_out, "q's output gradient")
+    if k is not None:
+        _current(dk_out, "k's output gradient")
+    pq = _norm_part(dev, "q", q, dq, q_w, dq_out, dq_w)
+    pk = None if k is None else _norm_part(dev, "k", k, dk, k_w, dk_out, dk_w)
+    rows, dim, pp, pf, R, begin = _norm_common(q, k, pos, inv_freq, rope_begin, dev)
+    size = 0 if workspace is None else workspace.numel()
+    _check(lib().v4_norm_rope_bwd(pq, pk, rows, dim, pp, pf, R, begin, layout, eps, _STORAGE_CODE[q.dtype],
+                                  None if workspace is None else _shaped(workspace, "workspace", (size,), torch.uint8, dev),
+                                  size, _stream_on(stream, dev)))
+    return dq, dk, dq_w, dk_w
+
+
+def _q4_width(dim):
+    return (dim // 2 + dim // 16 + 15) // 16 * 16
+
+
+def v4_q4_row_bytes(dim):
+    """Bytes of a row of dim values in a 4-bit cache."""
+    n = C.c_int32(0)
+    _check(lib().v4_q4_row_bytes(int(dim), C.byref(n)))
+    return n.value
+
+
+def _q4_cache(cache, dim, dev):
+    """Pointer and rows of a 4-bit cache."""
+    width = _q4_width(dim)
+    if not isinstance(cache, torch.Tensor) or cache.dim() < 2 or cache.shape[-1] != width:
+        raise ValueError("cache must be a tensor [..., %d] for rows of %d values" % (width, dim))
+    return _shaped(cache, "cache", cache.shape, torch.uint8, dev), cache.numel() // width
+
+
+def v4_cache_append_q4(x, slot, cache, stream=None):
+    """Store rows x [rows, dim], as they are, in 4 bits at rows slot of cache [..., v4_q4_row_bytes(dim)] uint8."""
+    dev = _current(x, "x")
+    px, sx = _strided(x, "x", 2, dev)
+    rows, dim = x.shape
+    pc, n = _q4_cache(cache, dim, dev)
+    if rows:
+        _check(lib().v4_cache_append_q4(px, rows, dim, sx[0], _shaped(slot, "slot", (rows,), torch.int32, dev), n,
+                                        _STORAGE_CODE[x.dtype], pc, _stream_on(stream, dev)))
+    return cache
+
+
+def v4_cache_read_q4(cache, slot, out, stream=None):
+    """Rows slot of a 4-bit cache as dense rows out [rows, dim] (bf16 or fp32, both exact); zeros for slot -1."""
+    dev = _current(out, "out")
+    po, so = _strided(out, "out", 2, dev)
+    rows, dim = out.shape
+    pc, n = _q4_cache(cache, dim, dev)
+    if rows:
+        _check(lib().v4_cache_read_q4(pc, n, _shaped(slot, "slot", (rows,), torch.int32, dev), rows, dim,
+                                      _STORAGE_CODE[out.dtype], po, so[0], _stream_on(stream, dev)))
+    return out
+
+
+def _table(t, name, dev):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError("%s must be a tensor [sequences, blocks]" % name)
+    return _shaped(t, name, t.shape, torch.int32, dev), t.shape[0], t.shape[1]
+
+
+def _pool(ref, dev):
+    if not isinstance(ref, torch.Tensor) or ref.dim() != 1:
+        raise ValueError("ref must be a tensor [pages]")
+    return _shaped(ref, "ref", ref.shape, torch.int32, dev)
+
+
+def _counted(t, name, n, dev):
+    return None if t is None else _shaped(t, name, (n,), torch.int32, dev)
+
+
+def v4_pages_alloc(table, ref, need, page_size, have=None, lack=None, stream=None):
+    """Give the entries -1 of table [n, blocks] that tokens have[i] .. need[i] - 1 want the lowest pages with ref 0;
+    lack [1] int32: entries that got none."""
+    dev = _current(table, "table")
+    pt, n, blocks = _table(table, "table", dev)
+    _check(lib().v4_pages_alloc(n, pt, blocks, int(page_size), _counted(have, "have", n, dev),
+                                _shaped(need, "need", (n,), torch.int32, dev), _pool(ref, dev),
+                                ref.numel(), _counted(lack, "lack", 1, dev), _stream_on(stream, dev)))
+    return table
+
+
+def v4_pages_fork(table, src, length, out_table, ref, page_size, copies, lack=None, stream=None):
+    """out_table[i] becomes the first length[i] tokens of sequence src[i] of table: whole pages shared, a partly filled last
+    one replaced by a free page, named with its rows in copies [n, 3] for v4_pages_copy."""
+    dev = _current(table, "table")
+    pt, B, blocks = _table(table, "table", dev)
+    po, n, out_blocks = _table(out_table, "out_table", dev)
+    i32 = torch.int32
+    _check(lib().v4_pages_fork(B, pt, blocks, n, _shaped(src, "src", (n,), i32, dev), _shaped(length, "length", (n,), i32, dev),
+                               po, out_blocks, int(page_size), _pool(ref, dev), ref.numel(),
+                               _shaped(copies, "copies", (n, 3), i32, dev), _counted(lack, "lack", 1, dev),
+                               _stream_on(stream, dev)))
+    return out_table
+
+
+def v4_pages_free(table, ref, page_size, lo=None, hi=None, stream=None):
+    """Release the entries of table [n, blocks] whose blocks hold no token in [lo[i], hi[i]) (hi None: all of them)."""
+    dev = _current(table, "table")
+    pt, n, blocks = _table(table, "table", dev)
+    _check(lib().v4_pages_free(n, pt, blocks, int(page_size), _counted(lo, "lo", n, dev), _counted(hi, "hi", n, dev),
+                               _pool(ref, dev), ref.numel(), _stream_on(stream, dev)))
+    return table
+
+
+def _layers(cache):
+    """Pointer, layers, layer stride in bytes, pages, page size, row bytes of a cache [(layers,) pages, page_size, width]."""
+    dev = _current(cache, "cache")
+    if cache.get_device() != dev:
+        raise ValueError("cache is on %s, the current device is cuda:%d" % (cache.device, dev))
+    if cache.dim() not in (3, 4):
+        raise ValueError("cache must be a tensor [layers, pages, page_size, width] or [pages, page_size, width]")
+    pages, page, width = cache.shape[-3:]
+    st, es = cache.stride(), cache.element_size()
+    if st[-1] != 1 and width > 1 or st[-2] != width and page > 1 or st[-3] != page * width and pages > 1:
+        raise ValueError("cache must be dense in its last three dims")
+    layers = cache.shape[0] if cache.dim() == 4 else 1
+    return dev, cache.data_ptr(), layers, st[0] * es if cache.dim() == 4 else 0, pages, page, width * es
+
+
+def v4_pages_copy(cache, copies, stream=None):
+    """Rows of pages as copies [n, 3] (source, target, rows) says, in every layer of cache."""
+    dev, pc, layers, stride, pages, page, row = _layers(cache)
+    if not isinstance(copies, torch.Tensor) or copies.dim() != 2:
+        raise ValueError("copies must be a tensor [n, 3]")
+    n = copies.shape[0]
+    _check(lib().v4_pages_copy(pc, layers, stride, pages, page, row, _shaped(copies, "copies", (n, 3), torch.int32, dev), n,
+                               _stream_on(stream, dev)))
+    return cache
+
+
+def v4_pages_compact(cache, table, base, count, keep, stream=None):
+    """Rows base[i] + keep[i, j] of sequence i of table move to rows base[i] + j, j < count[i], in every layer of cache."""
+    dev, pc, layers, stride, pages, page, row = _layers(cache)
+    pt, n, blocks = _table(table, "table", dev)
+    if not isinstance(keep, torch.Tensor) or keep.dim() != 2:
+        raise ValueError("keep must be a tensor [sequences, rows]")
+    width, i32 = keep.shape[1], torch.int32
+    _check(lib().v4_pages_compact(pc, layers, stride, pages, page, row, n, pt, blocks, _shaped(base, "base", (n,), i32, dev),
+                                  _shaped(count, "count", (n,), i32, dev), _shaped(keep, "keep", (n, width), i32, dev), width,
+                                  _stream_on(stream, dev)))
+    return cache
 
 
 def v4_last_error():

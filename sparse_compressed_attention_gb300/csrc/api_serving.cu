@@ -3,90 +3,12 @@
 #include <math.h>
 #include <stdio.h>
 
+#include "checks.h"
 #include "common.cuh"
 #include "internal.h"
 #include "tree.cuh"
 
 namespace v4 {
-
-static v4_status bad(const char* what) { return set_error(V4_ERR_INVALID_ARG, what); }
-
-static v4_status cuda_result(cudaError_t e, const char* what) {
-  if (e == cudaSuccess) return V4_OK;
-  char buf[256];
-  snprintf(buf, sizeof(buf), "%s: %s", what, cudaGetErrorString(e));
-  return set_error(V4_ERR_CUDA, buf);
-}
-
-static v4_status check_ptr(const void* p, const char* name, bool required = true) {
-  char buf[128];
-  if (!p) {
-    if (!required) return V4_OK;
-    snprintf(buf, sizeof(buf), "%s is NULL", name);
-    return bad(buf);
-  }
-  if ((uintptr_t)p & 15u) {
-    snprintf(buf, sizeof(buf), "%s is not 16-byte aligned", name);
-    return bad(buf);
-  }
-  return V4_OK;
-}
-
-#define TRY(expr)                     \
-  do {                                \
-    const v4_status s_ = (expr);      \
-    if (s_ != V4_OK) return s_;       \
-  } while (0)
-
-static v4_status check_rotation(int64_t rows, int32_t dim, int32_t rope_dim, int32_t rope_begin, int32_t layout,
-                                int32_t dtype) {
-  if (dtype != V4_F32 && dtype != V4_BF16) return bad("unknown dtype");
-  if (layout != V4_ROPE_INTERLEAVED && layout != V4_ROPE_HALF) return bad("unknown rotation layout");
-  if (rows < 0) return bad("rows must be >= 0");
-  if (rows > 0x7FFFFFFF) return bad("rows above 2^31 - 1");
-  if (dim < 8 || dim > 8192 || dim % 8) return bad("dim must be a multiple of 8 in [8, 8192]");
-  if (rope_dim < 0 || rope_dim > 1024 || rope_dim % (layout == V4_ROPE_HALF ? 16 : 8))
-    return bad("rope_dim must be a multiple of 8 (16 for the half layout) in [0, 1024]");
-  if (rope_begin < 0 || rope_begin % 8 || rope_begin > dim - rope_dim)
-    return bad("rope_begin must be a multiple of 8 with rope_begin + rope_dim <= dim");
-  return V4_OK;
-}
-
-// Bytes from the first to behind the last element of a strided tensor.
-static int64_t extent(int64_t rows, int64_t heads, int64_t dim, int64_t rs, int64_t hs, int es) {
-  return ((rows - 1) * rs + (heads - 1) * hs + dim) * es;
-}
-
-static bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
-  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-  return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
-}
-
-// Whether a view of no x ni runs of dim elements (nested: the inner runs of one outer
-// step end before the next) and the same view moved by `shift` elements have an
-// element in common: some difference of outer and inner steps brings a run within
-// dim of another.  The outer difference is one of the two around shift / so, since
-// what is left is smaller than so, the inner one likewise.
-static bool views_meet(int64_t shift, int64_t no, int64_t so, int64_t ni, int64_t si, int64_t dim) {
-  const int64_t moved = shift < 0 ? -shift : shift;                // the other way round it is the same
-  const int64_t o0 = no > 1 ? moved / so : 0;
-  for (int64_t o = o0; o <= o0 + 1 && o < no; ++o) {
-    const int64_t rest = moved - o * so < 0 ? o * so - moved : moved - o * so;
-    const int64_t i0 = ni > 1 ? rest / si : 0;
-    for (int64_t i = i0; i <= i0 + 1 && i < ni; ++i)
-      if (rest - i * si < dim && i * si - rest < dim) return true;
-  }
-  return false;
-}
-
-static v4_status check_stride(int64_t s, int es, const char* name) {
-  char buf[128];
-  if (s < 0 || s > (int64_t)1 << 40 || (s * es) % 16) {
-    snprintf(buf, sizeof(buf), "%s must be a multiple of 16 bytes in [0, 2^40]", name);
-    return bad(buf);
-  }
-  return V4_OK;
-}
 
 // Rows of a call: far above what memory holds, low enough for 32-bit row loops.
 constexpr int32_t kMaxRows = 1 << 24;
@@ -254,14 +176,14 @@ v4_status v4_tree_workspace_size(const v4_config* cfg, int32_t n_rows, size_t* b
   return V4_OK;
 }
 
-v4_status v4_tree_mqa_fwd(const v4_config* cfg, const v4_tree_inputs* in, void* o, float* lse, void* workspace,
-                          size_t ws_bytes, void* stream) {
+static v4_status tree_fwd(const v4_config* cfg, const v4_tree_inputs* in, bool q4, void* o, float* lse,
+                          void* workspace, size_t ws_bytes, void* stream) {
   v4_config c;
   TRY(tree_config(cfg, &c));
   if (!in) return bad("inputs struct is NULL");
   if (cfg->q_begin != 0) return set_error(V4_ERR_UNSUPPORTED, "the tree attention needs q_begin = 0");
   TRY(check_rows(in->n_rows));
-  const bool tc = tree_on_tc(c);
+  const bool tc = tree_on_tc(c) && !q4;
   if (c.path == V4_PATH_TC && !tc)
     return set_error(V4_ERR_UNSUPPORTED, "tensor-core tree attention needs bf16, H a multiple of 64 up to 512, D=512, R=64");
   if (in->n_rows == 0) return V4_OK;
@@ -337,7 +259,18 @@ v4_status v4_tree_mqa_fwd(const v4_config* cfg, const v4_tree_inputs* in, void* 
   a.K = c.ratio > 0 ? c.topk : 0;
   a.scale = c.softmax_scale > 0.f ? c.softmax_scale : 1.0f / sqrtf((float)c.head_dim);
   cudaStream_t st = (cudaStream_t)stream;
-  return cuda_result(tc ? launch_tree_tc(a, workspace, st) : launch_tree_simt(a, c.dtype, st), "tree attention kernel");
+  return cuda_result(tc ? launch_tree_tc(a, workspace, st) : launch_tree_simt(a, c.dtype, q4, st),
+                     "tree attention kernel");
+}
+
+v4_status v4_tree_mqa_fwd(const v4_config* cfg, const v4_tree_inputs* in, void* o, float* lse, void* workspace,
+                          size_t ws_bytes, void* stream) {
+  return tree_fwd(cfg, in, false, o, lse, workspace, ws_bytes, stream);
+}
+
+v4_status v4_tree_mqa_fwd_q4(const v4_config* cfg, const v4_tree_inputs* in, void* o, float* lse, void* workspace,
+                             size_t ws_bytes, void* stream) {
+  return tree_fwd(cfg, in, true, o, lse, workspace, ws_bytes, stream);
 }
 
 static v4_status check_w4(int32_t groups, int32_t K, int32_t N, int32_t group_size) {

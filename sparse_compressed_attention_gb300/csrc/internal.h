@@ -221,12 +221,62 @@ struct RopeCall {
 };
 cudaError_t launch_rope(const RopeCall& c, int* status, cudaStream_t st);
 
+// ---- norms of queries and keys with the rotation (norm.cu)
+struct NormPartCall {
+  const void* x;                // null: no such heads
+  const void* dy;               // gradient
+  const float* w;               // null: ones
+  void* out;                    // y, or dx
+  float* dw;                    // gradient, null: not wanted
+  int heads;
+  long long x_row_stride, x_head_stride, dy_row_stride, dy_head_stride, out_row_stride, out_head_stride;
+};
+struct NormCall {
+  NormPartCall part[2];         // queries, keys
+  const int32_t* pos;
+  const float* inv_freq;
+  void* workspace;              // gradient: norm_rope_workspace(dim) bytes
+  long long rows;
+  int dim, rope_dim, rope_begin, dtype;
+  bool half, grad;
+  float eps;
+};
+size_t norm_rope_workspace(int dim);
+cudaError_t launch_norm_rope(const NormCall& c, cudaStream_t st);
+
+// ---- rows of the 4-bit cache (cache4.cu)
+struct Q4Call {
+  const void* x;                // write
+  void* out;                    // read; null: write
+  void* cache;
+  const int32_t* slot;
+  long long n_slots, rows, row_stride;
+  int dim, dtype;
+};
+cudaError_t launch_q4_rows(const Q4Call& c, int* status, cudaStream_t st);
+
+// ---- pages of a cache (pages.cu)
+int pages_max_sequences();      // of one v4_pages_alloc or v4_pages_fork
+cudaError_t launch_pages_alloc(int n, int32_t* table, int blocks, int page, const int32_t* have, const int32_t* need,
+                               int32_t* ref, int pages, int32_t* lack, int* status, cudaStream_t st);
+cudaError_t launch_pages_fork(int B, const int32_t* table, int blocks, int n, const int32_t* src, const int32_t* len,
+                              int32_t* out, int out_blocks, int page, int32_t* ref, int pages, int32_t* copies,
+                              int32_t* lack, int* status, cudaStream_t st);
+cudaError_t launch_pages_free(int n, int32_t* table, int blocks, int page, const int32_t* lo, const int32_t* hi,
+                              int32_t* ref, int pages, int* status, cudaStream_t st);
+cudaError_t launch_pages_copy(void* cache, int layers, long long layer_bytes, int pages, int page, int row_bytes,
+                              const int32_t* copies, int n, int* status, cudaStream_t st);
+cudaError_t launch_pages_compact(void* cache, int layers, long long layer_bytes, int pages, int page, int row_bytes,
+                                 int n, const int32_t* table, int blocks, const int32_t* base, const int32_t* count,
+                                 const int32_t* keep, int width, int* status, cudaStream_t st);
+
 // ---- drafted token trees (tree.cu, tree_tc.cu)
 struct TreeArgs;
 cudaError_t launch_tree_plan(int B, int n_rows, const int32_t* node_begin, const int32_t* seq_len,
                              const int32_t* parent, const int32_t* table, int max_blocks, int page, long long n_slots,
                              int32_t* plan, int32_t* pos, int32_t* slot, int* status, cudaStream_t st);
-cudaError_t launch_tree_simt(const TreeArgs& a, int dtype, cudaStream_t st);
+// q4: the caches hold 4-bit rows
+cudaError_t launch_tree_simt(const TreeArgs& a, int dtype, bool q4, cudaStream_t st);
 
 // ---- 4-bit projections (w4.cu)
 cudaError_t launch_w4_pack(const void* w, int groups, int K, int N, int gs, uint8_t* codes, void* scales,

@@ -1,0 +1,520 @@
+// Pages of a cache: giving, sharing (fork), releasing them, copying rows of one
+// page to another and moving kept rows together (v4_pages_*).
+//
+// ref[p] counts the table entries that hold page p; a page with ref 0 is free, and
+// the lowest free pages are given first, so a call's result depends on its inputs
+// alone.  Counts change by integer atomics, whose order changes nothing.
+#include "common.cuh"
+#include "fastdiv.cuh"
+#include "internal.h"
+
+namespace v4 {
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// Giving pages.  One block: a warp counts the entries that a sequence wants, a
+// block scan numbers them, the block walks ref from page 0 and lists free pages
+// (kList at a time), and the warps hand them out in order.
+// ---------------------------------------------------------------------------
+constexpr int kGiveThreads = 1024, kGiveWarps = kGiveThreads / 32;
+constexpr int kMaxSeqs = 8192;                   // sequences of a call
+constexpr int kList = 8192;
+
+struct GiveShared {
+  int before[kMaxSeqs + 1];                      // wanted entries of the sequences before
+  int list[kList];
+  int warp_sum[kGiveWarps];
+};
+
+// Exclusive sum of v over the block's threads; the total of all in *total.
+__device__ __forceinline__ int block_scan(int v, GiveShared* sh, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += u;
+  }
+  __syncthreads();
+  if (lane == 31) sh->warp_sum[warp] = s;
+  __syncthreads();
+  int w = sh->warp_sum[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += u;
+  }
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  const int before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+  return s - v + (warp > 0 ? before : 0);
+}
+
+// count(i): entries that sequence i wants (a whole warp asks, every lane gets it).
+// give(i, first, lo, hi, list): hand list[r - lo] to the wanted entries number r in
+// [lo, hi), the first entry not yet served having number `first`.
+template <typename Count, typename Give>
+__device__ void give_pages(int n, int* ref, int pages, int* lack, int* status, GiveShared* sh, Count count, Give give) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int i = warp; i < n; i += kGiveWarps) {
+    const int c = count(i);
+    if (lane == 0) sh->before[i] = c;
+  }
+  __syncthreads();
+  int total = 0;
+  for (int i0 = 0; i0 < n; i0 += kGiveThreads) {
+    const int i = i0 + (int)threadIdx.x;
+    const int c = i < n ? sh->before[i] : 0;
+    int all;
+    const int at = total + block_scan(c, sh, &all);
+    if (i < n) sh->before[i] = at;
+    total += all;
+  }
+  if (threadIdx.x == 0) sh->before[n] = total;
+  __syncthreads();
+  int given = 0;                                 // numbers below have their page
+  int chunk = 0;                                 // first page of the next chunk
+  while (given < total) {
+    const int want = min(kList, total - given);
+    int found = 0;
+    while (found < want && chunk < pages) {
+      const int p0 = chunk + 4 * (int)threadIdx.x;
+      int4 r = make_int4(1, 1, 1, 1);
+      if (p0 + 3 < pages) {
+        r = *reinterpret_cast<const int4*>(ref + p0);
+      } else if (p0 < pages) {
+        r.x = ref[p0];
+        if (p0 + 1 < pages) r.y = ref[p0 + 1];
+        if (p0 + 2 < pages) r.z = ref[p0 + 2];
+      }
+      const int f[4] = {r.x == 0, r.y == 0, r.z == 0, r.w == 0};
+      int all;
+      int at = found + block_scan(f[0] + f[1] + f[2] + f[3], sh, &all);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (f[e] && at < want) sh->list[at] = p0 + e;
+        at += f[e];
+      }
+      found += all;
+      if (found <= want) chunk += 4 * kGiveThreads;       // else some of it is left for the next list
+    }
+    found = min(found, want);
+    __syncthreads();
+    if (found == 0) break;
+    for (int i = warp; i < n; i += kGiveWarps) {
+      const int lo = sh->before[i], hi = sh->before[i + 1];
+      if (max(lo, given) < min(hi, given + found)) give(i, max(lo, given), given, given + found, sh->list);
+    }
+    given += found;
+    __syncthreads();                             // the given pages' counts are seen by the next walk
+  }
+  if (threadIdx.x == 0) {
+    if (lack) *lack = total - given;
+    else if (given < total) set_status(status, kStatusBadIndex);
+  }
+}
+
+struct AllocArgs {
+  int32_t* table;
+  const int32_t *have, *need;
+  int32_t *ref, *lack;
+  int* status;
+  int n, blocks, page, pages;
+};
+
+__global__ void __launch_bounds__(kGiveThreads) pages_alloc_kernel(const AllocArgs p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  GiveShared* sh = reinterpret_cast<GiveShared*>(smem);
+  after_previous();
+  const int lane = threadIdx.x & 31;
+  // blocks [lo, hi) of a sequence
+  auto range = [&](int i, int* lo, int* hi) {
+    const long long have = p.have ? p.have[i] : 0, need = p.need[i];
+    *lo = *hi = 0;
+    if (have < 0 || need < 0 || (need + p.page - 1) / p.page > p.blocks) {
+      set_status(p.status, kStatusBadIndex);
+      return;
+    }
+    *lo = (int)min((have + p.page - 1) / p.page, (long long)p.blocks);
+    *hi = (int)((need + p.page - 1) / p.page);
+  };
+  give_pages(
+      p.n, p.ref, p.pages, p.lack, p.status, sh,
+      [&](int i) {
+        int lo, hi, c = 0;
+        range(i, &lo, &hi);
+        for (int k = lo; k < hi; k += 32)
+          c += __popc(__ballot_sync(0xffffffffu, k + lane < hi && p.table[(size_t)i * p.blocks + k + lane] == -1));
+        return c;
+      },
+      [&](int i, int first, int from, int to, const int* list) {
+        int lo, hi;
+        range(i, &lo, &hi);
+        for (int k = lo; k < hi && first < to; k += 32) {
+          int32_t* at = p.table + (size_t)i * p.blocks + k + lane;
+          const bool want = k + lane < hi && *at == -1;
+          const uint32_t vote = __ballot_sync(0xffffffffu, want);
+          const int r = first + __popc(vote & ((1u << lane) - 1u));
+          if (want && r < to) {
+            const int pg = list[r - from];
+            *at = pg;
+            p.ref[pg] = 1;
+          }
+          first += __popc(vote);
+        }
+      });
+}
+
+// ---------------------------------------------------------------------------
+// Fork.  Block 0 gives the partly filled last pages a free page each, the others
+// share the whole ones.
+// ---------------------------------------------------------------------------
+constexpr int kForkThreads = kGiveThreads;
+
+struct ForkArgs {
+  const int32_t *table, *src, *len;
+  int32_t *out, *ref, *copies, *lack;
+  int* status;
+  long long items;                               // n * out_blocks
+  int B, blocks, n, out_blocks, page, pages;
+  FastDiv by_out;
+};
+
+// Whole blocks and rows of the last of beam i; false: nothing is shared.
+__device__ __forceinline__ bool fork_row(const ForkArgs& p, int i, int* src, int* full, int* rest) {
+  const int s = p.src[i], L = p.len[i];
+  *src = s;
+  *full = *rest = 0;
+  if (s == -1) return false;
+  const long long used = ((long long)L + p.page - 1) / p.page;
+  if (s < 0 || s >= p.B || L < 0 || used > p.blocks || used > p.out_blocks) {
+    set_status(p.status, kStatusBadIndex);
+    return false;
+  }
+  *full = L / p.page;
+  *rest = L - *full * p.page;
+  return true;
+}
+
+__device__ __forceinline__ int fork_page(const ForkArgs& p, int src, int k) {
+  const int pg = p.table[(size_t)src * p.blocks + k];
+  if (pg >= -1 && pg < p.pages) return pg;
+  set_status(p.status, kStatusBadIndex);
+  return -1;
+}
+
+__global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(const ForkArgs p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  GiveShared* sh = reinterpret_cast<GiveShared*>(smem);
+  after_previous();
+  const int lane = threadIdx.x & 31;
+  if (blockIdx.x == 0) {
+    auto last = [&](int i, int* full, int* rest) {       // page of the partly filled block, -1: none
+      int src;
+      return fork_row(p, i, &src, full, rest) && *rest > 0 ? fork_page(p, src, *full) : -1;
+    };
+    for (int i = threadIdx.x; i < 3 * p.n; i += kForkThreads) p.copies[i] = i % 3 == 2 ? 0 : -1;
+    for (int i = threadIdx.x; i < p.n; i += kForkThreads) {
+      int full, rest, src;
+      if (fork_row(p, i, &src, &full, &rest) && rest > 0) p.out[(size_t)i * p.out_blocks + full] = -1;
+    }
+    __syncthreads();
+    give_pages(
+        p.n, p.ref, p.pages, p.lack, p.status, sh,
+        [&](int i) {
+          int full, rest;
+          return last(i, &full, &rest) >= 0 ? 1 : 0;
+        },
+        [&](int i, int first, int from, int, const int* list) {
+          if (lane != 0) return;
+          int full, rest;
+          const int old = last(i, &full, &rest), pg = list[first - from];
+          p.out[(size_t)i * p.out_blocks + full] = pg;
+          p.ref[pg] = 1;
+          p.copies[3 * i] = old;
+          p.copies[3 * i + 1] = pg;
+          p.copies[3 * i + 2] = rest;
+        });
+    return;
+  }
+  for (long long j = (long long)(blockIdx.x - 1) * kForkThreads + threadIdx.x; j < p.items;
+       j += (long long)(gridDim.x - 1) * kForkThreads) {
+    const int i = (int)p.by_out.div((uint32_t)j), k = (int)(j - (long long)i * p.out_blocks);
+    int src, full, rest, pg = -1;
+    const bool live = fork_row(p, i, &src, &full, &rest);
+    if (live && k == full && rest > 0) continue;         // block 0's
+    if (live && k < full) {
+      pg = fork_page(p, src, k);
+      if (pg >= 0 && atomicAdd(p.ref + pg, 1) <= 0) set_status(p.status, kStatusBadIndex);
+    }
+    p.out[j] = pg;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Release: entries whose block holds no token in [lo, hi).
+// ---------------------------------------------------------------------------
+struct FreeArgs {
+  int32_t *table, *ref;
+  const int32_t *lo, *hi;
+  int* status;
+  long long items;
+  int blocks, page, pages;
+  FastDiv by_blocks;
+};
+
+__global__ void __launch_bounds__(256) pages_free_kernel(const FreeArgs p) {
+  after_previous();
+  const long long j = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (j >= p.items) return;
+  const int pg = p.table[j];
+  if (pg == -1) return;
+  const int i = (int)p.by_blocks.div((uint32_t)j);
+  const long long k = j - (long long)i * p.blocks;
+  const long long lo = p.lo ? p.lo[i] : 0, hi = p.hi ? p.hi[i] : 0;
+  if (k * p.page < hi && (k + 1) * p.page > lo && lo < hi) return;
+  p.table[j] = -1;
+  if (pg < 0 || pg >= p.pages) {
+    set_status(p.status, kStatusBadIndex);
+  } else if (atomicSub(p.ref + pg, 1) <= 0) {
+    atomicAdd(p.ref + pg, 1);
+    set_status(p.status, kStatusBadIndex);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Copies of rows from one page to another, in 16-byte words: a block takes 16 KB
+// of a pair in one layer.
+// ---------------------------------------------------------------------------
+constexpr int kCopyThreads = 256, kCopyWords = 4;
+
+struct CopyArgs {
+  uint4* cache;
+  const int32_t* copies;
+  int* status;
+  long long layer_words, page_words;
+  int row_words, pages, page, chunks;
+  FastDiv by_chunks;
+};
+
+__global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const CopyArgs p) {
+  after_previous();
+  const int pair = (int)p.by_chunks.div(blockIdx.x), chunk = (int)blockIdx.x - pair * p.chunks;
+  const int from = p.copies[3 * pair], to = p.copies[3 * pair + 1], rows = p.copies[3 * pair + 2];
+  if (rows == 0 || (from == -1 && to == -1)) return;
+  if (from < 0 || from >= p.pages || to < 0 || to >= p.pages || rows < 0 || rows > p.page) {
+    set_status(p.status, kStatusBadIndex);
+    return;
+  }
+  if (from == to) return;
+  const int n = rows * p.row_words;
+  const uint4* a = p.cache + blockIdx.y * p.layer_words + from * p.page_words;
+  uint4* b = p.cache + blockIdx.y * p.layer_words + to * p.page_words;
+  uint4 v[kCopyWords];
+  const int i0 = chunk * (kCopyThreads * kCopyWords) + (int)threadIdx.x;
+#pragma unroll
+  for (int k = 0; k < kCopyWords; ++k)
+    if (i0 + k * kCopyThreads < n) v[k] = a[i0 + k * kCopyThreads];
+#pragma unroll
+  for (int k = 0; k < kCopyWords; ++k)
+    if (i0 + k * kCopyThreads < n) b[i0 + k * kCopyThreads] = v[k];
+}
+
+// ---------------------------------------------------------------------------
+// Kept rows move together: row base + keep[i] to row base + i.  keep ascends, so a
+// row never moves up, and rows are independent in every 16-byte column: a block
+// takes a strip of columns of one sequence and layer and walks its rows in order.
+// A round's rows are read before the barrier and written behind it; what a round
+// writes lies below everything that later rounds read.
+// ---------------------------------------------------------------------------
+constexpr int kKeepThreads = 256, kKeepRows = 4;   // words a thread has in flight
+
+struct KeepArgs {
+  uint4* cache;
+  const int32_t *table, *base, *count, *keep;
+  int* status;
+  long long layer_words;
+  int blocks, page, pages, width, row_words, strip, lg_strip;
+  FastDiv by_page;
+};
+
+__global__ void __launch_bounds__(kKeepThreads) pages_keep_kernel(const KeepArgs p) {
+  after_previous();
+  const int b = blockIdx.x;
+  const int n = p.count[b], base = p.base[b];
+  if (n < 0 || n > p.width || base < 0) {
+    if (threadIdx.x == 0) set_status(p.status, kStatusBadIndex);
+    return;
+  }
+  const int col = blockIdx.y * p.strip + (int)(threadIdx.x & (p.strip - 1)), r0 = threadIdx.x >> p.lg_strip;
+  const int rows = kKeepThreads >> p.lg_strip;   // rows of a round, kKeepRows times
+  const int32_t* keep = p.keep + (size_t)b * p.width;
+  const int32_t* table = p.table + (size_t)b * p.blocks;
+  uint4* cache = p.cache + blockIdx.z * p.layer_words + col;
+  auto place = [&](long long at) -> long long {          // first word of a logical row, -1: not held
+    const uint32_t blk = at < 0x7FFFFFFF ? p.by_page.div((uint32_t)at) : 0x7FFFFFFFu;
+    const int pg = blk < (uint32_t)p.blocks ? table[blk] : -1;
+    if (pg < 0 || pg >= p.pages) {
+      set_status(p.status, kStatusBadIndex);
+      return -1;
+    }
+    return ((long long)pg * p.page + (int)(at - (long long)blk * p.page)) * p.row_words;
+  };
+  for (int i0 = 0; i0 < n; i0 += rows * kKeepRows) {
+    uint4 v[kKeepRows];
+    long long to[kKeepRows];
+#pragma unroll
+    for (int k = 0; k < kKeepRows; ++k) {
+      const int i = i0 + k * rows + r0;
+      to[k] = -1;
+      if (i >= n || col >= p.row_words) continue;
+      const int s = keep[i];
+      if (s < i || (i > 0 && keep[i - 1] >= s)) {
+        set_status(p.status, kStatusBadIndex);
+        continue;
+      }
+      if (s == i) continue;
+      const long long from = place((long long)base + s), at = place((long long)base + i);
+      if (from < 0 || at < 0) continue;
+      v[k] = cache[from];
+      to[k] = at;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kKeepRows; ++k)
+      if (to[k] >= 0) cache[to[k]] = v[k];
+  }
+}
+
+cudaError_t give_shared(void (*kern)(const AllocArgs), void (*fork)(const ForkArgs)) {
+  static OncePerDevice once;
+  return once.run([&] {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(GiveShared));
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(fork, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(GiveShared));
+  });
+}
+
+}  // namespace
+
+int pages_max_sequences() { return kMaxSeqs; }
+
+cudaError_t launch_pages_alloc(int n, int32_t* table, int blocks, int page, const int32_t* have, const int32_t* need,
+                               int32_t* ref, int pages, int32_t* lack, int* status, cudaStream_t st) {
+  cudaError_t e = give_shared(pages_alloc_kernel, pages_fork_kernel);
+  if (e != cudaSuccess) return e;
+  AllocArgs p;
+  p.table = table;
+  p.have = have;
+  p.need = need;
+  p.ref = ref;
+  p.lack = lack;
+  p.status = status;
+  p.n = n;
+  p.blocks = blocks;
+  p.page = page;
+  p.pages = pages;
+  e = launch_overlapped(pages_alloc_kernel, dim3(1), dim3(kGiveThreads), sizeof(GiveShared), st, p);
+  if (e == cudaSuccess) note_launch();
+  return e;
+}
+
+cudaError_t launch_pages_fork(int B, const int32_t* table, int blocks, int n, const int32_t* src, const int32_t* len,
+                              int32_t* out, int out_blocks, int page, int32_t* ref, int pages, int32_t* copies,
+                              int32_t* lack, int* status, cudaStream_t st) {
+  cudaError_t e = give_shared(pages_alloc_kernel, pages_fork_kernel);
+  if (e != cudaSuccess) return e;
+  ForkArgs p;
+  p.table = table;
+  p.src = src;
+  p.len = len;
+  p.out = out;
+  p.ref = ref;
+  p.copies = copies;
+  p.lack = lack;
+  p.status = status;
+  p.items = (long long)n * out_blocks;
+  p.B = B;
+  p.blocks = blocks;
+  p.n = n;
+  p.out_blocks = out_blocks;
+  p.page = page;
+  p.pages = pages;
+  p.by_out.set((uint32_t)out_blocks);
+  long long grid = (p.items + kForkThreads - 1) / kForkThreads;
+  if (grid > 304) grid = 304;
+  e = launch_overlapped(pages_fork_kernel, dim3((unsigned)grid + 1), dim3(kForkThreads), sizeof(GiveShared), st, p);
+  if (e == cudaSuccess) note_launch();
+  return e;
+}
+
+cudaError_t launch_pages_free(int n, int32_t* table, int blocks, int page, const int32_t* lo, const int32_t* hi,
+                              int32_t* ref, int pages, int* status, cudaStream_t st) {
+  FreeArgs p;
+  p.table = table;
+  p.ref = ref;
+  p.lo = lo;
+  p.hi = hi;
+  p.status = status;
+  p.items = (long long)n * blocks;
+  p.blocks = blocks;
+  p.page = page;
+  p.pages = pages;
+  p.by_blocks.set((uint32_t)blocks);
+  const cudaError_t e =
+      launch_overlapped(pages_free_kernel, dim3((unsigned)((p.items + 255) / 256)), dim3(256), 0, st, p);
+  if (e == cudaSuccess) note_launch();
+  return e;
+}
+
+cudaError_t launch_pages_copy(void* cache, int layers, long long layer_bytes, int pages, int page, int row_bytes,
+                              const int32_t* copies, int n, int* status, cudaStream_t st) {
+  CopyArgs p;
+  p.cache = (uint4*)cache;
+  p.copies = copies;
+  p.status = status;
+  p.layer_words = layer_bytes / 16;
+  p.row_words = row_bytes / 16;
+  p.page_words = (long long)page * p.row_words;
+  p.pages = pages;
+  p.page = page;
+  const int per = kCopyThreads * kCopyWords;
+  p.chunks = (int)((p.page_words + per - 1) / per);
+  p.by_chunks.set((uint32_t)p.chunks);
+  const cudaError_t e = launch_overlapped(pages_copy_kernel, dim3((unsigned)(n * p.chunks), (unsigned)layers),
+                                          dim3(kCopyThreads), 0, st, p);
+  if (e == cudaSuccess) note_launch();
+  return e;
+}
+
+cudaError_t launch_pages_compact(void* cache, int layers, long long layer_bytes, int pages, int page, int row_bytes,
+                                 int n, const int32_t* table, int blocks, const int32_t* base, const int32_t* count,
+                                 const int32_t* keep, int width, int* status, cudaStream_t st) {
+  KeepArgs p;
+  p.cache = (uint4*)cache;
+  p.table = table;
+  p.base = base;
+  p.count = count;
+  p.keep = keep;
+  p.status = status;
+  p.layer_words = layer_bytes / 16;
+  p.blocks = blocks;
+  p.page = page;
+  p.pages = pages;
+  p.width = width;
+  p.row_words = row_bytes / 16;
+  p.by_page.set((uint32_t)page);
+  // strips of 1 KB, narrower while there are fewer blocks than four for each SM and
+  // a strip keeps 64 bytes
+  p.lg_strip = 6;
+  while (p.lg_strip > 2 && ((1 << (p.lg_strip - 1)) >= p.row_words ||
+                            (long long)n * layers * ((p.row_words + (1 << p.lg_strip) - 1) >> p.lg_strip) < 608))
+    --p.lg_strip;
+  p.strip = 1 << p.lg_strip;
+  const dim3 grid((unsigned)n, (unsigned)((p.row_words + p.strip - 1) / p.strip), (unsigned)layers);
+  const cudaError_t e = launch_overlapped(pages_keep_kernel, grid, dim3(kKeepThreads), 0, st, p);
+  if (e == cudaSuccess) note_launch();
+  return e;
+}
+
+}  // namespace v4

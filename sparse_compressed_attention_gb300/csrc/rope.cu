@@ -14,6 +14,7 @@
 #include <math.h>
 
 #include "common.cuh"
+#include "fastdiv.cuh"
 #include "internal.h"
 #include "turn.cuh"
 
@@ -35,19 +36,6 @@ constexpr int rope_units() {
 }
 constexpr int kMaxAngles = 1024;                 // (row, pair) angles of a tile
 
-// Division by a run-time constant below 2^31: n / d for n < 2^31.
-struct FastDiv {
-  uint32_t mul, sh;
-  void set(uint32_t v) {
-    sh = 0;
-    while ((1u << sh) < v) ++sh;                 // 2^sh >= v
-    mul = (uint32_t)(((uint64_t)1 << 32) * (((uint64_t)1 << sh) - v) / v + 1);
-  }
-  __device__ __forceinline__ uint32_t div(uint32_t n) const {
-    return (uint32_t)(((uint64_t)__umulhi(mul, n) + n) >> sh);
-  }
-};
-
 struct RopeArgs {
   const void* x;
   void* out;
@@ -63,21 +51,6 @@ struct RopeArgs {
   int rot_units, units;        // units of a (row, head): rotated ones first, then copied ones
   int rb, hb;                  // rows and heads of a tile
   FastDiv by_unit, by_head, by_half;
-};
-
-// Eight elements as raw 16-byte words: one for bf16, two for float.
-template <typename T>
-struct Raw {
-  uint4 w[sizeof(T) / 2];
-  __device__ __forceinline__ void load(const T* p) {
-#pragma unroll
-    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
-  }
-  __device__ __forceinline__ void store(T* p) const {
-#pragma unroll
-    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) reinterpret_cast<uint4*>(p)[i] = w[i];
-  }
-  __device__ __forceinline__ void floats(float* v) const { load8(reinterpret_cast<const T*>(w), v); }
 };
 
 // kHalf: pairs half a rotation apart.

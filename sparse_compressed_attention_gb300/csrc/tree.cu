@@ -10,6 +10,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "q4.cuh"
 #include "tree.cuh"
 #include "turn.cuh"
 
@@ -121,14 +122,33 @@ __global__ void __launch_bounds__(V4_TREE_MAX_NODES) tree_plan_kernel(const Plan
 // ---------------------------------------------------------------------------
 constexpr int kHG = 8, kKT = 32, kSimtThreads = kHG * 32;
 
-template <typename T>
+// Rows of a cache, dense or 4-bit.
+template <typename C>
+__device__ __forceinline__ const C* cache_row(const void* cache, long long s, int D) {
+  return reinterpret_cast<const C*>(cache) + s * D;
+}
+template <>
+__device__ __forceinline__ const Q4* cache_row<Q4>(const void* cache, long long s, int D) {
+  return reinterpret_cast<const Q4*>(cache) + s * q4_row_bytes(D);
+}
+template <typename C>
+__device__ __forceinline__ void load8_key(const C* row, int c8, int, float* v) {
+  load8(row + c8, v);
+}
+__device__ __forceinline__ void load8_key(const Q4* row, int c8, int D, float* v) {
+  const uint8_t* b = reinterpret_cast<const uint8_t*>(row);
+  q4_values(*reinterpret_cast<const uint32_t*>(b + c8 / 2), q4_scale(b[D / 2 + c8 / kQ4Group]), v);
+}
+
+// T: queries and output; C: what the caches hold.
+template <typename T, typename C>
 __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const TreeArgs a) {
   extern __shared__ float sm[];
   const int D = a.D, R = a.R, ldk = D + 1;
   float* s_q = sm;                               // [kHG][D]
   float* s_k = s_q + kHG * D;                    // [kKT][D + 1]
   float* s_p = s_k + kKT * ldk;                  // [kHG][kKT]
-  __shared__ const T* s_ptr[kKT];
+  __shared__ const C* s_ptr[kKT];
   __shared__ float s_cs[2][512];
   __shared__ int s_draft[V4_TREE_MAX_NODES];
   __shared__ int s_count[V4_TREE_MAX_NODES / 32];
@@ -192,14 +212,14 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const TreeArgs 
     __syncthreads();
     if (threadIdx.x < kKT) {
       const long long j = k0 + threadIdx.x;
-      const T* p = nullptr;
+      const C* p = nullptr;
       if (j < r.ne) {
         const long long s = tree_entry_row(a, r, row, (int)j);
-        if (s >= 0) p = reinterpret_cast<const T*>(a.ent_cache) + s * D;
+        if (s >= 0) p = cache_row<C>(a.ent_cache, s, D);
       } else if (j < nk) {
         const long long at = j - r.ne < r.nw ? r.lo + (j - r.ne) : (long long)r.L + s_draft[j - r.ne - r.nw];
         const long long s = tree_token_row(a, r, at);
-        if (s >= 0) p = reinterpret_cast<const T*>(a.tok_cache) + s * D;
+        if (s >= 0) p = cache_row<C>(a.tok_cache, s, D);
       }
       s_ptr[threadIdx.x] = p;
     }
@@ -207,9 +227,9 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const TreeArgs 
     for (int i = threadIdx.x; i < kKT * (D / 8); i += kSimtThreads) {
       const int j = i / (D / 8), c8 = (i % (D / 8)) * 8;
       float v[8];
-      const T* p = s_ptr[j];
+      const C* p = s_ptr[j];
       if (p) {
-        load8(p + c8, v);
+        load8_key(p, c8, D, v);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = 0.f;
@@ -269,10 +289,10 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const TreeArgs 
   if (a.lse && lane == 0) a.lse[(size_t)row * a.H + h] = l == 0.f ? -INFINITY : m + logf(l);
 }
 
-template <typename T>
+template <typename T, typename C>
 cudaError_t tree_simt_t(const TreeArgs& a, cudaStream_t st) {
   const size_t smem = (size_t)(kHG * a.D + kKT * (a.D + 1) + kHG * kKT) * sizeof(float);
-  auto kern = tree_simt_kernel<T>;
+  auto kern = tree_simt_kernel<T, C>;
   static OncePerDevice once;
   const cudaError_t e = allow_shared(kern, once);
   if (e != cudaSuccess) return e;
@@ -307,9 +327,9 @@ cudaError_t launch_tree_plan(int B, int n_rows, const int32_t* node_begin, const
   return e;
 }
 
-cudaError_t launch_tree_simt(const TreeArgs& a, int dtype, cudaStream_t st) {
-  if (dtype == V4_BF16) return tree_simt_t<bf16>(a, st);
-  return tree_simt_t<float>(a, st);
+cudaError_t launch_tree_simt(const TreeArgs& a, int dtype, bool q4, cudaStream_t st) {
+  if (q4) return dtype == V4_BF16 ? tree_simt_t<bf16, Q4>(a, st) : tree_simt_t<float, Q4>(a, st);
+  return dtype == V4_BF16 ? tree_simt_t<bf16, bf16>(a, st) : tree_simt_t<float, float>(a, st);
 }
 
 }  // namespace v4
