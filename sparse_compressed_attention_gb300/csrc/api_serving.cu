@@ -183,7 +183,7 @@ static v4_status tree_fwd(const v4_config* cfg, const v4_tree_inputs* in, bool q
   if (!in) return bad("inputs struct is NULL");
   if (cfg->q_begin != 0) return set_error(V4_ERR_UNSUPPORTED, "the tree attention needs q_begin = 0");
   TRY(check_rows(in->n_rows));
-  const bool tc = tree_on_tc(c) && !q4;
+  const bool tc = tree_on_tc(c);
   if (c.path == V4_PATH_TC && !tc)
     return set_error(V4_ERR_UNSUPPORTED, "tensor-core tree attention needs bf16, H a multiple of 64 up to 512, D=512, R=64");
   if (in->n_rows == 0) return V4_OK;
@@ -259,7 +259,7 @@ static v4_status tree_fwd(const v4_config* cfg, const v4_tree_inputs* in, bool q
   a.K = c.ratio > 0 ? c.topk : 0;
   a.scale = c.softmax_scale > 0.f ? c.softmax_scale : 1.0f / sqrtf((float)c.head_dim);
   cudaStream_t st = (cudaStream_t)stream;
-  return cuda_result(tc ? launch_tree_tc(a, workspace, st) : launch_tree_simt(a, c.dtype, q4, st),
+  return cuda_result(tc ? launch_tree_tc(a, q4, workspace, st) : launch_tree_simt(a, c.dtype, q4, st),
                      "tree attention kernel");
 }
 

@@ -32,4 +32,21 @@ __device__ __forceinline__ void q4_values(uint32_t word, float scale, float* v) 
   }
 }
 
+// Eight values of a word as bf16 pairs, value 0 lowest.  0x4300 | n is 128 + n in
+// bf16; (128 + n) s - 136 s in one fused step is (n - 8) s, which bf16 holds, and so
+// does 136 s = 17 (8 + m) 2^k, 17 * 15 being below 2^8.
+__device__ __forceinline__ uint4 q4_word_bf16(uint32_t word, uint32_t byte) {
+  const uint32_t s = byte * 0x00100010u + 0x35803580u;           // the scale in both halves
+  const __nv_bfloat162 scale = *reinterpret_cast<const __nv_bfloat162*>(&s);
+  const __nv_bfloat162 shift = __hmul2(scale, __float2bfloat162_rn(-136.f));
+  uint32_t v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t two = ((word >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+    const __nv_bfloat162 r = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&two), scale, shift);
+    v[i] = *reinterpret_cast<const uint32_t*>(&r);
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
 }  // namespace v4

@@ -57,6 +57,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "q4.cuh"
 #include "sm100.cuh"
 #include "tree.cuh"
 #include "turn.cuh"
@@ -68,6 +69,7 @@ using namespace sm100;
 namespace {
 
 constexpr int kH = 64, kD = 512, kR = 64;
+constexpr int kQ4RowBytes = kD / 2 + kD / kQ4Group;
 constexpr int kThreads = 448;
 constexpr int kSoftThreads = 256;                 // warps 4-11
 constexpr int kSoftWarps = kSoftThreads / 32;
@@ -175,11 +177,12 @@ __device__ __forceinline__ int nth_node(const int4 w, int i) {
 }
 
 // Cache row behind position `at` of a row's key list; null where there is no key.
-__device__ __forceinline__ const bf16* key_row(const TreeArgs& a, const TreeRow& r, const int4 bits, int row,
-                                               long long at) {
+template <int kRowBytes>
+__device__ __forceinline__ const uint8_t* key_row(const TreeArgs& a, const TreeRow& r, const int4 bits, int row,
+                                                  long long at) {
   if (at < r.ne) {
     const long long s = tree_entry_row(a, r, row, (int)at);
-    return s < 0 ? nullptr : reinterpret_cast<const bf16*>(a.ent_cache) + s * kD;
+    return s < 0 ? nullptr : reinterpret_cast<const uint8_t*>(a.ent_cache) + s * kRowBytes;
   }
   at -= r.ne;
   long long u;
@@ -192,7 +195,7 @@ __device__ __forceinline__ const bf16* key_row(const TreeArgs& a, const TreeRow&
     u = (long long)r.L + j;
   }
   const long long s = tree_token_row(a, r, u);
-  return s < 0 ? nullptr : reinterpret_cast<const bf16*>(a.tok_cache) + s * kD;
+  return s < 0 ? nullptr : reinterpret_cast<const uint8_t*>(a.tok_cache) + s * kRowBytes;
 }
 
 // 16 bytes of global memory, or zeros, into shared memory.
@@ -283,6 +286,7 @@ __device__ __forceinline__ float sink_mass(float s2, float m) {
 // its tiles.  Block c of the grid takes units [c * share, (c + 1) * share).
 __device__ __forceinline__ int share_of(int total, int ctas) { return (total + ctas - 1) / ctas; }
 
+template <bool kQ4>
 __global__ void __launch_bounds__(kThreads, 1)
 tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_pages, const Args p) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -299,7 +303,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kPairs; ++i) {
-      mbar_init(&c->full_g[i], 32 * kGatherWarps);
+      mbar_init(&c->full_g[i], kQ4 ? kGatherWarps : 32 * kGatherWarps);
       mbar_init(&c->full_t[i], 1);
       mbar_init(&c->empty[i], 1);
     }
@@ -522,7 +526,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
 #pragma unroll
           for (int m = kPairs - 1; m >= 0; --m) {
             ok = ok && warp_wait(&full[m], par, c, a.status);
-            if (!dense) fence_proxy_async_smem();     // cp.async writes -> tensor-core reads
+            if (!kQ4 && !dense) fence_proxy_async_smem();     // cp.async writes -> tensor-core reads
             if (lead) {
 #pragma unroll
               for (int ks = 0; ks < 8; ++ks)
@@ -568,6 +572,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     __syncwarp();
   } else if (warp < 4 || warp >= 12) {
     // ------------------------------------------------------------ key rows
+    constexpr int kRowBytes = kQ4 ? kQ4RowBytes : kD * 2;
     const int gw = warp < 4 ? warp - 2 : warp - 10;
     const int chunk = lane & 7;
     int qc = 0, g = 0;
@@ -582,11 +587,65 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
       const int4 bits = *reinterpret_cast<const int4*>(a.plan + (size_t)pc.row * kPlanWords + 4);
       // lane i looks after key row 32 gw + i of a tile
       auto look_up = [&](int j) {
-        return key_row(a, r, bits, pc.row, (long long)(pc.tile0 + j) * kTile + 32 * gw + lane);
+        return key_row<kRowBytes>(a, r, bits, pc.row, (long long)(pc.tile0 + j) * kTile + 32 * gw + lane);
       };
-      const bf16* next = look_up(0);
+      const uint8_t* next = look_up(0);
+      if constexpr (kQ4) {
+        // A lane holds its row's codes in registers a tile ahead, unpacks a pair of
+        // K-blocks when their slots are released and asks for the next tile's.
+        const int row = 32 * gw + lane;
+        uint4 codes[16], scales[2];
+        auto load = [&](const uint8_t* from, int m) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            codes[4 * m + i] = from ? reinterpret_cast<const uint4*>(from)[4 * m + i]
+                                    : make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);   // zeros
+        };
+        auto load_scales = [&](const uint8_t* from) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            scales[i] = from ? reinterpret_cast<const uint4*>(from + kD / 2)[i] : make_uint4(0, 0, 0, 0);
+        };
+#pragma unroll
+        for (int m = 0; m < kPairs; ++m) load(next, m);
+        load_scales(next);
+        for (int j = 0; j < pc.tiles && ok; ++j) {
+          const uint32_t live = __ballot_sync(0xffffffffu, next != nullptr);
+          if (lane == 0) {
+            c->valid[g & 1][gw] = live;           // tile g - 2's bits have been read, as below
+            mbar_arrive(&c->valid_full[g & 1]);
+          }
+          const bool more = j + 1 < pc.tiles;
+          if (more) next = look_up(j + 1);
+#pragma unroll
+          for (int m = kPairs - 1; m >= 0; --m) {
+            if (g >= 1 && ok) ok = warp_wait(&c->empty[m], (g - 1) & 1, c, a.status);
+            if (ok) {
+              const uint32_t* sc = reinterpret_cast<const uint32_t*>(scales) + 2 * m;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {       // K-block 2 m + h
+                uint8_t* to = smem + OFF_SLOT + (2 * m + h) * kSlotBytes + row * 128;
+#pragma unroll
+                for (int ch = 0; ch < 8; ++ch) {  // 16-byte chunk: one word of codes
+                  const uint4 w4 = codes[4 * m + 2 * h + ch / 4];
+                  const uint32_t w = ch % 4 == 0 ? w4.x : ch % 4 == 1 ? w4.y : ch % 4 == 2 ? w4.z : w4.w;
+                  const uint32_t b = (sc[h] >> (8 * (ch / 2))) & 255u;
+                  *reinterpret_cast<uint4*>(to + ((ch ^ (row & 7)) << 4)) = q4_word_bf16(w, b);
+                }
+              }
+              fence_proxy_async_smem();
+              warp_arrive(&c->full_g[m], lane);
+            }
+            if (more) load(next, m);
+          }
+          if (more) load_scales(next);
+          ++g;
+        }
+        ++qc;
+        continue;
+      }
       for (int j = 0; j < pc.tiles && ok; ++j) {
-        const bf16* src = next;
+        const uint8_t* src = next;
         const uint32_t live = __ballot_sync(0xffffffffu, src != nullptr);
         if (lane == 0) {
           // tile g - 2's bits have been read: its O products completed before
@@ -594,10 +653,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
           c->valid[g & 1][gw] = live;
           mbar_arrive(&c->valid_full[g & 1]);
         }
-        const bf16* rows[8];
+        const uint8_t* rows[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          rows[i] = reinterpret_cast<const bf16*>(
+          rows[i] = reinterpret_cast<const uint8_t*>(
               __shfl_sync(0xffffffffu, (unsigned long long)src, 4 * i + (lane >> 3)));
         for (int m = kPairs - 1; m >= 0; --m) {
           if (g >= 1) ok = warp_wait(&c->empty[m], (g - 1) & 1, c, a.status);
@@ -608,10 +667,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
           for (int i = 0; i < 8; ++i) {
             const int row = 32 * gw + 4 * i + (lane >> 3);
             const bool key = rows[i] != nullptr;
-            const bf16* from = key ? rows[i] + m * 128 + chunk * 8 : reinterpret_cast<const bf16*>(a.q);
+            const uint8_t* from = key ? rows[i] + m * 256 + chunk * 16 : reinterpret_cast<const uint8_t*>(a.q);
             const uint32_t to = d0 + row * 128 + ((chunk ^ (row & 7)) << 4);
             cp_async_16_or_zero(to, from, key);
-            cp_async_16_or_zero(to + kSlotBytes, from + (key ? 64 : 0), key);
+            cp_async_16_or_zero(to + kSlotBytes, from + (key ? 128 : 0), key);
           }
           cp_async_mbar_arrive(&c->full_g[m]);
         }
@@ -1015,7 +1074,7 @@ size_t tree_tc_workspace() {
   return (size_t)2 * kMaxCtas * kPartBytes + ((kMaxCtas * sizeof(int4) + 255) & ~(size_t)255);
 }
 
-cudaError_t launch_tree_tc(const TreeArgs& a, void* workspace, cudaStream_t st) {
+cudaError_t launch_tree_tc(const TreeArgs& a, bool q4, void* workspace, cudaStream_t st) {
   Args p;
   p.t = a;
   p.HS = a.H / kH;
@@ -1026,7 +1085,7 @@ cudaError_t launch_tree_tc(const TreeArgs& a, void* workspace, cudaStream_t st) 
   // swizzle atom).  A window or a selection starts anywhere and is gathered.
   p.dense_tok = a.ratio == 0 && a.window < 0;
   p.box = 0;
-  if (p.dense_tok || (a.ratio > 0 && a.K == 0)) {
+  if (!q4 && (p.dense_tok || (a.ratio > 0 && a.K == 0))) {
     const int page = p.dense_tok ? a.tok_page : a.ent_page;
     int box = kTile;
     while (page % box) box >>= 1;
@@ -1051,14 +1110,16 @@ cudaError_t launch_tree_tc(const TreeArgs& a, void* workspace, cudaStream_t st) 
     cudaError_t r = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (r != cudaSuccess) return r;
     sm_count[dev].store(sms, std::memory_order_relaxed);
-    return cudaFuncSetAttribute(tree_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    r = cudaFuncSetAttribute(tree_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    if (r != cudaSuccess) return r;
+    return cudaFuncSetAttribute(tree_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
   });
   if (e != cudaSuccess) return e;
   const int sms = sm_count[dev].load(std::memory_order_relaxed);
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
   {
     StageTiming ps(16, st);
-    e = launch_overlapped(tree_tc_kernel, dim3(grid), dim3(kThreads), kSmemBytes, st, mq, mp, p);
+    e = launch_overlapped(q4 ? tree_tc_kernel<true> : tree_tc_kernel<false>, dim3(grid), dim3(kThreads), kSmemBytes, st, mq, mp, p);
     if (e != cudaSuccess) return e;
     note_launch();
   }
