@@ -678,7 +678,7 @@ v4_status v4_cache_read_q4(const void* cache, int64_t n_slots, const int32_t* sl
 
 /* ----------------------------------------------------------------------
  * v4_tree_mqa_fwd over 4-bit caches: tok_cache and ent_cache hold rows of
- * v4_q4_row_bytes(D) bytes, everything else (keys, masks, sinks, padding, bad
+ * v4_q4_row_bytes(D) bytes and are 32-byte aligned, everything else (keys, masks, sinks, padding, bad
  * indices, workspace, dtype of q and o, shapes of either path) is
  * v4_tree_mqa_fwd's.  The values of the rows are exact in bf16, so on the same
  * values both give the same sums but for their order.

@@ -207,6 +207,8 @@ static v4_status tree_fwd(const v4_config* cfg, const v4_tree_inputs* in, bool q
     if (in->ent_slots < 1 || in->ent_slots > 0x7FFFFFFF) return bad("ent_slots must be in [1, 2^31)");
     if (c.topk > 0) TRY(check_ptr(in->idx, "idx"));
   }
+  if (q4 && (((c.window != 0 ? (uintptr_t)in->tok_cache : 0) | (c.ratio > 0 ? (uintptr_t)in->ent_cache : 0)) & 31u))
+    return bad("4-bit caches must be 32-byte aligned");
   size_t need = 0;
   TRY(v4_tree_workspace_size(cfg, in->n_rows, &need));
   if (ws_bytes < need) {

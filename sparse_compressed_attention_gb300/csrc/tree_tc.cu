@@ -56,6 +56,7 @@
 #include <math.h>
 
 #include "common.cuh"
+#include "fastdiv.cuh"
 #include "internal.h"
 #include "q4.cuh"
 #include "sm100.cuh"
@@ -70,7 +71,14 @@ namespace {
 
 constexpr int kH = 64, kD = 512, kR = 64;
 constexpr int kQ4RowBytes = kD / 2 + kD / kQ4Group;
-constexpr int kThreads = 448;
+constexpr int kThreads = 448, kThreadsQ4 = 640;
+constexpr int kRowsAhead = 4;                     // 4-bit caches: tiles whose rows are looked up ahead
+constexpr int kLookWarps = 2;                     // 4-bit caches: 64 key rows each
+constexpr int kUnpackWarps = 8;                   // 4-bit caches: two groups, 32 key rows each
+// Registers of a thread of the 4-bit kernel after the split: shares and products,
+// softmax, unpacking.  They add up to what 640 threads start with.
+constexpr int kRegsStart = 96, kRegsLead = 56, kRegsSoft = 112, kRegsUnpack = 96;
+static_assert(128 * kRegsLead + 256 * kRegsSoft + 256 * kRegsUnpack <= kThreadsQ4 * kRegsStart, "register split");
 constexpr int kSoftThreads = 256;                 // warps 4-11
 constexpr int kSoftWarps = kSoftThreads / 32;
 constexpr int kGatherWarps = 4;                   // 32 key rows each
@@ -83,6 +91,16 @@ constexpr uint32_t kPBytes = kTile * kH * 2;
 constexpr int kMaxCtas = 152;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRaise = 8.f;                     // how far (log2) a logit may exceed m
+
+// TMEM columns.  Dense caches: two S^T, O^T.  4-bit caches: one S^T, O^T, and a ring
+// of unpacked keys (pairs of K-blocks, 32 columns each) that are the S products' A.
+template <bool kQ4>
+struct Tm {
+  static constexpr uint32_t S1 = kQ4 ? 0 : 64, O = kQ4 ? 64 : 128;
+};
+constexpr int kRing = 3;
+constexpr uint32_t kRingTmem = 320;
+static_assert(Tm<true>::O + 4 * kH == kRingTmem && kRingTmem + 64 * kRing == 512, "TMEM columns");
 
 constexpr uint32_t OFF_Q = 0;                                     // 8 K-blocks, then q's low part
 constexpr uint32_t OFF_SLOT = OFF_Q + 9 * kQBlockBytes;           // 73728
@@ -113,16 +131,21 @@ struct Ctl {
   uint64_t s_full[2], p_ready[2];
   uint64_t o_full, o_empty;
   uint64_t info_full[2], info_empty[2];
+  // 4-bit caches: the S products have read a pair of unpacked K-blocks; a tile's rows
+  // are looked up, and used
+  uint64_t ring_empty[kRing];
+  uint64_t rows_full[kRowsAhead], rows_empty[kRowsAhead];
   uint64_t fin;
   Piece info[2];
-  uint32_t valid[2][kGatherWarps];       // bit per key row of a tile
+  uint32_t valid[kRowsAhead][kGatherWarps];      // bit per key row of a tile (dense caches: of two tiles)
+  const uint8_t* rows[kRowsAhead][kTile];
   float2 cs[2][kR / 2];                  // cos/sin of the piece's position
   alignas(16) float m[kH];               // shift of each head (log2 units), read four at a time
   float hmax[4][kH];
   float fac[kH];
   float part_l[4][kH];
   float inv[kH];
-  int scan[kThreads / 32];
+  int scan[kThreadsQ4 / 32];
   int start_item, start_unit;            // where this block's share begins
   Tiles start_tiles;
   uint32_t tmem_base;
@@ -146,6 +169,7 @@ struct Args {
   int box;                               // rows of a page run that one TMA box takes, 0: gather everything
   int dense_tok;                         // the runs are token pages (else entry pages)
   char* parts;
+  FastDiv by_tok, by_ent;                // pages
   int4* cuts;                            // per block: the item that goes on behind its end (or -1), that item's first and last block
 };
 
@@ -177,12 +201,11 @@ __device__ __forceinline__ int nth_node(const int4 w, int i) {
 }
 
 // Cache row behind position `at` of a row's key list; null where there is no key.
-template <int kRowBytes>
-__device__ __forceinline__ const uint8_t* key_row(const TreeArgs& a, const TreeRow& r, const int4 bits, int row,
-                                                  long long at) {
+__device__ __forceinline__ const bf16* key_row(const TreeArgs& a, const TreeRow& r, const int4 bits, int row,
+                                               long long at) {
   if (at < r.ne) {
     const long long s = tree_entry_row(a, r, row, (int)at);
-    return s < 0 ? nullptr : reinterpret_cast<const uint8_t*>(a.ent_cache) + s * kRowBytes;
+    return s < 0 ? nullptr : reinterpret_cast<const bf16*>(a.ent_cache) + s * kD;
   }
   at -= r.ne;
   long long u;
@@ -195,12 +218,60 @@ __device__ __forceinline__ const uint8_t* key_row(const TreeArgs& a, const TreeR
     u = (long long)r.L + j;
   }
   const long long s = tree_token_row(a, r, u);
-  return s < 0 ? nullptr : reinterpret_cast<const uint8_t*>(a.tok_cache) + s * kRowBytes;
+  return s < 0 ? nullptr : reinterpret_cast<const bf16*>(a.tok_cache) + s * kD;
+}
+
+// The same for 4-bit rows.  Unpacking lies between two tiles' products and the
+// look-up before it: positions fit 31 bits, and a division by the page costs a
+// product (tree_*_row divide 64-bit numbers).
+__device__ __forceinline__ const uint8_t* key_row_q4(const Args& p, const TreeRow& r, const int4 bits, int row,
+                                                     long long at) {
+  const TreeArgs& a = p.t;
+  const bool ent = at < r.ne;
+  long long u;                                    // row of the sequence's entries or tokens
+  if (ent) {
+    u = at;
+    if (a.K > 0) {
+      const int s = a.idx[(size_t)row * a.K + at];
+      if (s < 0 || s >= r.nv) {
+        if (s != -1) set_status(a.status, kStatusBadIndex);
+        return nullptr;
+      }
+      u = s;
+    }
+  } else if (at - r.ne < r.nw) {
+    u = r.lo + (at - r.ne);
+  } else {
+    if (a.window == 0 || at - r.ne - r.nw >= V4_TREE_MAX_NODES) return nullptr;
+    const int j = nth_node(bits, (int)(at - r.ne - r.nw));
+    if (j < 0 || !tree_draft_key(a, r, row, j, 0xFFFFFFFFu)) return nullptr;
+    u = (long long)r.L + j;
+  }
+  const int blocks = ent ? a.ent_blocks : a.tok_blocks, page = ent ? a.ent_page : a.tok_page;
+  const uint32_t blk = u <= 0x7FFFFFFF ? (ent ? p.by_ent : p.by_tok).div((uint32_t)u) : 0xFFFFFFFFu;
+  const int pg = blk < (uint32_t)blocks ? (ent ? a.ent_table : a.tok_table)[(size_t)r.b * blocks + blk] : -1;
+  const long long s = (long long)pg * page + ((int)u - (int)blk * page);
+  if (pg < 0 || s >= (ent ? a.ent_slots : a.tok_slots)) {
+    set_status(a.status, kStatusBadIndex);
+    return nullptr;
+  }
+  return reinterpret_cast<const uint8_t*>(ent ? a.ent_cache : a.tok_cache) + s * kQ4RowBytes;
 }
 
 // 16 bytes of global memory, or zeros, into shared memory.
 __device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
 }
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
@@ -219,7 +290,7 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
       "r"(__float_as_uint(v[27])), "r"(__float_as_uint(v[28])), "r"(__float_as_uint(v[29])),
       "r"(__float_as_uint(v[30])), "r"(__float_as_uint(v[31]))
       : "memory");
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+  tmem_wait_st();
 }
 
 // Barrier of n threads that also tells whether any of them saw `p`.
@@ -286,9 +357,30 @@ __device__ __forceinline__ float sink_mass(float s2, float m) {
 // its tiles.  Block c of the grid takes units [c * share, (c + 1) * share).
 __device__ __forceinline__ int share_of(int total, int ctas) { return (total + ctas - 1) / ctas; }
 
+// 32 bytes, one sector: half the requests of 16-byte loads where every lane reads a row of
+// its own, and no line of the little L1 that shared memory leaves (single tokens over long
+// caches 209 -> 195 us).
+__device__ __forceinline__ void load32(const uint8_t* from, uint4* to) {
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(to[0].x), "=r"(to[0].y), "=r"(to[0].z), "=r"(to[0].w), "=r"(to[1].x), "=r"(to[1].y),
+                 "=r"(to[1].z), "=r"(to[1].w)
+               : "l"(from)
+               : "memory");
+}
+
+// A warpgroup's registers after the split (the kernel starts with kRegsStart each):
+// `dec` may only lower and `inc` only raise.
+template <int kRegs>
+__device__ __forceinline__ void set_registers() {
+  static_assert(kRegs % 8 == 0 && kRegs >= 24 && kRegs <= 256, "setmaxnreg");
+  if constexpr (kRegs > kRegsStart) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+  if constexpr (kRegs < kRegsStart) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
 template <bool kQ4>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kQ4 ? kThreadsQ4 : kThreads, 1)
 tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_pages, const Args p) {
+  constexpr int kBlock = kQ4 ? kThreadsQ4 : kThreads, kKeyWarps = kQ4 ? kUnpackWarps + kLookWarps : kGatherWarps;
   extern __shared__ __align__(1024) uint8_t smem[];
   Ctl* c = reinterpret_cast<Ctl*>(smem + OFF_CTL);
   const TreeArgs& a = p.t;
@@ -303,9 +395,16 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kPairs; ++i) {
-      mbar_init(&c->full_g[i], kQ4 ? kGatherWarps : 32 * kGatherWarps);
+      mbar_init(&c->full_g[i], kQ4 ? kUnpackWarps / 2 : 32 * kGatherWarps);
       mbar_init(&c->full_t[i], 1);
       mbar_init(&c->empty[i], 1);
+    }
+    if (kQ4) {
+      for (int i = 0; i < kRing; ++i) mbar_init(&c->ring_empty[i], 1);
+      for (int i = 0; i < kRowsAhead; ++i) {
+        mbar_init(&c->rows_full[i], kLookWarps);
+        mbar_init(&c->rows_empty[i], kUnpackWarps + kSoftWarps);
+      }
     }
     mbar_init(&c->q_full, 1);
     mbar_init(&c->q_ready, kSoftWarps);
@@ -315,7 +414,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
       mbar_init(&c->s_full[i], 1);
       mbar_init(&c->p_ready[i], kSoftWarps);
       mbar_init(&c->info_full[i], 1);
-      mbar_init(&c->info_empty[i], 1 + kSoftWarps + kGatherWarps);
+      mbar_init(&c->info_empty[i], 1 + kSoftWarps + kKeyWarps);
     }
     mbar_init(&c->o_full, 1);
     mbar_init(&c->o_empty, kSoftWarps);
@@ -329,7 +428,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
   wait_previous();                              // nothing of global memory is read before
 
   // ---- this block's share: prefix sum of the items' units
-  const int per = (p.items + kThreads - 1) / kThreads;
+  const int per = (p.items + kBlock - 1) / kBlock;
   const int i0 = threadIdx.x * per, i1 = min(i0 + per, p.items);
   int mine = 0;
   Tiles first = {0, 0, 0};
@@ -347,7 +446,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
   if (lane == 31) c->scan[warp] = upto;
   __syncthreads();
   int before = upto - mine, total = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
+  for (int w = 0; w < kBlock / 32; ++w) {
     if (w < warp) before += c->scan[w];
     total += c->scan[w];
   }
@@ -380,316 +479,320 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
   tc_fence_after();
   const uint32_t tmem = c->tmem_base;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ shares and query rows
-    int item = c->start_item, unit = c->start_unit, qc = 0, g = 0;
-    bool ok = true;
-    int4 cut = make_int4(-1, -1, -1, 0);         // the item that goes on in the next block
-    auto next_piece = [&]() -> Piece {
-      Piece pc = {0, 0, 0, 0, 1, 0, -1, 0};
-      while (item < p.items && unit < s1) {
-        const Tiles t = item == c->start_item ? c->start_tiles : tree_tiles(p, item / p.HS);
-        const int n = t.n;
-        const int base = unit + 1;               // unit of the item's tile 0
-        const int lo = max(s0, base), hi = min(s1, base + n);
-        if (n > 0 && lo < hi) {
-          pc.done = 0;
-          pc.row = item / p.HS;
-          pc.hs = item % p.HS;
-          pc.tile0 = lo - base;
-          pc.tiles = hi - lo;
-          pc.dense = min(max(t.dense - pc.tile0, 0), pc.tiles);
-          // a share that begins behind tile 0 leaves its part in the block's
-          // first place, one that begins with it in the second
-          pc.seq = t.seq;
-          pc.part = pc.tiles == n ? -1 : 2 * (int)blockIdx.x + (lo > base ? 0 : 1);
-          if (base + n > s1) cut = make_int4(item, base / share, (base + n - 1) / share, 0);
+  // A warpgroup's warps share a branch: its registers change in one instruction.
+  if (warp < 4 || (!kQ4 && warp >= 12)) {
+    if constexpr (kQ4) set_registers<kRegsLead>();
+    if (warp == 0) {
+      // ------------------------------------------------------------ shares and query rows
+      int item = c->start_item, unit = c->start_unit, qc = 0, g = 0;
+      bool ok = true;
+      int4 cut = make_int4(-1, -1, -1, 0);         // the item that goes on in the next block
+      auto next_piece = [&]() -> Piece {
+        Piece pc = {0, 0, 0, 0, 1, 0, -1, 0};
+        while (item < p.items && unit < s1) {
+          const Tiles t = item == c->start_item ? c->start_tiles : tree_tiles(p, item / p.HS);
+          const int n = t.n;
+          const int base = unit + 1;               // unit of the item's tile 0
+          const int lo = max(s0, base), hi = min(s1, base + n);
+          if (n > 0 && lo < hi) {
+            pc.done = 0;
+            pc.row = item / p.HS;
+            pc.hs = item % p.HS;
+            pc.tile0 = lo - base;
+            pc.tiles = hi - lo;
+            pc.dense = min(max(t.dense - pc.tile0, 0), pc.tiles);
+            // a share that begins behind tile 0 leaves its part in the block's
+            // first place, one that begins with it in the second
+            pc.seq = t.seq;
+            pc.part = pc.tiles == n ? -1 : 2 * (int)blockIdx.x + (lo > base ? 0 : 1);
+            if (base + n > s1) cut = make_int4(item, base / share, (base + n - 1) / share, 0);
+          }
+          unit += n ? n + 1 : 0;
+          ++item;
+          if (!pc.done) break;
         }
-        unit += n ? n + 1 : 0;
-        ++item;
-        if (!pc.done) break;
-      }
-      return pc;
-    };
-    auto publish = [&](const Piece& pc, int q) {
-      if (lane == 0) {
-        const int is = q & 1;
-        if (q >= 2) ok = mbar_wait(&c->info_empty[is], ((q >> 1) - 1) & 1, &c->abort, a.status);
-        if (ok) {
-          c->info[is] = pc;
-          mbar_arrive(&c->info_full[is]);
+        return pc;
+      };
+      auto publish = [&](const Piece& pc, int q) {
+        if (lane == 0) {
+          const int is = q & 1;
+          if (q >= 2) ok = mbar_wait(&c->info_empty[is], ((q >> 1) - 1) & 1, &c->abort, a.status);
+          if (ok) {
+            c->info[is] = pc;
+            mbar_arrive(&c->info_full[is]);
+          }
         }
-      }
-      ok = __shfl_sync(0xffffffffu, (int)ok, 0);
-    };
-    // lane: box lane & 15 of K-block 2 m + (lane >> 4), m in the order in which the
-    // O products release them
-    const int box = lane & 15, odd = lane >> 4;
-    const int boxes = p.box ? kTile / p.box : 0;
-    const int32_t* table = p.dense_tok ? a.tok_table : a.ent_table;
-    const int blocks = p.dense_tok ? a.tok_blocks : a.ent_blocks, page = p.dense_tok ? a.tok_page : a.ent_page;
-    const int slots = (int)(p.dense_tok ? a.tok_slots : a.ent_slots);
-    Piece pc = next_piece();
-    publish(pc, 0);
-    while (ok && !pc.done) {
-      if (lane == 0) {
-        if (qc >= 1) ok = mbar_wait(&c->q_empty, (qc - 1) & 1, &c->abort, a.status);
-        if (ok) mbar_expect_tx(&c->q_full, 8 * kQBlockBytes);
-      }
-      ok = __shfl_sync(0xffffffffu, (int)ok, 0);
-      if (!ok) break;
-      if (lane < 8)
-        tma_load_2d(smem + OFF_Q + lane * kQBlockBytes, &map_q, 64 * lane, pc.row * a.H + kH * pc.hs, &c->q_full);
-      // the next piece is described while this one's tiles load
-      Piece nxt = {0, 0, 0, 0, 1, 0, -1, 0};
-      if (pc.dense == 0) {
-        nxt = next_piece();
-        publish(nxt, qc + 1);
-      }
-      for (int j = 0; j < pc.dense && ok; ++j) {
-        // cache row of this lane's box, looked up before the slots are free; a
-        // page that the table does not hold reads zeros (its rows are masked)
-        int y = slots;
-        if (box < boxes) {
-          const long long at = (long long)(pc.tile0 + j) * kTile + box * p.box;
-          const long long blk = at / page;
-          const int pg = blk < blocks ? table[(size_t)pc.seq * blocks + blk] : -1;
-          const long long r = (long long)pg * page + (at - blk * page);
-          if (pg >= 0 && r < slots) y = (int)r;
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+      };
+      // lane: box lane & 15 of K-block 2 m + (lane >> 4), m in the order in which the
+      // O products release them
+      const int box = lane & 15, odd = lane >> 4;
+      const int boxes = p.box ? kTile / p.box : 0;
+      const int32_t* table = p.dense_tok ? a.tok_table : a.ent_table;
+      const int blocks = p.dense_tok ? a.tok_blocks : a.ent_blocks, page = p.dense_tok ? a.tok_page : a.ent_page;
+      const int slots = (int)(p.dense_tok ? a.tok_slots : a.ent_slots);
+      Piece pc = next_piece();
+      publish(pc, 0);
+      while (ok && !pc.done) {
+        if (lane == 0) {
+          if (qc >= 1) ok = mbar_wait(&c->q_empty, (qc - 1) & 1, &c->abort, a.status);
+          if (ok) mbar_expect_tx(&c->q_full, 8 * kQBlockBytes);
         }
-        for (int m = kPairs - 1; m >= 0 && ok; --m) {
-          const int kb = 2 * m + odd;
-          if (g >= 1) ok = mbar_wait(&c->empty[m], (g - 1) & 1, &c->abort, a.status);
-          if (!ok) break;
-          if (lane == 0) mbar_expect_tx(&c->full_t[m], 2 * kSlotBytes);
-          if (box < boxes)
-            tma_load_2d(smem + OFF_SLOT + kb * kSlotBytes + box * p.box * 128, &map_pages, 64 * kb, y, &c->full_t[m]);
-        }
-        ok = __all_sync(0xffffffffu, ok);
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0);
         if (!ok) break;
-        ++g;
-        if (j == 0) {
+        if (lane < 8)
+          tma_load_2d(smem + OFF_Q + lane * kQBlockBytes, &map_q, 64 * lane, pc.row * a.H + kH * pc.hs, &c->q_full);
+        // the next piece is described while this one's tiles load
+        Piece nxt = {0, 0, 0, 0, 1, 0, -1, 0};
+        if (kQ4 || pc.dense == 0) {
           nxt = next_piece();
           publish(nxt, qc + 1);
         }
+        for (int j = 0; !kQ4 && j < pc.dense && ok; ++j) {
+          // cache row of this lane's box, looked up before the slots are free; a
+          // page that the table does not hold reads zeros (its rows are masked)
+          int y = slots;
+          if (box < boxes) {
+            const long long at = (long long)(pc.tile0 + j) * kTile + box * p.box;
+            const long long blk = at / page;
+            const int pg = blk < blocks ? table[(size_t)pc.seq * blocks + blk] : -1;
+            const long long r = (long long)pg * page + (at - blk * page);
+            if (pg >= 0 && r < slots) y = (int)r;
+          }
+          for (int m = kPairs - 1; m >= 0 && ok; --m) {
+            const int kb = 2 * m + odd;
+            if (g >= 1) ok = mbar_wait(&c->empty[m], (g - 1) & 1, &c->abort, a.status);
+            if (!ok) break;
+            if (lane == 0) mbar_expect_tx(&c->full_t[m], 2 * kSlotBytes);
+            if (box < boxes)
+              tma_load_2d(smem + OFF_SLOT + kb * kSlotBytes + box * p.box * 128, &map_pages, 64 * kb, y, &c->full_t[m]);
+          }
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          ++g;
+          if (j == 0) {
+            nxt = next_piece();
+            publish(nxt, qc + 1);
+          }
+        }
+        // gathered tiles: their slot releases are awaited too, a parity wait being
+        // unambiguous one phase ahead only
+        for (int j = pc.dense; !kQ4 && j < pc.tiles && ok; ++j) {
+          for (int m = kPairs - 1; m >= 0 && ok; --m)
+            if (g >= 1) ok = warp_wait(&c->empty[m], (g - 1) & 1, c, a.status);
+          ++g;
+        }
+        pc = nxt;
+        ++qc;
       }
-      // gathered tiles: their slot releases are awaited too, a parity wait being
-      // unambiguous one phase ahead only
-      for (int j = pc.dense; j < pc.tiles && ok; ++j) {
-        for (int m = kPairs - 1; m >= 0 && ok; --m)
-          if (g >= 1) ok = warp_wait(&c->empty[m], (g - 1) & 1, c, a.status);
-        ++g;
+      if (lane == 0) p.cuts[blockIdx.x] = cut;
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ products
+      // The whole warp walks the tiles and one elected lane issues: with warp-uniform
+      // control and operands the descriptors stay in uniform registers.  The same
+      // loop inside `if (lane == 0)` moved each of them there for every product
+      // (402 against 371 us for 16 nodes over 32768 tokens).
+      {
+        const bool lead = elect_one();               // issues for the converged warp
+        const uint32_t id1 = idesc_bf16_f32(128, 64, 0, 0);
+        const uint32_t id2 = idesc_bf16_f32(128, 64, 1, 1);
+        const uint64_t dA1 = smem_desc(smem_u32(smem + OFF_SLOT), 16, 1024, kLayoutSW128);
+        const uint64_t dQ = smem_desc(smem_u32(smem + OFF_Q), 16, 1024, kLayoutSW128);
+        const uint64_t dA2 = smem_desc(smem_u32(smem + OFF_SLOT), kSlotBytes, 1024, kLayoutSW128);
+        const uint64_t dP = smem_desc(smem_u32(smem + OFF_P), 128, 2048, kLayoutNone);
+        const uint32_t hA1 = (uint32_t)(dA1 >> 32), hQ = (uint32_t)(dQ >> 32), hA2 = (uint32_t)(dA2 >> 32),
+                       hP = (uint32_t)(dP >> 32);
+        const uint32_t a1 = (uint32_t)dA1, q1 = (uint32_t)dQ, a2 = (uint32_t)dA2, p2 = (uint32_t)dP;
+        const auto desc = [](uint32_t hi, uint32_t lo) { return ((uint64_t)hi << 32) | lo; };
+        int qc = 0, g = 0, gg = 0, gt = 0;            // all tiles, gathered ones, page runs
+        int ring = 0;
+        bool ok = true;
+        while (ok) {
+          const int is = qc & 1;
+          ok = warp_wait(&c->info_full[is], (qc >> 1) & 1, c, a.status);
+          if (!ok) break;
+          const Piece pc = c->info[is];
+          __syncwarp();
+          if (lead) mbar_arrive(&c->info_empty[is]);
+          if (pc.done) break;
+          ok = warp_wait(&c->q_ready, qc & 1, c, a.status);
+          tc_fence_after();
+          for (int j = 0; j < pc.tiles && ok; ++j) {
+            const int sb = g & 1;
+            const uint32_t s_tmem = tmem + Tm<kQ4>::S1 * sb;
+            // K-blocks as they land, two at a time (the O products release them in
+            // pairs), the rotated dims' pair first: their second products then run
+            // while the others land.  TMA writes need no proxy fence.
+            const bool dense = j < pc.dense;
+            uint64_t* full = dense ? c->full_t : c->full_g;
+            const uint32_t par = (dense ? gt : gg) & 1;
+#pragma unroll
+            for (int m = kPairs - 1; m >= 0; --m) {
+              ok = ok && warp_wait(&full[m], par, c, a.status);
+              if (!kQ4 && !dense) fence_proxy_async_smem();     // cp.async writes -> tensor-core reads
+              if constexpr (kQ4) {
+                tc_fence_after();                           // the unpacked keys were stored by other warps
+                const uint32_t k_tmem = tmem + kRingTmem + 64 * ring;
+                if (lead) {
+#pragma unroll
+                  for (int ks = 0; ks < 8; ++ks)
+                    umma_f16_ts(s_tmem, k_tmem + 8 * ks,
+                                desc(hQ, q1 + (((2 * m + ks / 4) * kQBlockBytes + 32 * (ks & 3)) >> 4)), id1,
+                                m < kPairs - 1 || ks > 0);
+                  if (m == kPairs - 1)
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                      umma_f16_ts(s_tmem, k_tmem + 32 + 8 * ks, desc(hQ, q1 + ((8 * kQBlockBytes + 32 * ks) >> 4)), id1, 1u);
+                  umma_commit(&c->ring_empty[ring]);
+                }
+                ring = ring == kRing - 1 ? 0 : ring + 1;
+              } else if (lead) {
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                  umma_f16_ss(s_tmem, desc(hA1, a1 + (((2 * m + ks / 4) * kSlotBytes + 32 * (ks & 3)) >> 4)),
+                              desc(hQ, q1 + (((2 * m + ks / 4) * kQBlockBytes + 32 * (ks & 3)) >> 4)), id1,
+                              m < kPairs - 1 || ks > 0);
+                if (m == kPairs - 1)                    // the rotated dims once more, against q's low part
+#pragma unroll
+                  for (int ks = 0; ks < 4; ++ks)
+                    umma_f16_ss(s_tmem, desc(hA1, a1 + ((7 * kSlotBytes + 32 * ks) >> 4)),
+                                desc(hQ, q1 + ((8 * kQBlockBytes + 32 * ks) >> 4)), id1, 1u);
+              }
+            }
+            if (dense) ++gt; else ++gg;
+            if (lead) {
+              umma_commit(&c->s_full[sb]);
+              if (j == pc.tiles - 1) umma_commit(&c->q_empty);
+            }
+            __syncwarp();
+            if (!ok) break;
+            ok = warp_wait(&c->p_ready[sb], (g >> 1) & 1, c, a.status);
+            if (ok && j == 0 && qc >= 1) ok = warp_wait(&c->o_empty, (qc - 1) & 1, c, a.status);
+            tc_fence_after();
+            if (lead) {
+#pragma unroll
+              for (int m = kPairs - 1; m >= 0; --m) {
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                  umma_f16_ss(tmem + Tm<kQ4>::O + 64 * m, desc(hA2, a2 + ((2 * m * kSlotBytes + 2048 * ks) >> 4)),
+                              desc(hP, p2 + ((256 * ks) >> 4)), id2, (j > 0 || ks > 0) ? 1u : 0u);
+                umma_commit(&c->empty[m]);
+              }
+            }
+            __syncwarp();
+            ++g;
+          }
+          if (lead) umma_commit(&c->o_full);
+          ++qc;
+        }
+        if (lead) umma_commit(&c->fin);                        // every product completes before TMEM is released
+        mbar_wait(&c->fin, 0, &c->abort, a.status, 200000000ull);
       }
-      pc = nxt;
-      ++qc;
-    }
-    if (lane == 0) p.cuts[blockIdx.x] = cut;
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ products
-    // The whole warp walks the tiles and one elected lane issues: with warp-uniform
-    // control and operands the descriptors stay in uniform registers.  The same
-    // loop inside `if (lane == 0)` moved each of them there for every product
-    // (402 against 371 us for 16 nodes over 32768 tokens).
-    {
-      const bool lead = elect_one();               // issues for the converged warp
-      const uint32_t id1 = idesc_bf16_f32(128, 64, 0, 0);
-      const uint32_t id2 = idesc_bf16_f32(128, 64, 1, 1);
-      const uint64_t dA1 = smem_desc(smem_u32(smem + OFF_SLOT), 16, 1024, kLayoutSW128);
-      const uint64_t dQ = smem_desc(smem_u32(smem + OFF_Q), 16, 1024, kLayoutSW128);
-      const uint64_t dA2 = smem_desc(smem_u32(smem + OFF_SLOT), kSlotBytes, 1024, kLayoutSW128);
-      const uint64_t dP = smem_desc(smem_u32(smem + OFF_P), 128, 2048, kLayoutNone);
-      const uint32_t hA1 = (uint32_t)(dA1 >> 32), hQ = (uint32_t)(dQ >> 32), hA2 = (uint32_t)(dA2 >> 32),
-                     hP = (uint32_t)(dP >> 32);
-      const uint32_t a1 = (uint32_t)dA1, q1 = (uint32_t)dQ, a2 = (uint32_t)dA2, p2 = (uint32_t)dP;
-      const auto desc = [](uint32_t hi, uint32_t lo) { return ((uint64_t)hi << 32) | lo; };
-      int qc = 0, g = 0, gg = 0, gt = 0;            // all tiles, gathered ones, page runs
+      __syncwarp();
+    } else if constexpr (kQ4) {
+      // ------------------------------------------------------------ look-ups of 4-bit rows
+      const int lw = warp - 2;
+      int qc = 0, g = 0;
       bool ok = true;
       while (ok) {
         const int is = qc & 1;
         ok = warp_wait(&c->info_full[is], (qc >> 1) & 1, c, a.status);
-        if (!ok) break;
         const Piece pc = c->info[is];
-        __syncwarp();
-        if (lead) mbar_arrive(&c->info_empty[is]);
-        if (pc.done) break;
-        ok = warp_wait(&c->q_ready, qc & 1, c, a.status);
-        tc_fence_after();
+        warp_arrive(&c->info_empty[is], lane);
+        if (!ok || pc.done) break;
+        const TreeRow r = tree_row(a, pc.row);
+        const int4 bits = *reinterpret_cast<const int4*>(a.plan + (size_t)pc.row * kPlanWords + 4);
         for (int j = 0; j < pc.tiles && ok; ++j) {
-          const int sb = g & 1;
-          const uint32_t s_tmem = tmem + 64 * sb;
-          // K-blocks as they land, two at a time (the O products release them in
-          // pairs), the rotated dims' pair first: their second products then run
-          // while the others land.  TMA writes need no proxy fence.
-          const bool dense = j < pc.dense;
-          uint64_t* full = dense ? c->full_t : c->full_g;
-          const uint32_t par = (dense ? gt : gg) & 1;
+          const int rs = g & (kRowsAhead - 1);
+          const long long at = (long long)(pc.tile0 + j) * kTile + 64 * lw + lane;
+          const uint8_t* row[2];
 #pragma unroll
-          for (int m = kPairs - 1; m >= 0; --m) {
-            ok = ok && warp_wait(&full[m], par, c, a.status);
-            if (!kQ4 && !dense) fence_proxy_async_smem();     // cp.async writes -> tensor-core reads
-            if (lead) {
-#pragma unroll
-              for (int ks = 0; ks < 8; ++ks)
-                umma_f16_ss(s_tmem, desc(hA1, a1 + (((2 * m + ks / 4) * kSlotBytes + 32 * (ks & 3)) >> 4)),
-                            desc(hQ, q1 + (((2 * m + ks / 4) * kQBlockBytes + 32 * (ks & 3)) >> 4)), id1,
-                            m < kPairs - 1 || ks > 0);
-              if (m == kPairs - 1)                    // the rotated dims once more, against q's low part
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                  umma_f16_ss(s_tmem, desc(hA1, a1 + ((7 * kSlotBytes + 32 * ks) >> 4)),
-                              desc(hQ, q1 + ((8 * kQBlockBytes + 32 * ks) >> 4)), id1, 1u);
-            }
-          }
-          if (dense) ++gt; else ++gg;
-          if (lead) {
-            umma_commit(&c->s_full[sb]);
-            if (j == pc.tiles - 1) umma_commit(&c->q_empty);
-          }
-          __syncwarp();
+          for (int i = 0; i < 2; ++i) row[i] = key_row_q4(p, r, bits, pc.row, at + 32 * i);
+          if (g >= kRowsAhead) ok = warp_wait(&c->rows_empty[rs], (g / kRowsAhead - 1) & 1, c, a.status);
           if (!ok) break;
-          ok = warp_wait(&c->p_ready[sb], (g >> 1) & 1, c, a.status);
-          if (ok && j == 0 && qc >= 1) ok = warp_wait(&c->o_empty, (qc - 1) & 1, c, a.status);
-          tc_fence_after();
-          if (lead) {
 #pragma unroll
-            for (int m = kPairs - 1; m >= 0; --m) {
-#pragma unroll
-              for (int ks = 0; ks < 8; ++ks)
-                umma_f16_ss(tmem + 128 + 64 * m, desc(hA2, a2 + ((2 * m * kSlotBytes + 2048 * ks) >> 4)),
-                            desc(hP, p2 + ((256 * ks) >> 4)), id2, (j > 0 || ks > 0) ? 1u : 0u);
-              umma_commit(&c->empty[m]);
-            }
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t live = __ballot_sync(0xffffffffu, row[i] != nullptr);
+            c->rows[rs][64 * lw + 32 * i + lane] = row[i];
+            if (lane == 0) c->valid[rs][2 * lw + i] = live;
+            if (row[i] != nullptr) {
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(row[i]) : "memory");
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(row[i] + 128) : "memory");
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(row[i] + 256) : "memory");
           }
-          __syncwarp();
+          }
+          warp_arrive(&c->rows_full[rs], lane);
           ++g;
         }
-        if (lead) umma_commit(&c->o_full);
         ++qc;
       }
-      if (lead) umma_commit(&c->fin);                        // every product completes before TMEM is released
-      mbar_wait(&c->fin, 0, &c->abort, a.status, 200000000ull);
-    }
-    __syncwarp();
-  } else if (warp < 4 || warp >= 12) {
-    // ------------------------------------------------------------ key rows
-    constexpr int kRowBytes = kQ4 ? kQ4RowBytes : kD * 2;
-    const int gw = warp < 4 ? warp - 2 : warp - 10;
-    const int chunk = lane & 7;
-    int qc = 0, g = 0;
-    bool ok = true;
-    while (ok) {
-      const int is = qc & 1;
-      ok = warp_wait(&c->info_full[is], (qc >> 1) & 1, c, a.status);
-      const Piece pc = c->info[is];
-      warp_arrive(&c->info_empty[is], lane);
-      if (!ok || pc.done) break;
-      const TreeRow r = tree_row(a, pc.row);
-      const int4 bits = *reinterpret_cast<const int4*>(a.plan + (size_t)pc.row * kPlanWords + 4);
-      // lane i looks after key row 32 gw + i of a tile
-      auto look_up = [&](int j) {
-        return key_row<kRowBytes>(a, r, bits, pc.row, (long long)(pc.tile0 + j) * kTile + 32 * gw + lane);
-      };
-      const uint8_t* next = look_up(0);
-      if constexpr (kQ4) {
-        // A lane holds its row's codes in registers a tile ahead, unpacks a pair of
-        // K-blocks when their slots are released and asks for the next tile's.
-        const int row = 32 * gw + lane;
-        uint4 codes[16], scales[2];
-        auto load = [&](const uint8_t* from, int m) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            codes[4 * m + i] = from ? reinterpret_cast<const uint4*>(from)[4 * m + i]
-                                    : make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);   // zeros
+    } else {
+      // ------------------------------------------------------------ key rows
+      const int gw = warp < 4 ? warp - 2 : warp - 10;
+      const int chunk = lane & 7;
+      int qc = 0, g = 0;
+      bool ok = true;
+      while (ok) {
+        const int is = qc & 1;
+        ok = warp_wait(&c->info_full[is], (qc >> 1) & 1, c, a.status);
+        const Piece pc = c->info[is];
+        warp_arrive(&c->info_empty[is], lane);
+        if (!ok || pc.done) break;
+        const TreeRow r = tree_row(a, pc.row);
+        const int4 bits = *reinterpret_cast<const int4*>(a.plan + (size_t)pc.row * kPlanWords + 4);
+        // lane i looks after key row 32 gw + i of a tile
+        auto look_up = [&](int j) {
+          return key_row(a, r, bits, pc.row, (long long)(pc.tile0 + j) * kTile + 32 * gw + lane);
         };
-        auto load_scales = [&](const uint8_t* from) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            scales[i] = from ? reinterpret_cast<const uint4*>(from + kD / 2)[i] : make_uint4(0, 0, 0, 0);
-        };
-#pragma unroll
-        for (int m = 0; m < kPairs; ++m) load(next, m);
-        load_scales(next);
+        const bf16* next = look_up(0);
         for (int j = 0; j < pc.tiles && ok; ++j) {
-          const uint32_t live = __ballot_sync(0xffffffffu, next != nullptr);
+          const bf16* src = next;
+          const uint32_t live = __ballot_sync(0xffffffffu, src != nullptr);
           if (lane == 0) {
-            c->valid[g & 1][gw] = live;           // tile g - 2's bits have been read, as below
+            // tile g - 2's bits have been read: its O products completed before
+            // this warp could fill the slots of tile g - 1
+            c->valid[g & 1][gw] = live;
             mbar_arrive(&c->valid_full[g & 1]);
           }
-          const bool more = j + 1 < pc.tiles;
-          if (more) next = look_up(j + 1);
+          const bf16* rows[8];
 #pragma unroll
+          for (int i = 0; i < 8; ++i)
+            rows[i] = reinterpret_cast<const bf16*>(
+                __shfl_sync(0xffffffffu, (unsigned long long)src, 4 * i + (lane >> 3)));
           for (int m = kPairs - 1; m >= 0; --m) {
-            if (g >= 1 && ok) ok = warp_wait(&c->empty[m], (g - 1) & 1, c, a.status);
-            if (ok) {
-              const uint32_t* sc = reinterpret_cast<const uint32_t*>(scales) + 2 * m;
+            if (g >= 1) ok = warp_wait(&c->empty[m], (g - 1) & 1, c, a.status);
+            if (!ok) break;
+            if (j < pc.dense) continue;               // arrives as page runs
+            const uint32_t d0 = smem_u32(smem + OFF_SLOT + 2 * m * kSlotBytes);
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {       // K-block 2 m + h
-                uint8_t* to = smem + OFF_SLOT + (2 * m + h) * kSlotBytes + row * 128;
-#pragma unroll
-                for (int ch = 0; ch < 8; ++ch) {  // 16-byte chunk: one word of codes
-                  const uint4 w4 = codes[4 * m + 2 * h + ch / 4];
-                  const uint32_t w = ch % 4 == 0 ? w4.x : ch % 4 == 1 ? w4.y : ch % 4 == 2 ? w4.z : w4.w;
-                  const uint32_t b = (sc[h] >> (8 * (ch / 2))) & 255u;
-                  *reinterpret_cast<uint4*>(to + ((ch ^ (row & 7)) << 4)) = q4_word_bf16(w, b);
-                }
-              }
-              fence_proxy_async_smem();
-              warp_arrive(&c->full_g[m], lane);
+            for (int i = 0; i < 8; ++i) {
+              const int row = 32 * gw + 4 * i + (lane >> 3);
+              const bool key = rows[i] != nullptr;
+              const bf16* from = key ? rows[i] + m * 128 + chunk * 8 : reinterpret_cast<const bf16*>(a.q);
+              const uint32_t to = d0 + row * 128 + ((chunk ^ (row & 7)) << 4);
+              cp_async_16_or_zero(to, from, key);
+              cp_async_16_or_zero(to + kSlotBytes, from + (key ? 64 : 0), key);
             }
-            if (more) load(next, m);
+            cp_async_mbar_arrive(&c->full_g[m]);
           }
-          if (more) load_scales(next);
+          // Rows of the next tile are looked up while this one is in use, and asked
+          // into L2: only one tile fits in shared memory, too few bytes in flight to
+          // cover the latency of HBM (16 ragged rows over all their tokens: 105 us
+          // without, 93 with).
+          if (j + 1 < pc.tiles) {
+            next = look_up(j + 1);
+            if (next != nullptr)
+              asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(next), "r"(kD * 2) : "memory");
+          }
           ++g;
         }
         ++qc;
-        continue;
       }
-      for (int j = 0; j < pc.tiles && ok; ++j) {
-        const uint8_t* src = next;
-        const uint32_t live = __ballot_sync(0xffffffffu, src != nullptr);
-        if (lane == 0) {
-          // tile g - 2's bits have been read: its O products completed before
-          // this warp could fill the slots of tile g - 1
-          c->valid[g & 1][gw] = live;
-          mbar_arrive(&c->valid_full[g & 1]);
-        }
-        const uint8_t* rows[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          rows[i] = reinterpret_cast<const uint8_t*>(
-              __shfl_sync(0xffffffffu, (unsigned long long)src, 4 * i + (lane >> 3)));
-        for (int m = kPairs - 1; m >= 0; --m) {
-          if (g >= 1) ok = warp_wait(&c->empty[m], (g - 1) & 1, c, a.status);
-          if (!ok) break;
-          if (j < pc.dense) continue;               // arrives as page runs
-          const uint32_t d0 = smem_u32(smem + OFF_SLOT + 2 * m * kSlotBytes);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int row = 32 * gw + 4 * i + (lane >> 3);
-            const bool key = rows[i] != nullptr;
-            const uint8_t* from = key ? rows[i] + m * 256 + chunk * 16 : reinterpret_cast<const uint8_t*>(a.q);
-            const uint32_t to = d0 + row * 128 + ((chunk ^ (row & 7)) << 4);
-            cp_async_16_or_zero(to, from, key);
-            cp_async_16_or_zero(to + kSlotBytes, from + (key ? 128 : 0), key);
-          }
-          cp_async_mbar_arrive(&c->full_g[m]);
-        }
-        // Rows of the next tile are looked up while this one is in use, and asked
-        // into L2: only one tile fits in shared memory, too few bytes in flight to
-        // cover the latency of HBM (16 ragged rows over all their tokens: 105 us
-        // without, 93 with).
-        if (j + 1 < pc.tiles) {
-          next = look_up(j + 1);
-          if (next != nullptr)
-            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(next), "r"(kD * 2) : "memory");
-        }
-        ++g;
-      }
-      ++qc;
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-  } else {
+  } else if (warp < 12) {
     // ------------------------------------------------------------ softmax and output
+    if constexpr (kQ4) set_registers<kRegsSoft>();
     const int ts = threadIdx.x - 128;         // 0..255
     const int quarter = warp & 3;             // TMEM lane quarter
     const int hh = (warp - 4) >> 2;           // head half
@@ -756,13 +859,21 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
       for (int i = 0; i < 32; ++i) lsum[i] = 0.f;
       for (int j = 0; j < pc.tiles; ++j) {
         const int sb = g & 1;
-        warp_wait(&c->valid_full[sb], (g >> 1) & 1, c, a.status);
-        const bool valid = (c->valid[sb][quarter] >> lane) & 1u;
+        bool valid;
+        if constexpr (kQ4) {
+          const int rs = g & (kRowsAhead - 1);
+          warp_wait(&c->rows_full[rs], (g / kRowsAhead) & 1, c, a.status);
+          valid = (c->valid[rs][quarter] >> lane) & 1u;
+          warp_arrive(&c->rows_empty[rs], lane);
+        } else {
+          warp_wait(&c->valid_full[sb], (g >> 1) & 1, c, a.status);
+          valid = (c->valid[sb][quarter] >> lane) & 1u;
+        }
         warp_wait(&c->s_full[sb], (g >> 1) & 1, c, a.status);
         tc_fence_after();
         // x = logit (log2 units) minus the head's shift, the exponent's argument
         float x[32];
-        tmem_ld32(tmem + lane_base + 64 * sb + h0, x);
+        tmem_ld32(tmem + lane_base + Tm<kQ4>::S1 * sb + h0, x);
         tmem_wait_ld();
         bool raise = j == 0;
         if (j > 0) {
@@ -782,7 +893,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
           // set this half's shifts to the running maximum (a piece's first tile,
           // rarely a later one) and rescale
           if (j > 0) {
-            tmem_ld32(tmem + lane_base + 64 * sb + h0, x);      // the logits again
+            tmem_ld32(tmem + lane_base + Tm<kQ4>::S1 * sb + h0, x);      // the logits again
             tmem_wait_ld();
           }
 #pragma unroll
@@ -799,15 +910,16 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
           if (j > 0) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) lsum[i] *= c->fac[h0 + i];
+#pragma unroll 1                                // unrolled, its registers spilled in the whole tile loop
             for (int mb = 0; mb < 4; ++mb) {      // the products into O^T so far completed before S
-              tmem_ld32(tmem + lane_base + 128 + 64 * mb + h0, x);
+              tmem_ld32(tmem + lane_base + Tm<kQ4>::O + 64 * mb + h0, x);
               tmem_wait_ld();
 #pragma unroll
               for (int i = 0; i < 32; ++i) x[i] *= c->fac[h0 + i];
-              tmem_st32(tmem + lane_base + 128 + 64 * mb + h0, x);
+              tmem_st32(tmem + lane_base + Tm<kQ4>::O + 64 * mb + h0, x);
             }
           }
-          tmem_ld32(tmem + lane_base + 64 * sb + h0, x);
+          tmem_ld32(tmem + lane_base + Tm<kQ4>::S1 * sb + h0, x);
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
@@ -886,7 +998,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
       bf16* opair = reinterpret_cast<bf16*>(a.o) + (orow + h0 + (lane & 1)) * kD + (krow & ~1);
       for (int m = 0; m < 4; ++m) {
         float v[32];
-        tmem_ld32(tmem + lane_base + 128 + 64 * m + h0, v);
+        tmem_ld32(tmem + lane_base + Tm<kQ4>::O + 64 * m + h0, v);
         tmem_wait_ld();
         if (m == 3) {
           tc_fence_before();
@@ -921,6 +1033,93 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
       }
       named_bar_sync(1, kSoftThreads);            // this piece's shifts and factors are read
       ++qc;
+    }
+  } else if constexpr (kQ4) {
+    // ------------------------------------------------------------ keys out of 4-bit rows
+    // Two groups of four warps take the pairs of K-blocks in turn (3 and 1, 2 and 0), so
+    // that one waits for memory while the other unpacks.  A lane holds its row's codes in
+    // registers a tile ahead and asks for the next tile's once they are unpacked.  Keys go
+    // to TMEM for the S products, where a warp reaches its own lane quarter, and to shared
+    // memory for the O products.
+    set_registers<kRegsUnpack>();
+    const int quarter = warp & 3, row = 32 * quarter + lane, grp = (warp - 12) >> 2;
+    uint4 codes[8];
+    uint2 scales[2];
+    int qc = 0, tiles = 0;                       // pieces read, tiles left of the last one
+    bool ok = true;
+    // whether there is a tile behind those taken so far
+    auto more_tiles = [&]() -> bool {
+      if (tiles == 0) {
+        const int is = qc & 1;
+        ok = ok && warp_wait(&c->info_full[is], (qc >> 1) & 1, c, a.status);
+        tiles = !ok || c->info[is].done ? -1 : c->info[is].tiles;
+        warp_arrive(&c->info_empty[is], lane);
+        ++qc;
+      }
+      return tiles > 0;
+    };
+    // row of tile g
+    auto row_of = [&](int g) -> const uint8_t* {
+      const int rs = g & (kRowsAhead - 1);
+      ok = ok && warp_wait(&c->rows_full[rs], (g / kRowsAhead) & 1, c, a.status);
+      const uint8_t* from = ok ? c->rows[rs][row] : nullptr;
+      warp_arrive(&c->rows_empty[rs], lane);
+      --tiles;
+      return from;
+    };
+    auto load = [&](const uint8_t* from, int i, int m) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) codes[4 * i + k] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);  // zeros
+      if (from != nullptr) {
+        load32(from + 64 * m, &codes[4 * i]);
+        load32(from + 64 * m + 32, &codes[4 * i + 2]);
+      }
+      scales[i] = from ? reinterpret_cast<const uint2*>(from + kD / 2)[m] : make_uint2(0, 0);
+    };
+    bool more = more_tiles();
+    if (more) {
+      const uint8_t* from = row_of(0);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) load(from, i, kPairs - 1 - grp - 2 * i);
+    }
+    for (int g = 0; more && ok; ++g) {
+      const uint8_t* next = nullptr;
+      more = more_tiles();
+      if (more) next = row_of(g + 1);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int m = kPairs - 1 - grp - 2 * i;
+        const uint32_t n = 4 * (uint32_t)g + grp + 2 * i, turn = n / kRing, ring = n - kRing * turn;
+        if (g >= 1 && ok) ok = warp_wait(&c->empty[m], (g - 1) & 1, c, a.status);
+        if (turn >= 1 && ok) ok = warp_wait(&c->ring_empty[ring], (turn - 1) & 1, c, a.status);
+        if (ok) {
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {          // half a K-block: 32 dims
+            uint8_t* to = smem + OFF_SLOT + (2 * m + k / 2) * kSlotBytes + row * 128;
+            const uint32_t sc = (k / 2 ? scales[i].y : scales[i].x) >> (16 * (k & 1));
+            uint32_t v[16];
+#pragma unroll
+            for (int c4 = 0; c4 < 4; ++c4) {     // 16-byte chunk: one word of codes
+              const int ch = 4 * (k & 1) + c4;
+              const uint4 w4 = codes[4 * i + k];
+              const uint32_t w = c4 == 0 ? w4.x : c4 == 1 ? w4.y : c4 == 2 ? w4.z : w4.w;
+              const uint4 u = q4_word_bf16(w, (sc >> (8 * (c4 / 2))) & 255u);
+              *reinterpret_cast<uint4*>(to + ((ch ^ (row & 7)) << 4)) = u;
+              v[4 * c4] = u.x;
+              v[4 * c4 + 1] = u.y;
+              v[4 * c4 + 2] = u.z;
+              v[4 * c4 + 3] = u.w;
+            }
+            tmem_st16_async(tmem + ((uint32_t)(32 * quarter) << 16) + kRingTmem + 64 * ring + 16 * k, v);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          fence_proxy_async_smem();
+          warp_arrive(&c->full_g[m], lane);
+        }
+        if (more) load(next, i, m);
+      }
     }
   }
 
@@ -1091,6 +1290,8 @@ cudaError_t launch_tree_tc(const TreeArgs& a, bool q4, void* workspace, cudaStre
     while (page % box) box >>= 1;
     if (box >= 8) p.box = box;
   }
+  p.by_tok.set((uint32_t)(a.tok_page > 0 ? a.tok_page : 1));
+  p.by_ent.set((uint32_t)(a.ent_page > 0 ? a.ent_page : 1));
   p.parts = (char*)workspace;
   p.cuts = (int4*)((char*)workspace + (size_t)2 * kMaxCtas * kPartBytes);
   CUtensorMap mq, mp;
@@ -1112,6 +1313,10 @@ cudaError_t launch_tree_tc(const TreeArgs& a, bool q4, void* workspace, cudaStre
     sm_count[dev].store(sms, std::memory_order_relaxed);
     r = cudaFuncSetAttribute(tree_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
     if (r != cudaSuccess) return r;
+    cudaFuncAttributes at;                        // the split waits for registers that the launch must have
+    r = cudaFuncGetAttributes(&at, tree_tc_kernel<true>);
+    if (r != cudaSuccess) return r;
+    if (at.numRegs != kRegsStart) return cudaErrorInvalidDeviceFunction;
     return cudaFuncSetAttribute(tree_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
   });
   if (e != cudaSuccess) return e;
@@ -1119,7 +1324,8 @@ cudaError_t launch_tree_tc(const TreeArgs& a, bool q4, void* workspace, cudaStre
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
   {
     StageTiming ps(16, st);
-    e = launch_overlapped(q4 ? tree_tc_kernel<true> : tree_tc_kernel<false>, dim3(grid), dim3(kThreads), kSmemBytes, st, mq, mp, p);
+    e = launch_overlapped(q4 ? tree_tc_kernel<true> : tree_tc_kernel<false>, dim3(grid),
+                          dim3(q4 ? kThreadsQ4 : kThreads), kSmemBytes, st, mq, mp, p);
     if (e != cudaSuccess) return e;
     note_launch();
   }
