@@ -7,11 +7,18 @@
 // Memory bound: x is read and y written once, the gradient reads x and dy and
 // writes dx.  A head belongs to a group of 1 to 32 lanes that keeps it in
 // registers, so the mean is a butterfly over the group and nothing is read
-// twice; the weight stays in registers over all heads of a block, which are
-// queries or keys alone.  The block forms the angles of its rows once in shared
-// memory while the first heads are in flight.  Weight gradients are summed in
-// registers over all heads of a block, then over its warps; a second kernel adds
-// the blocks' sums in a fixed order, so results repeat bit for bit.
+// twice.  A group takes a short run of consecutive heads, of queries or of keys,
+// that arrive through a ring in shared memory (16-byte asynchronous copies, up to
+// 256 bytes a lane in flight, which registers would not hold): the weight stays in
+// registers and a row's angles are formed once in the run.  Weight gradients are
+// summed in registers over the run, then over the block's warps; a second kernel
+// adds the blocks' sums in a fixed order, so results repeat bit for bit.
+//
+// Times (device, in a replayed graph): 4096 rows of 64 + 1 heads of 512 in bf16 84 us
+// (6.5 TB/s; a block for 16 heads with loads into registers 111), their gradients 131
+// (6.2 TB/s; 310), gradients of 5003 rows of 32 + 8 heads of 128 in fp32, half layout, 62
+// (5.0 TB/s, bound by instructions and shared memory; 101), 16 rows of 64 + 1 heads 2.3
+// (launch).
 #include <math.h>
 
 #include "common.cuh"
@@ -23,9 +30,8 @@ namespace v4 {
 
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kMaxAngles = 1024;                 // (row, pair) angles of a tile
-constexpr int kGradBlocks = 912;                 // six for each of 152 SMs
+constexpr int kThreads = 128, kWarps = kThreads / 32;
+constexpr int kMaxBlocks = 4864;                 // of the gradient: each leaves a row of sums
 
 struct Part {
   const void* x;
@@ -33,9 +39,9 @@ struct Part {
   const float* w;                                // null: ones
   void* out;                                     // y or dx
   long long xr, xh, gr, gh, yr, yh;              // strides in elements
-  int heads, rb, hb;                             // rows and heads of a tile
-  int head_tiles, tiles, blocks;
-  FastDiv by_tiles, by_hb;
+  long long items;                               // (row, head) pairs
+  int heads, chunk, blocks;                      // chunk: items of a group
+  FastDiv by_heads;
 };
 
 struct Args {
@@ -43,179 +49,251 @@ struct Args {
   const int32_t* pos;
   const float* inv_freq;
   float* partial;                                // [blocks of both parts][dim]
-  long long rows;
   float eps, inv_dim;
   int dim, units, lg;                            // units of eight, log2 of a group's lanes
   int R, begin;                                  // in elements
-  FastDiv by_half;
 };
 
-// Heads that a group has in flight: up to 64 bytes a lane of each input.
-template <typename T, int U, bool kGrad>
-constexpr int ahead() {
-  const int n = 8 / (U * (int)sizeof(T)) / (kGrad ? 2 : 1);
-  return n < 1 ? 1 : n;
+// What a kernel keeps in shared memory for each warp: a ring of raw heads (x, and dy
+// for the gradient), the angles of each group's row, and for the forward half layout
+// the values that partners exchange.  Up to 256 bytes a lane are in flight.
+template <typename T, int U, bool kHalf, bool kGrad>
+struct Lay {
+  static constexpr int kTensors = kGrad ? 2 : 1;
+  static constexpr int kHead = 256 * U * (int)sizeof(T);          // bytes of a warp's heads
+  static constexpr int kWant = 256 / (kTensors * U * 8 * (int)sizeof(T));
+  static constexpr int kStages = kWant < 2 ? 2 : kWant > 4 ? 4 : kWant;
+  static constexpr int kTable = kStages * kTensors * kHead;       // offset of the angles
+  static constexpr int kStrip = kTable + 128 * U * (int)sizeof(float2);
+  static constexpr int kWarp = kStrip + (kHalf && !kGrad ? 256 * U * (int)sizeof(float) : 0);
+  static constexpr int kBlocks = kGrad ? (U == 1 ? 5 : U == 2 ? 4 : 2) : U > 2 ? 3 : 8;      // resident, without spills
+};
+
+__device__ __forceinline__ void copy_16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
+}
+
+// Two fp32 operations in one instruction: the kernels are as near to the issue rate as
+// to HBM's (the gradient of a head of 512: 309 instructions, 433 without).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+
+// Eight elements as pairs.
+__device__ __forceinline__ void load8(const bf16* p, float2* v) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+__device__ __forceinline__ void load8(const float* p, float2* v) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = make_float2(a.x, a.y);
+  v[1] = make_float2(a.z, a.w);
+  v[2] = make_float2(b.x, b.y);
+  v[3] = make_float2(b.z, b.w);
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float2* v) {
+  const float f[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
+  v4::store8(p, f);
 }
 
 // U: units of a lane.  kHalf: pairs half a rotation apart.
 template <typename T, int U, bool kHalf, bool kGrad>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const Args p) {
-  constexpr int K = ahead<T, U, kGrad>();
-  __shared__ float2 s_cs[kMaxAngles];
-  __shared__ __align__(16) float s_x[kHalf || kGrad ? kThreads * 8 * U : 4];
+__global__ void __launch_bounds__(kThreads, (Lay<T, U, kHalf, kGrad>::kBlocks)) norm_rope_kernel(const Args p) {
+  using L = Lay<T, U, kHalf, kGrad>;
+  constexpr int S = L::kStages, kWord = (int)sizeof(T) / 2;       // 16-byte words of a unit
+  extern __shared__ __align__(16) uint8_t smem[];
   after_previous();
-  const int G = 1 << p.lg;
-  const int lane = threadIdx.x & (G - 1), grp = threadIdx.x >> p.lg, groups = kThreads >> p.lg;
+  const int warp = threadIdx.x >> 5;
+  const int G = 1 << p.lg, lane = threadIdx.x & (G - 1), grp = (threadIdx.x & 31) >> p.lg;
   const bool second = blockIdx.x >= (unsigned)p.part[0].blocks;
   const Part& q = p.part[second];
   const int half = p.R >> 1;
   const int v0 = p.begin >> 3, nv = p.R >> 3;    // rotated units
-  float* strip = s_x + (kHalf ? grp * (G * 8 * U) : 0);
+  uint8_t* mine = smem + warp * L::kWarp;
+  uint8_t* ring = mine + grp * (G * U * 8 * (int)sizeof(T));
+  float2* cs = reinterpret_cast<float2*>(mine + L::kTable) + grp * (G * U * 4);
+  float* strip = reinterpret_cast<float*>(mine + L::kStrip) + grp * (G * U * 8);
 
-  float w[U][8], dw[kGrad ? U : 1][8];
+  float2 w[U][4], dw[kGrad ? U : 1][4];
   int rot[U];                                    // number of a rotated unit, -1: not rotated
+  bool here[U];
 #pragma unroll
   for (int s = 0; s < U; ++s) {
     const int u = lane + G * s;
+    here[s] = u < p.units;
     rot[s] = u >= v0 && u < v0 + nv ? u - v0 : -1;
-    if (q.w != nullptr && u < p.units) {
+    if (q.w != nullptr && here[s]) {
       load8(q.w + 8 * u, w[s]);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[s][e] = 1.f;
+      for (int e = 0; e < 4; ++e) w[s][e] = make_float2(1.f, 1.f);
     }
     if (kGrad) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) dw[s][e] = 0.f;
+      for (int e = 0; e < 4; ++e) dw[s][e] = make_float2(0.f, 0.f);
     }
   }
+  // words of the ring behind a head's last stay zero
+  for (int i = p.units * kWord + lane; i < G * U * kWord; i += G)
+    for (int k = 0; k < S * L::kTensors; ++k) reinterpret_cast<uint4*>(ring + k * L::kHead)[i] = make_uint4(0, 0, 0, 0);
 
-  for (int tile = blockIdx.x - (second ? p.part[0].blocks : 0); tile < q.tiles; tile += q.blocks) {
-    const int rt = (int)q.by_tiles.div((uint32_t)tile);
-    const int head0 = (tile - rt * q.head_tiles) * q.hb;
-    const long long row0 = (long long)rt * q.rb;
-    const int nr = (int)min((long long)q.rb, p.rows - row0), nh = min(q.hb, q.heads - head0);
-    const int n = nr * q.hb;
-    const T* x = reinterpret_cast<const T*>(q.x) + row0 * q.xr + (long long)head0 * q.xh;
-    const T* dy = kGrad ? reinterpret_cast<const T*>(q.dy) + row0 * q.gr + (long long)head0 * q.gh : nullptr;
-    T* out = reinterpret_cast<T*>(q.out) + row0 * q.yr + (long long)head0 * q.yh;
-    bool angles = half == 0;                     // formed once the first loads are in flight
-    if (kGrad) __syncthreads();                  // the tile before has used its angles
-    for (int base = 0; base < n; base += groups * K) {
-      Raw<T> a[K][U], d[kGrad ? K : 1][U];
-      int row[K], head[K];
-      bool live[K];
+  // this group's items: consecutive heads, so that a row's angles are formed once
+  const long long first =
+      ((long long)((blockIdx.x - (second ? p.part[0].blocks : 0)) * kWarps + warp) * (32 >> p.lg) + grp) * q.chunk;
+  const int n = (int)max(0ll, min((long long)q.chunk, q.items - first));
+  int row = n > 0 ? (int)q.by_heads.div((uint32_t)first) : 0, head = n > 0 ? (int)(first - (long long)row * q.heads) : 0;
+  const T* x = reinterpret_cast<const T*>(q.x) + row * q.xr + head * q.xh + 8 / kWord * lane;
+  const T* dy = kGrad ? reinterpret_cast<const T*>(q.dy) + row * q.gr + head * q.gh + 8 / kWord * lane : nullptr;
+  T* out = reinterpret_cast<T*>(q.out) + row * q.yr + head * q.yh + 8 * lane;
+  const long long xw = q.xr - (q.heads - 1) * q.xh, gw = q.gr - (q.heads - 1) * q.gh, yw = q.yr - (q.heads - 1) * q.yh;
+  int ihead = head;                              // of the next item that is asked for
+  auto ask = [&](int j) {
+    if (j < n) {
+      uint8_t* to = ring + (j % S) * (L::kTensors * L::kHead);
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int i = base + k * groups + grp;
-        row[k] = (int)q.by_hb.div((uint32_t)i);
-        head[k] = i - row[k] * q.hb;
-        live[k] = i < n && head[k] < nh;
-#pragma unroll
-        for (int s = 0; s < U; ++s) {
-          const int u = lane + G * s;
-          if (live[k] && u < p.units) {
-            a[k][s].load(x + row[k] * q.xr + head[k] * q.xh + 8 * u);
-            if (kGrad) d[k][s].load(dy + row[k] * q.gr + head[k] * q.gh + 8 * u);
-          } else {
-#pragma unroll
-            for (int e = 0; e < (int)(sizeof(T) / 2); ++e) {
-              a[k][s].w[e] = make_uint4(0, 0, 0, 0);
-              if (kGrad) d[k][s].w[e] = make_uint4(0, 0, 0, 0);
-            }
-          }
+      for (int k = 0; k < U * kWord; ++k) {
+        if (lane + G * k < p.units * kWord) {
+          uint8_t* word = to + 16 * (lane + G * k);
+          copy_16(word, x + 8 / kWord * G * k);
+          if (kGrad) copy_16(word + L::kHead, dy + 8 / kWord * G * k);
         }
       }
-      if (!angles) {
-        angles = true;
-        for (int j = threadIdx.x; j < nr * half; j += kThreads) {
-          const int r = (int)p.by_half.div((uint32_t)j), c = j - r * half;
-          float cs, sn;
-          turn_cos_sin(p.pos[row0 + r], turn_fraction(p.inv_freq[c]), &cs, &sn);
-          s_cs[j] = make_float2(cs, kGrad ? -sn : sn);
-        }
-        __syncthreads();
-      }
+      const bool wrap = ++ihead == q.heads;
+      x += wrap ? xw : q.xh;
+      if (kGrad) dy += wrap ? gw : q.gh;
+      if (wrap) ihead = 0;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const float2* cs = s_cs + (live[k] ? row[k] : 0) * half;
-        // the tensor that is turned: y before its rotation, or the gradient
-        auto turn = [&](float (*v)[8]) {
-          if (kHalf) {
-            __syncwarp();
-#pragma unroll
-            for (int s = 0; s < U; ++s)
-              if (rot[s] >= 0) store8(strip + 8 * rot[s], v[s]);
-            __syncwarp();
-          }
-#pragma unroll
-          for (int s = 0; s < U; ++s) {
-            if (rot[s] < 0) continue;
-            if (kHalf) {
-              const bool low = rot[s] < nv / 2;
-              const int j = low ? rot[s] : rot[s] - nv / 2;
-              float o[8];
-              load8(strip + 8 * (low ? rot[s] + nv / 2 : j), o);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float2 c = cs[8 * j + e];
-                v[s][e] = low ? v[s][e] * c.x - o[e] * c.y : o[e] * c.y + v[s][e] * c.x;
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 c = cs[4 * rot[s] + e];
-                rot_pair(v[s][2 * e], v[s][2 * e + 1], c.x, c.y);
-              }
-            }
-          }
-        };
-        float v[U][8], g[kGrad ? U : 1][8];
-        float sq = 0.f, dot = 0.f;
-#pragma unroll
-        for (int s = 0; s < U; ++s) {
-          a[k][s].floats(v[s]);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) sq = fmaf(v[s][e], v[s][e], sq);
-        }
-        if (kGrad) {
-#pragma unroll
-          for (int s = 0; s < U; ++s) d[k][s].floats(g[s]);
-          turn(g);
-#pragma unroll
-          for (int s = 0; s < U; ++s)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dot = fmaf(w[s][e] * g[s][e], v[s][e], dot);
-        }
-        for (int o = G >> 1; o > 0; o >>= 1) {
-          sq += __shfl_xor_sync(0xffffffffu, sq, o);
-          if (kGrad) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        }
-        const float r = 1.f / sqrtf(fmaf(sq, p.inv_dim, p.eps));
-        if (kGrad) {
-          const float m = dot * p.inv_dim * (r * r);
-#pragma unroll
-          for (int s = 0; s < U; ++s)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              if (live[k]) dw[s][e] = fmaf(g[s][e], v[s][e] * r, dw[s][e]);
-              v[s][e] = r * (w[s][e] * g[s][e] - v[s][e] * m);
-            }
-        } else {
-#pragma unroll
-          for (int s = 0; s < U; ++s)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[s][e] *= r * w[s][e];
-          turn(v);
-        }
-        if (!live[k]) continue;
-#pragma unroll
-        for (int s = 0; s < U; ++s) {
-          const int u = lane + G * s;
-          if (u < p.units) store8(out + row[k] * q.yr + head[k] * q.yh + 8 * u, v[s]);
-        }
+  for (int j = 0; j < S - 1; ++j) ask(j);
+  int formed = -1;                               // row of the angles
+  const int most = q.chunk;                      // the same for all lanes
+  for (int j = 0; j < most; ++j) {
+    ask(j + S - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+    const bool live = j < n;
+    if (live && half > 0 && row != formed) {
+      formed = row;
+      for (int c = lane; c < half; c += G) {
+        float co, si;
+        turn_cos_sin(p.pos[row], turn_fraction(p.inv_freq[c]), &co, &si);
+        // two pairs to a word, words of a unit apart: neighbouring lanes read neighbouring words
+        constexpr int kPairs = kHalf ? 8 : 4;
+        const int unit = c / kPairs, e = c % kPairs;
+        cs[((e >> 1) * (half / kPairs) + unit) * 2 + (e & 1)] = make_float2(co, kGrad ? -si : si);
       }
     }
+    __syncwarp();
+    const T* at = reinterpret_cast<const T*>(ring + (j % S) * (L::kTensors * L::kHead));
+    const T* gat = reinterpret_cast<const T*>(reinterpret_cast<const uint8_t*>(at) + L::kHead);
+    float2 v[U][4], g[kGrad ? U : 1][4];
+    float2 sq = make_float2(0.f, 0.f), dot = make_float2(0.f, 0.f);
+    // one unit of the tensor that is turned: y before its rotation, or dy.  o: its partners'.
+    auto turn = [&](int s, float2* a, const float2* o) {
+      if (kHalf) {
+        const bool low = rot[s] < nv / 2;
+        const float4* c = reinterpret_cast<const float4*>(cs) + (low ? rot[s] : rot[s] - nv / 2);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float4 t = c[e * (nv / 2)];
+          a[e] = make_float2(fmaf(o[e].x, low ? -t.y : t.y, a[e].x * t.x), fmaf(o[e].y, low ? -t.w : t.w, a[e].y * t.z));
+        }
+      } else {
+        const float4* c = reinterpret_cast<const float4*>(cs) + rot[s];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float4 t = c[e * nv];
+          rot_pair(a[2 * e].x, a[2 * e].y, t.x, t.y);
+          rot_pair(a[2 * e + 1].x, a[2 * e + 1].y, t.z, t.w);
+        }
+      }
+    };
+    // the unit of the partners, kHalf alone
+    auto partner = [&](int s) { return rot[s] < nv / 2 ? rot[s] + nv / 2 : rot[s] - nv / 2; };
+#pragma unroll
+    for (int s = 0; s < U; ++s) {
+      const int u = lane + G * s;
+      load8(at + 8 * u, v[s]);
+      if (kGrad) {
+        load8(gat + 8 * u, g[s]);
+        if (rot[s] >= 0) {
+          float2 o[4];
+          if (kHalf) load8(gat + 8 * (v0 + partner(s)), o);
+          turn(s, g[s], o);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        sq = fma2(v[s][e], v[s][e], sq);
+        if (kGrad) dot = fma2(mul2(w[s][e], g[s][e]), v[s][e], dot);
+      }
+    }
+    float t_sq = sq.x + sq.y, t_dot = dot.x + dot.y;
+    for (int o = G >> 1; o > 0; o >>= 1) {
+      t_sq += __shfl_xor_sync(0xffffffffu, t_sq, o);
+      if (kGrad) t_dot += __shfl_xor_sync(0xffffffffu, t_dot, o);
+    }
+    const float r = rsqrtf(fmaf(t_sq, p.inv_dim, p.eps));
+    const float2 r2 = make_float2(r, r);
+    if (kGrad) {
+      const float m = -t_dot * p.inv_dim * (r * r) * r;
+      const float2 m2 = make_float2(m, m);
+      if (live) {                                // r of nothing may be infinite
+#pragma unroll
+        for (int s = 0; s < U; ++s)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            dw[s][e] = fma2(g[s][e], mul2(v[s][e], r2), dw[s][e]);
+            v[s][e] = fma2(mul2(w[s][e], g[s][e]), r2, mul2(v[s][e], m2));
+          }
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < U; ++s)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[s][e] = mul2(mul2(v[s][e], r2), w[s][e]);
+      if (kHalf) {
+#pragma unroll
+        for (int s = 0; s < U; ++s)
+          if (rot[s] >= 0) store8(strip + 8 * rot[s], v[s]);
+        __syncwarp();
+      }
+#pragma unroll
+      for (int s = 0; s < U; ++s) {
+        if (rot[s] < 0) continue;
+        float2 o[4];
+        if (kHalf) load8(strip + 8 * partner(s), o);
+        turn(s, v[s], o);
+      }
+    }
+    if (live) {
+#pragma unroll
+      for (int s = 0; s < U; ++s)
+        if (here[s]) store8(out + 8 * G * s, v[s]);
+      const bool wrap = ++head == q.heads;
+      out += wrap ? yw : q.yh;
+      if (wrap) {
+        head = 0;
+        ++row;
+      }
+    }
+    __syncwarp();                                // the slot, the angles and the strip are read
   }
 
   if (kGrad) {
@@ -223,26 +301,35 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const Args p) {
 #pragma unroll
     for (int s = 0; s < U; ++s)
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        for (int o = G; o < 32; o <<= 1) dw[s][e] += __shfl_xor_sync(0xffffffffu, dw[s][e], o);
-    __syncthreads();                             // the strips are free
-    const int warp = threadIdx.x >> 5, width = G * 8 * U;
-    if ((threadIdx.x & 31) < G) {
+      for (int e = 0; e < 4; ++e)
+        for (int o = G; o < 32; o <<= 1) {
+          dw[s][e].x += __shfl_xor_sync(0xffffffffu, dw[s][e].x, o);
+          dw[s][e].y += __shfl_xor_sync(0xffffffffu, dw[s][e].y, o);
+        }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();                             // the rings are free
+    float* sums = reinterpret_cast<float*>(smem);
+    const int width = G * 8 * U;
+    if (grp == 0) {
 #pragma unroll
-      for (int s = 0; s < U; ++s) store8(s_x + warp * width + 8 * (lane + G * s), dw[s]);
+      for (int s = 0; s < U; ++s) store8(sums + warp * width + 8 * (lane + G * s), dw[s]);
     }
     __syncthreads();
     float* to = p.partial + (size_t)blockIdx.x * p.dim;
     for (int c = threadIdx.x; c < p.dim; c += kThreads) {
       float t = 0.f;
 #pragma unroll
-      for (int i = 0; i < kThreads / 32; ++i) t += s_x[i * width + c];
+      for (int i = 0; i < kWarps; ++i) t += sums[i * width + c];
       to[c] = t;
     }
   }
 }
 
-// dw[c] = sum of the blocks' sums: 32 columns a block, a warp every 32nd row.
+// dw[c] = sum of the blocks' sums.  A cluster takes 32 columns, its blocks every eighth
+// row of 1024-row steps, and adds up through distributed shared memory: always in the
+// same order.
+constexpr int kSumThreads = 1024, kSumCluster = 8, kSumRows = kSumThreads / 8;
+
 struct SumArgs {
   const float* partial;
   float* out[2];
@@ -250,41 +337,87 @@ struct SumArgs {
   int dim;
 };
 
-__global__ void __launch_bounds__(1024) norm_weight_kernel(const SumArgs p) {
-  __shared__ float s_t[32][33];
+__global__ void __launch_bounds__(kSumThreads) norm_weight_kernel(const SumArgs p) {
+  __shared__ float4 s_t[kSumThreads / 32][8];
+  __shared__ float s_sum[32];
   after_previous();
-  const int part = blockIdx.y;
-  if (p.out[part] == nullptr) return;
-  const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + cx;
-  float t = 0.f;
-  if (c < p.dim) {
-    const float* from = p.partial + (size_t)p.first[part] * p.dim + c;
+  const int part = blockIdx.z, rank = blockIdx.x;         // the cluster runs along x
+  if (p.out[part] == nullptr) return;                     // the whole cluster
+  const int c4 = threadIdx.x & 7, r0 = rank * kSumRows + (threadIdx.x >> 3), warp = threadIdx.x >> 5;
+  const int col = blockIdx.y * 32 + 4 * c4;
+  float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (col < p.dim) {
+    const float* from = p.partial + (size_t)p.first[part] * p.dim + col;
 #pragma unroll 4
-    for (int b = ry; b < p.blocks[part]; b += 32) t += from[(size_t)b * p.dim];
+    for (int b = r0; b < p.blocks[part]; b += kSumRows * kSumCluster) {
+      const float4 v = *reinterpret_cast<const float4*>(from + (size_t)b * p.dim);
+      t.x += v.x;
+      t.y += v.y;
+      t.z += v.z;
+      t.w += v.w;
+    }
   }
-  s_t[ry][cx] = t;
-  __syncthreads();
-  t = s_t[cx][ry];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-  if (cx == 0 && blockIdx.x * 32 + ry < p.dim) p.out[part][blockIdx.x * 32 + ry] = t;
+  for (int o = 8; o < 32; o <<= 1) {
+    t.x += __shfl_xor_sync(0xffffffffu, t.x, o);
+    t.y += __shfl_xor_sync(0xffffffffu, t.y, o);
+    t.z += __shfl_xor_sync(0xffffffffu, t.z, o);
+    t.w += __shfl_xor_sync(0xffffffffu, t.w, o);
+  }
+  if ((threadIdx.x & 31) < 8) s_t[warp][c4] = t;
+  __syncthreads();
+  // 32 columns x 32 warps' sums, one column a warp
+  float v = reinterpret_cast<const float*>(s_t[threadIdx.x & 31])[warp];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) s_sum[warp] = v;
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (rank == 0 && threadIdx.x < 32 && blockIdx.y * 32 + threadIdx.x < p.dim) {
+    float sum = 0.f;
+    for (int k = 0; k < kSumCluster; ++k) {
+      uint32_t at;
+      float other;
+      asm("mapa.shared::cluster.u32 %0, %1, %2;"
+          : "=r"(at)
+          : "r"((uint32_t)__cvta_generic_to_shared(&s_sum[threadIdx.x])), "r"(k));
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other) : "r"(at) : "memory");
+      sum += other;
+    }
+    p.out[part][blockIdx.y * 32 + threadIdx.x] = sum;
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-template <typename T, int U, bool kGrad>
-void (*kernel_of(bool half))(const Args) {
-  return half ? norm_rope_kernel<T, U, true, kGrad> : norm_rope_kernel<T, U, false, kGrad>;
+struct Kernel {
+  void (*run)(const Args);
+  int smem, blocks;                              // of a block, resident on an SM
+};
+
+template <typename T, int U, bool kHalf, bool kGrad>
+cudaError_t kernel_of(Kernel* k) {
+  using L = Lay<T, U, kHalf, kGrad>;
+  static_assert(L::kWarp >= 256 * U * (int)sizeof(float) || !kGrad, "the weight sums fit in the rings");
+  k->run = norm_rope_kernel<T, U, kHalf, kGrad>;
+  k->smem = kWarps * L::kWarp;
+  k->blocks = L::kBlocks;
+  while (k->blocks > 1 && k->blocks * (k->smem + 1024) > 227 * 1024) --k->blocks;
+  static OncePerDevice once;
+  return once.run([] {
+    return cudaFuncSetAttribute(norm_rope_kernel<T, U, kHalf, kGrad>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kWarps * Lay<T, U, kHalf, kGrad>::kWarp);
+  });
 }
 
 template <typename T, bool kGrad>
-void (*kernel_of(int units_a_lane, bool half))(const Args) {
-  return units_a_lane == 1 ? kernel_of<T, 1, kGrad>(half)
-                           : units_a_lane == 2 ? kernel_of<T, 2, kGrad>(half) : kernel_of<T, 4, kGrad>(half);
+cudaError_t kernel_of(int units_a_lane, bool half, Kernel* k) {
+  if (units_a_lane == 1) return half ? kernel_of<T, 1, true, kGrad>(k) : kernel_of<T, 1, false, kGrad>(k);
+  if (units_a_lane == 2) return half ? kernel_of<T, 2, true, kGrad>(k) : kernel_of<T, 2, false, kGrad>(k);
+  return half ? kernel_of<T, 4, true, kGrad>(k) : kernel_of<T, 4, false, kGrad>(k);
 }
 
 }  // namespace
 
-size_t norm_rope_workspace(int dim) { return (size_t)(kGradBlocks + 2) * dim * sizeof(float); }
+size_t norm_rope_workspace(int dim) { return (size_t)(kMaxBlocks + 2) * dim * sizeof(float); }
 
 cudaError_t launch_norm_rope(const NormCall& c, cudaStream_t st) {
   const bool grad = c.grad;
@@ -292,31 +425,35 @@ cudaError_t launch_norm_rope(const NormCall& c, cudaStream_t st) {
   p.pos = c.pos;
   p.inv_freq = c.inv_freq;
   p.partial = (float*)c.workspace;
-  p.rows = c.rows;
   p.eps = c.eps;
   p.inv_dim = 1.f / (float)c.dim;
   p.dim = c.dim;
   p.units = c.dim / 8;
+  p.R = c.rope_dim;
+  p.begin = c.rope_begin;
   // lanes of a head: the next power of two of its units, a lane holding up to four
   const int U = p.units <= 32 ? 1 : p.units <= 64 ? 2 : 4;
   p.lg = 0;
   while ((U << p.lg) < p.units) ++p.lg;
-  p.R = c.rope_dim;
-  p.begin = c.rope_begin;
-  const int half = p.R / 2;
-  p.by_half.set((uint32_t)(half > 0 ? half : 1));
   const int groups = kThreads >> p.lg;
-  const int es = c.dtype == V4_BF16 ? 2 : 4;
-  // Heads of a tile: four rounds of loads, one while that would leave SMs without a
-  // block; the gradient's blocks walk tiles of 16 rounds.
-  int k = 8 / (U * es) / (grad ? 2 : 1);
-  if (k < 1) k = 1;
+  Kernel k;
+  cudaError_t e;
+  if (c.dtype == V4_BF16) e = grad ? kernel_of<bf16, true>(U, c.half, &k) : kernel_of<bf16, false>(U, c.half, &k);
+  else e = grad ? kernel_of<float, true>(U, c.half, &k) : kernel_of<float, false>(U, c.half, &k);
+  if (e != cudaSuccess) return e;
+  // A group takes a run of about `most` heads, such that the blocks fill whole waves, and
+  // a shorter one while SMs would be left without blocks.  Runs as long as one wave allows
+  // were slower, since SMs do not progress alike (4096 x 64 heads of 512: 120 against 84
+  // us), and so were shorter ones in the gradient, whose blocks each leave sums (run 4: 220
+  // us, 8 and 16: 131, 32: 141).
+  const long long wave = 152ll * k.blocks * groups, most = grad ? 16 : 8;
   long long all = 0;
   for (int i = 0; i < 2; ++i) all += c.rows * (c.part[i].x ? c.part[i].heads : 0);
-  int want = groups * k * (grad ? 16 : 4);
-  while (want > groups && all / want < (grad ? kGradBlocks : 608)) want /= 2;
-  if (want < groups) want = groups;
-  long long first = 0, work[2] = {0, 0};
+  long long waves = (all + most * wave / 2) / (most * wave);
+  if (waves < 1) waves = 1;
+  long long run = (all + waves * wave - 1) / (waves * wave);
+  if (grad && all > run * groups * (kMaxBlocks - 2)) run = all / ((long long)groups * (kMaxBlocks - 2)) + 1;
+  if (run < 1) run = 1;
   for (int i = 0; i < 2; ++i) {
     Part& q = p.part[i];
     const NormPartCall& s = c.part[i];
@@ -331,39 +468,14 @@ cudaError_t launch_norm_rope(const NormCall& c, cudaStream_t st) {
     q.gh = s.dy_head_stride;
     q.yr = s.out_row_stride;
     q.yh = s.out_head_stride;
-    q.rb = q.hb = q.head_tiles = 1;
-    q.tiles = q.blocks = 0;
-    if (q.heads > 0) {
-      q.hb = q.heads < want ? q.heads : want;
-      long long rb = q.hb == q.heads ? want / q.heads : 1;
-      if (half > 0 && rb > kMaxAngles / half) rb = kMaxAngles / half;
-      if (rb < 1) rb = 1;
-      if (rb > c.rows) rb = c.rows;
-      q.rb = (int)rb;
-      q.head_tiles = (q.heads + q.hb - 1) / q.hb;
-      const long long tiles = ((c.rows + rb - 1) / rb) * q.head_tiles;
-      if (tiles > 0x7FFFFFFF / 2) return cudaErrorInvalidValue;
-      q.tiles = q.blocks = (int)tiles;
-      work[i] = tiles;
-    }
-    q.by_tiles.set((uint32_t)q.head_tiles);
-    q.by_hb.set((uint32_t)q.hb);
-    first += q.blocks;
-  }
-  if (grad && work[0] + work[1] > kGradBlocks) {
-    // blocks in proportion to the parts' tiles, one at least
-    for (int i = 0; i < 2; ++i) {
-      const long long n = work[i] * kGradBlocks / (work[0] + work[1]);
-      p.part[i].blocks = work[i] == 0 ? 0 : n < 1 ? 1 : (int)n;
-    }
+    q.items = c.rows * q.heads;
+    q.by_heads.set((uint32_t)(q.heads > 0 ? q.heads : 1));
+    q.chunk = (int)run;
+    q.blocks = (int)((q.items + run * groups - 1) / (run * groups));
   }
   const int blocks = p.part[0].blocks + p.part[1].blocks;
-  void (*kern)(const Args);
-  if (c.dtype == V4_BF16) kern = grad ? kernel_of<bf16, true>(U, c.half) : kernel_of<bf16, false>(U, c.half);
-  else kern = grad ? kernel_of<float, true>(U, c.half) : kernel_of<float, false>(U, c.half);
-  cudaError_t e = cudaSuccess;
   if (blocks > 0) {                              // else weight gradients of no rows: zeros
-    e = launch_overlapped(kern, dim3((unsigned)blocks), dim3(kThreads), 0, st, p);
+    e = launch_overlapped(k.run, dim3((unsigned)blocks), dim3(kThreads), (size_t)k.smem, st, p);
     if (e != cudaSuccess) return e;
     note_launch();
   }
@@ -377,7 +489,19 @@ cudaError_t launch_norm_rope(const NormCall& c, cudaStream_t st) {
     s.blocks[i] = p.part[i].blocks;
   }
   if (s.out[0] == nullptr && s.out[1] == nullptr) return cudaSuccess;
-  e = launch_overlapped(norm_weight_kernel, dim3((unsigned)((c.dim + 31) / 32), 2), dim3(1024), 0, st, s);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kSumCluster, (unsigned)((c.dim + 31) / 32), 2);
+  cfg.blockDim = dim3(kSumThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = kSumCluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, norm_weight_kernel, (const SumArgs)s);
   if (e == cudaSuccess) note_launch();
   return e;
 }
