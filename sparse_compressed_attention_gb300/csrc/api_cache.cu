@@ -343,7 +343,8 @@ v4_status v4_pages_compact(void* cache, int32_t layers, int64_t layer_stride, in
                            const int32_t* count, const int32_t* keep, int32_t max_keep, void* stream) {
   TRY(check_cache(cache, layers, layer_stride, pages, page_size, row_bytes));
   TRY(check_table(table, "table", n, blocks, page_size));
-  if (max_keep < 0 || (int64_t)n * max_keep > 0x7FFFFFFF) return bad("keep must have at most 2^31 - 1 entries");
+  if (max_keep < 0 || max_keep > (1 << 30) || (int64_t)n * max_keep > 0x7FFFFFFF)
+    return bad("keep must have at most 2^31 - 1 entries, 2^30 for a sequence");
   if (row_bytes / 64 > 65535) return bad("a row has more than 4 MB");
   if (n == 0 || max_keep == 0) return V4_OK;
   TRY(check_ptr(base, "base"));

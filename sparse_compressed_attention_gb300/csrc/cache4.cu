@@ -5,7 +5,9 @@
 //   even), code = 8 + clamp(round_to_even(x / scale), -8, 7)
 //
 // Memory bound: a thread takes one group of 16 values, so its maximum needs no
-// exchange, and a row's threads write neighbouring words.
+// exchange, and a row's threads write neighbouring words.  16384 rows of 512 in bf16 are
+// written and read back in 11.5 us (3.7 TB/s, of which 3 us are the two launches; 15.6
+// with a division for each value), 64 rows in 2.8 (launches).
 #include <math.h>
 
 #include "common.cuh"
@@ -30,12 +32,35 @@ struct Q4Args {
   FastDiv by_groups;
 };
 
-// One scale byte: the quotients are IEEE divisions, whose result lies on the same
-// side of every tie as the exact quotient (ties have at most five significant bits).
+// The byte of the scale nearest to amax / 7.  An IEEE quotient lies on the same side
+// of every tie as the exact one (ties have at most five significant bits).
 __device__ __forceinline__ uint32_t scale_byte(float amax) {
   const uint32_t f = __float_as_uint(__fdiv_rn(amax, 7.f));
   const int b = (int)((f + 0x7FFFFu + ((f >> 20) & 1u)) >> 20) - (107 << 3);
   return (uint32_t)min(max(b, 0), 255);
+}
+
+// Two words of codes of sixteen values.  x / scale is the correctly rounded quotient by
+// Markstein's theorem: with inv the rounded reciprocal, q = x inv needs one step of its
+// exact remainder.  Values outside [-8, 7] scales are cut before, exactly.  Adding 1.5
+// 2^23 + 8 rounds to an integer, ties to even, and leaves the code in the low bits: the
+// words are sums of those floats' bits, less what the constant adds.
+__device__ __forceinline__ uint2 pack_codes(const float* v, float scale) {
+  const float inv = __frcp_rn(scale), lo = -8.f * scale, hi = 7.f * scale;
+  uint32_t w[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    w[k] = 0u - 0x4B400000u * 0x11111111u;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float x = fminf(fmaxf(v[8 * k + e], lo), hi);
+      const float q0 = x * inv;
+      const float q = fmaf(fmaf(-q0, scale, x), inv, q0);
+      const int nib = (e & 1) * 4 + (e >> 1);
+      w[k] += __float_as_uint(q + 12582920.f) << (4 * nib);
+    }
+  }
+  return make_uint2(w[0], w[1]);
 }
 
 template <typename T, int K>
@@ -68,25 +93,37 @@ __global__ void __launch_bounds__(kThreads) q4_append_kernel(const Q4Args p) {
     float v[16];
     a[k][0].floats(v);
     a[k][1].floats(v + 8);
-    float amax = 0.f;
+    uint32_t top = 0;                              // bits of the largest magnitude: NaN lies above infinity
 #pragma unroll
-    for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(v[e]));        // drops NaN
-    const uint32_t b = scale_byte(fminf(amax, 1e30f));
-    const float scale = q4_scale(b);
-    uint32_t w[2] = {0, 0};
+    for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+    if (top > 0x7F800000u) {                       // NaN counts as zero
+      top = 0;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      // NaN becomes zero: fmaxf and fminf drop it, but not to the same side
-      const float q = v[e] == v[e] ? fminf(fmaxf(rintf(__fdiv_rn(v[e], scale)), -8.f), 7.f) : 0.f;
-      const int nib = (e & 1) * 4 + ((e & 7) >> 1);
-      w[e >> 3] |= (uint32_t)((int)q + 8) << (4 * nib);
+      for (int e = 0; e < 16; ++e) {
+        if (v[e] != v[e]) v[e] = 0.f;
+        top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+      }
     }
+    const uint32_t b = scale_byte(fminf(__uint_as_float(top), 1e30f));
     uint8_t* row = p.cache + (size_t)at[k] * p.row_bytes;
-    *reinterpret_cast<uint2*>(row + 8 * g[k]) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(row + 8 * g[k]) = pack_codes(v, q4_scale(b));
     row[p.D / 2 + g[k]] = (uint8_t)b;
     if (g[k] == 0)
       for (int i = p.D / 2 + per; i < p.row_bytes; ++i) row[i] = 0;
   }
+}
+
+// Eight values, exact in bf16.
+__device__ __forceinline__ void store_values(bf16* to, uint4 v) { *reinterpret_cast<uint4*>(to) = v; }
+__device__ __forceinline__ void store_values(float* to, uint4 v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+  store8(to, f);
 }
 
 template <typename T, int K>
@@ -119,12 +156,8 @@ __global__ void __launch_bounds__(kThreads) q4_read_kernel(const Q4Args p) {
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     if (to[k] == nullptr) continue;
-    const float scale = q4_scale(b[k]);
-    float v[16];
-    q4_values(w[k].x, scale, v);
-    q4_values(w[k].y, scale, v + 8);
-    store8(to[k], v);
-    store8(to[k] + 8, v + 8);
+    store_values(to[k], q4_word_bf16(w[k].x, b[k]));
+    store_values(to[k] + 8, q4_word_bf16(w[k].y, b[k]));
   }
 }
 

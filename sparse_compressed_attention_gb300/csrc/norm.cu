@@ -156,7 +156,8 @@ __global__ void __launch_bounds__(kThreads, (Lay<T, U, kHalf, kGrad>::kBlocks)) 
   const long long first =
       ((long long)((blockIdx.x - (second ? p.part[0].blocks : 0)) * kWarps + warp) * (32 >> p.lg) + grp) * q.chunk;
   const int n = (int)max(0ll, min((long long)q.chunk, q.items - first));
-  int row = n > 0 ? (int)q.by_heads.div((uint32_t)first) : 0, head = n > 0 ? (int)(first - (long long)row * q.heads) : 0;
+  int row = n > 0 ? (int)q.by_heads.div((uint32_t)first) : 0;
+  int head = n > 0 ? (int)(first - (long long)row * q.heads) : 0;
   const T* x = reinterpret_cast<const T*>(q.x) + row * q.xr + head * q.xh + 8 / kWord * lane;
   const T* dy = kGrad ? reinterpret_cast<const T*>(q.dy) + row * q.gr + head * q.gh + 8 / kWord * lane : nullptr;
   T* out = reinterpret_cast<T*>(q.out) + row * q.yr + head * q.yh + 8 * lane;
@@ -212,7 +213,8 @@ __global__ void __launch_bounds__(kThreads, (Lay<T, U, kHalf, kGrad>::kBlocks)) 
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float4 t = c[e * (nv / 2)];
-          a[e] = make_float2(fmaf(o[e].x, low ? -t.y : t.y, a[e].x * t.x), fmaf(o[e].y, low ? -t.w : t.w, a[e].y * t.z));
+          a[e] = make_float2(fmaf(o[e].x, low ? -t.y : t.y, a[e].x * t.x),
+                             fmaf(o[e].y, low ? -t.w : t.w, a[e].y * t.z));
         }
       } else {
         const float4* c = reinterpret_cast<const float4*>(cs) + rot[s];

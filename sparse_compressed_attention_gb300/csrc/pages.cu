@@ -50,6 +50,35 @@ __device__ __forceinline__ int block_scan(int v, GiveShared* sh, int* total) {
   return s - v + (warp > 0 ? before : 0);
 }
 
+// The lowest free pages, up to `want` <= kList of them, in sh->list; *chunk is the page
+// from which the walk goes on.  Ends with a barrier.
+__device__ int list_free(const int* ref, int pages, int want, int* chunk, GiveShared* sh) {
+  int found = 0;
+  while (found < want && *chunk < pages) {
+    const int p0 = *chunk + 4 * (int)threadIdx.x;
+    int4 r = make_int4(1, 1, 1, 1);
+    if (p0 + 3 < pages) {
+      r = *reinterpret_cast<const int4*>(ref + p0);
+    } else if (p0 < pages) {
+      r.x = ref[p0];
+      if (p0 + 1 < pages) r.y = ref[p0 + 1];
+      if (p0 + 2 < pages) r.z = ref[p0 + 2];
+    }
+    const int f[4] = {r.x == 0, r.y == 0, r.z == 0, r.w == 0};
+    int all;
+    int at = found + block_scan(f[0] + f[1] + f[2] + f[3], sh, &all);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (f[e] && at < want) sh->list[at] = p0 + e;
+      at += f[e];
+    }
+    found += all;
+    if (found <= want) *chunk += 4 * kGiveThreads;        // else some of it is left for the next list
+  }
+  __syncthreads();
+  return min(found, want);
+}
+
 // count(i): entries that sequence i wants (a whole warp asks, every lane gets it).
 // give(i, first, lo, hi, list): hand list[r - lo] to the wanted entries number r in
 // [lo, hi), the first entry not yet served having number `first`.
@@ -75,31 +104,7 @@ __device__ void give_pages(int n, int* ref, int pages, int* lack, int* status, G
   int given = 0;                                 // numbers below have their page
   int chunk = 0;                                 // first page of the next chunk
   while (given < total) {
-    const int want = min(kList, total - given);
-    int found = 0;
-    while (found < want && chunk < pages) {
-      const int p0 = chunk + 4 * (int)threadIdx.x;
-      int4 r = make_int4(1, 1, 1, 1);
-      if (p0 + 3 < pages) {
-        r = *reinterpret_cast<const int4*>(ref + p0);
-      } else if (p0 < pages) {
-        r.x = ref[p0];
-        if (p0 + 1 < pages) r.y = ref[p0 + 1];
-        if (p0 + 2 < pages) r.z = ref[p0 + 2];
-      }
-      const int f[4] = {r.x == 0, r.y == 0, r.z == 0, r.w == 0};
-      int all;
-      int at = found + block_scan(f[0] + f[1] + f[2] + f[3], sh, &all);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (f[e] && at < want) sh->list[at] = p0 + e;
-        at += f[e];
-      }
-      found += all;
-      if (found <= want) chunk += 4 * kGiveThreads;       // else some of it is left for the next list
-    }
-    found = min(found, want);
-    __syncthreads();
+    const int found = list_free(ref, pages, min(kList, total - given), &chunk, sh);
     if (found == 0) break;
     for (int i = warp; i < n; i += kGiveWarps) {
       const int lo = sh->before[i], hi = sh->before[i + 1];
@@ -207,34 +212,36 @@ __global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(const ForkArgs
   extern __shared__ __align__(16) uint8_t smem[];
   GiveShared* sh = reinterpret_cast<GiveShared*>(smem);
   after_previous();
-  const int lane = threadIdx.x & 31;
   if (blockIdx.x == 0) {
-    auto last = [&](int i, int* full, int* rest) {       // page of the partly filled block, -1: none
-      int src;
-      return fork_row(p, i, &src, full, rest) && *rest > 0 ? fork_page(p, src, *full) : -1;
-    };
-    for (int i = threadIdx.x; i < 3 * p.n; i += kForkThreads) p.copies[i] = i % 3 == 2 ? 0 : -1;
-    for (int i = threadIdx.x; i < p.n; i += kForkThreads) {
-      int full, rest, src;
-      if (fork_row(p, i, &src, &full, &rest) && rest > 0) p.out[(size_t)i * p.out_blocks + full] = -1;
+    // a thread for each beam, 1024 at a time: at most one page each
+    int chunk = 0, wanted = 0, given = 0;
+    for (int i0 = 0; i0 < p.n; i0 += kForkThreads) {
+      const int i = i0 + (int)threadIdx.x;
+      int src, full = 0, rest = 0, old = -1;
+      const bool part = i < p.n && fork_row(p, i, &src, &full, &rest) && rest > 0;
+      if (part) old = fork_page(p, src, full);
+      int want;
+      const int r = block_scan(old >= 0, sh, &want);
+      const int found = list_free(p.ref, p.pages, want, &chunk, sh);
+      int pg = -1;
+      if (old >= 0 && r < found) {
+        pg = sh->list[r];
+        p.ref[pg] = 1;
+      }
+      if (part) p.out[(size_t)i * p.out_blocks + full] = pg;
+      if (i < p.n) {
+        p.copies[3 * i] = pg >= 0 ? old : -1;
+        p.copies[3 * i + 1] = pg;
+        p.copies[3 * i + 2] = pg >= 0 ? rest : 0;
+      }
+      wanted += want;
+      given += found;
+      __syncthreads();                           // the counts are seen by the next walk, the list is read
     }
-    __syncthreads();
-    give_pages(
-        p.n, p.ref, p.pages, p.lack, p.status, sh,
-        [&](int i) {
-          int full, rest;
-          return last(i, &full, &rest) >= 0 ? 1 : 0;
-        },
-        [&](int i, int first, int from, int, const int* list) {
-          if (lane != 0) return;
-          int full, rest;
-          const int old = last(i, &full, &rest), pg = list[first - from];
-          p.out[(size_t)i * p.out_blocks + full] = pg;
-          p.ref[pg] = 1;
-          p.copies[3 * i] = old;
-          p.copies[3 * i + 1] = pg;
-          p.copies[3 * i + 2] = rest;
-        });
+    if (threadIdx.x == 0) {
+      if (p.lack) *p.lack = wanted - given;
+      else if (given < wanted) set_status(p.status, kStatusBadIndex);
+    }
     return;
   }
   for (long long j = (long long)(blockIdx.x - 1) * kForkThreads + threadIdx.x; j < p.items;
@@ -323,66 +330,108 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const CopyArgs
 // ---------------------------------------------------------------------------
 // Kept rows move together: row base + keep[i] to row base + i.  keep ascends, so a
 // row never moves up, and rows are independent in every 16-byte column: a block
-// takes a strip of columns of one sequence and layer and walks its rows in order.
-// A round's rows are read before the barrier and written behind it; what a round
-// writes lies below everything that later rounds read.
+// takes a strip of columns of one sequence and layer and walks its rows in rounds.
+// A round's words are asked for three rounds ahead by asynchronous copies (what a round writes lies below
+// everything that later rounds read) and written behind a barrier that says that all
+// of them have arrived.
 // ---------------------------------------------------------------------------
-constexpr int kKeepThreads = 256, kKeepRows = 4;   // words a thread has in flight
+constexpr int kKeepStages = 4;
 
 struct KeepArgs {
   uint4* cache;
   const int32_t *table, *base, *count, *keep;
   int* status;
   long long layer_words;
-  int blocks, page, pages, width, row_words, strip, lg_strip;
+  int blocks, page, pages, width, row_words, lg_strip;
   FastDiv by_page;
 };
 
+// Threads and words of a thread: many threads for long lists (half of 8 x 16000 rows of
+// 1 KB in 4 layers: 87 us with 512 x 1, 106 with 128 x 2), few for short ones, where more
+// blocks fit on an SM (6 of 16 rows for 32 sequences in 43 layers: 5.8 and 3.5 us).
+template <int kKeepThreads, int kKeepWords>
 __global__ void __launch_bounds__(kKeepThreads) pages_keep_kernel(const KeepArgs p) {
+  __shared__ uint4 s_ring[kKeepStages][kKeepWords][kKeepThreads];
+  __shared__ int2 s_rows[kKeepStages][kKeepThreads];     // a round's rows: from, to (-1: stays)
   after_previous();
-  const int b = blockIdx.x;
+  const int b = blockIdx.x, t = threadIdx.x;
   const int n = p.count[b], base = p.base[b];
   if (n < 0 || n > p.width || base < 0) {
-    if (threadIdx.x == 0) set_status(p.status, kStatusBadIndex);
+    if (t == 0) set_status(p.status, kStatusBadIndex);
     return;
   }
-  const int col = blockIdx.y * p.strip + (int)(threadIdx.x & (p.strip - 1)), r0 = threadIdx.x >> p.lg_strip;
-  const int rows = kKeepThreads >> p.lg_strip;   // rows of a round, kKeepRows times
+  const int strip = 1 << p.lg_strip, col0 = blockIdx.y << p.lg_strip;
+  const int rows = min(kKeepThreads, (kKeepThreads * kKeepWords) >> p.lg_strip);      // of a round
   const int32_t* keep = p.keep + (size_t)b * p.width;
   const int32_t* table = p.table + (size_t)b * p.blocks;
-  uint4* cache = p.cache + blockIdx.z * p.layer_words + col;
-  auto place = [&](long long at) -> long long {          // first word of a logical row, -1: not held
-    const uint32_t blk = at < 0x7FFFFFFF ? p.by_page.div((uint32_t)at) : 0x7FFFFFFFu;
-    const int pg = blk < (uint32_t)p.blocks ? table[blk] : -1;
-    if (pg < 0 || pg >= p.pages) {
-      set_status(p.status, kStatusBadIndex);
-      return -1;
-    }
-    return ((long long)pg * p.page + (int)(at - (long long)blk * p.page)) * p.row_words;
+  uint4* cache = p.cache + blockIdx.z * p.layer_words + col0;
+  // A thread looks after one row of a round: its index two rounds ahead of the round's
+  // copies, its pages one round ahead, so that no load of the chain is waited for.
+  int next = 0, before = -1;                             // keep[i], keep[i - 1] of the next look-up
+  int2 pages = make_int2(-1, -1), offset;                // pages and rows within them, from and to
+  bool bad = false, moves = false;
+  auto index = [&](int round) {
+    const int i = round * rows + t;
+    const bool mine = t < rows && i < n;
+    next = mine ? keep[i] : i;
+    before = mine && i > 0 ? keep[i - 1] : -1;
   };
-  for (int i0 = 0; i0 < n; i0 += rows * kKeepRows) {
-    uint4 v[kKeepRows];
-    long long to[kKeepRows];
+  auto find = [&](int round) {
+    const int i = round * rows + t;
+    bad = next < i || (next > i && before >= next);
+    moves = next > i && !bad;
+    pages = make_int2(-1, -1);
+    if (moves) {
+      const long long at[2] = {(long long)base + next, (long long)base + i};
+      int blk[2];
 #pragma unroll
-    for (int k = 0; k < kKeepRows; ++k) {
-      const int i = i0 + k * rows + r0;
-      to[k] = -1;
-      if (i >= n || col >= p.row_words) continue;
-      const int s = keep[i];
-      if (s < i || (i > 0 && keep[i - 1] >= s)) {
-        set_status(p.status, kStatusBadIndex);
-        continue;
-      }
-      if (s == i) continue;
-      const long long from = place((long long)base + s), at = place((long long)base + i);
-      if (from < 0 || at < 0) continue;
-      v[k] = cache[from];
-      to[k] = at;
+      for (int k = 0; k < 2; ++k) blk[k] = at[k] < 0x7FFFFFFF ? (int)p.by_page.div((uint32_t)at[k]) : 0x7FFFFFFF;
+      offset = make_int2((int)(at[0] - (long long)blk[0] * p.page), (int)(at[1] - (long long)blk[1] * p.page));
+      if (blk[0] < p.blocks && blk[1] < p.blocks) pages = make_int2(table[blk[0]], table[blk[1]]);
     }
-    __syncthreads();
+  };
+  auto ask = [&](int round) {
+    const int slot = round & (kKeepStages - 1);
+    if (round * rows < n) {                              // the same for all threads
+      int2 r = make_int2(-1, -1);
+      if (moves && pages.x >= 0 && pages.x < p.pages && pages.y >= 0 && pages.y < p.pages)
+        r = make_int2(pages.x * p.page + offset.x, pages.y * p.page + offset.y);
+      else if (moves || bad)
+        set_status(p.status, kStatusBadIndex);
+      s_rows[slot][t] = r;
+      __syncthreads();
+      find(round + 1);
+      index(round + 2);
 #pragma unroll
-    for (int k = 0; k < kKeepRows; ++k)
-      if (to[k] >= 0) cache[to[k]] = v[k];
+      for (int k = 0; k < kKeepWords; ++k) {
+        const int w = t + k * kKeepThreads, row = w >> p.lg_strip, col = w & (strip - 1);
+        if (row >= rows || col0 + col >= p.row_words || s_rows[slot][row].y < 0) continue;
+        const uint4* from = cache + (long long)s_rows[slot][row].x * p.row_words + col;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                         (uint32_t)__cvta_generic_to_shared(&s_ring[slot][k][t])),
+                     "l"(from)
+                     : "memory");
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  index(0);
+  find(0);
+  index(1);
+  for (int r = 0; r < kKeepStages - 1; ++r) ask(r);
+  for (int r = 0; r * rows < n; ++r) {
+    ask(r + kKeepStages - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kKeepStages - 1) : "memory");
+    __syncthreads();
+    const int slot = r & (kKeepStages - 1);
+#pragma unroll
+    for (int k = 0; k < kKeepWords; ++k) {
+      const int w = t + k * kKeepThreads, row = w >> p.lg_strip, col = w & (strip - 1);
+      if (row >= rows || col0 + col >= p.row_words) continue;
+      const int to = s_rows[slot][row].y;
+      if (to >= 0) cache[(long long)to * p.row_words + col] = s_ring[slot][k][t];
+    }
+    __syncthreads();                                     // the round's rows are read: the slot may be taken
   }
 }
 
@@ -504,15 +553,17 @@ cudaError_t launch_pages_compact(void* cache, int layers, long long layer_bytes,
   p.width = width;
   p.row_words = row_bytes / 16;
   p.by_page.set((uint32_t)page);
-  // strips of 1 KB, narrower while there are fewer blocks than four for each SM and
-  // a strip keeps 64 bytes
+  // strips of 1 KB, narrower while there are fewer blocks than two for each SM and a
+  // strip keeps 64 bytes
   p.lg_strip = 6;
   while (p.lg_strip > 2 && ((1 << (p.lg_strip - 1)) >= p.row_words ||
-                            (long long)n * layers * ((p.row_words + (1 << p.lg_strip) - 1) >> p.lg_strip) < 608))
+                            (long long)n * layers * ((p.row_words + (1 << p.lg_strip) - 1) >> p.lg_strip) < 304))
     --p.lg_strip;
-  p.strip = 1 << p.lg_strip;
-  const dim3 grid((unsigned)n, (unsigned)((p.row_words + p.strip - 1) / p.strip), (unsigned)layers);
-  const cudaError_t e = launch_overlapped(pages_keep_kernel, grid, dim3(kKeepThreads), 0, st, p);
+  const int strip = 1 << p.lg_strip;
+  const dim3 grid((unsigned)n, (unsigned)((p.row_words + strip - 1) / strip), (unsigned)layers);
+  const bool few = width <= 16;
+  const cudaError_t e = launch_overlapped(few ? pages_keep_kernel<128, 2> : pages_keep_kernel<512, 1>, grid,
+                                          dim3(few ? 128 : 512), 0, st, p);
   if (e == cudaSuccess) note_launch();
   return e;
 }
