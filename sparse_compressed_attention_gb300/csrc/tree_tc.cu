@@ -77,7 +77,7 @@ constexpr int kLookWarps = 2;                     // 4-bit caches: 64 key rows e
 constexpr int kUnpackWarps = 8;                   // 4-bit caches: two groups, 32 key rows each
 // Registers of a thread of the 4-bit kernel after the split: shares and products,
 // softmax, unpacking.  They add up to what 640 threads start with.
-constexpr int kRegsStart = 96, kRegsLead = 56, kRegsSoft = 112, kRegsUnpack = 96;
+constexpr int kRegsStart = 96, kRegsLead = 56, kRegsSoft = 128, kRegsUnpack = 80;
 static_assert(128 * kRegsLead + 256 * kRegsSoft + 256 * kRegsUnpack <= kThreadsQ4 * kRegsStart, "register split");
 constexpr int kSoftThreads = 256;                 // warps 4-11
 constexpr int kSoftWarps = kSoftThreads / 32;
@@ -626,7 +626,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             const bool dense = j < pc.dense;
             uint64_t* full = dense ? c->full_t : c->full_g;
             const uint32_t par = (dense ? gt : gg) & 1;
-#pragma unroll
+// (rolled for 4-bit caches, whose roles' code is too long for the instruction cache: 195 -> 184 us)
+#pragma unroll kQ4 ? 1 : kPairs
             for (int m = kPairs - 1; m >= 0; --m) {
               ok = ok && warp_wait(&full[m], par, c, a.status);
               if (!kQ4 && !dense) fence_proxy_async_smem();     // cp.async writes -> tensor-core reads
@@ -670,7 +671,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             if (ok && j == 0 && qc >= 1) ok = warp_wait(&c->o_empty, (qc - 1) & 1, c, a.status);
             tc_fence_after();
             if (lead) {
-#pragma unroll
+#pragma unroll kQ4 ? 1 : kPairs
               for (int m = kPairs - 1; m >= 0; --m) {
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)
@@ -705,21 +706,19 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         for (int j = 0; j < pc.tiles && ok; ++j) {
           const int rs = g & (kRowsAhead - 1);
           const long long at = (long long)(pc.tile0 + j) * kTile + 64 * lw + lane;
-          const uint8_t* row[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) row[i] = key_row_q4(p, r, bits, pc.row, at + 32 * i);
           if (g >= kRowsAhead) ok = warp_wait(&c->rows_empty[rs], (g / kRowsAhead - 1) & 1, c, a.status);
           if (!ok) break;
-#pragma unroll
+#pragma unroll 1
           for (int i = 0; i < 2; ++i) {
-            const uint32_t live = __ballot_sync(0xffffffffu, row[i] != nullptr);
-            c->rows[rs][64 * lw + 32 * i + lane] = row[i];
+            const uint8_t* row = key_row_q4(p, r, bits, pc.row, at + 32 * i);
+            const uint32_t live = __ballot_sync(0xffffffffu, row != nullptr);
+            c->rows[rs][64 * lw + 32 * i + lane] = row;
             if (lane == 0) c->valid[rs][2 * lw + i] = live;
-            if (row[i] != nullptr) {
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(row[i]) : "memory");
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(row[i] + 128) : "memory");
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(row[i] + 256) : "memory");
-          }
+            if (row != nullptr) {
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(row) : "memory");
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(row + 128) : "memory");
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(row + 256) : "memory");
+            }
           }
           warp_arrive(&c->rows_full[rs], lane);
           ++g;
@@ -1043,9 +1042,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     // memory for the O products.
     set_registers<kRegsUnpack>();
     const int quarter = warp & 3, row = 32 * quarter + lane, grp = (warp - 12) >> 2;
-    uint4 codes[8];
-    uint2 scales[2];
-    int qc = 0, tiles = 0;                       // pieces read, tiles left of the last one
+    uint4 codes[4];
+    uint2 scales;
+    int qc = 0, tiles = 0;                         // pieces read, tiles left of the last one
     bool ok = true;
     // whether there is a tile behind those taken so far
     auto more_tiles = [&]() -> bool {
@@ -1058,68 +1057,61 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
       }
       return tiles > 0;
     };
-    // row of tile g
-    auto row_of = [&](int g) -> const uint8_t* {
-      const int rs = g & (kRowsAhead - 1);
-      ok = ok && warp_wait(&c->rows_full[rs], (g / kRowsAhead) & 1, c, a.status);
-      const uint8_t* from = ok ? c->rows[rs][row] : nullptr;
-      warp_arrive(&c->rows_empty[rs], lane);
-      --tiles;
-      return from;
-    };
-    auto load = [&](const uint8_t* from, int i, int m) {
+    const uint8_t* from = nullptr;                 // the row whose codes are asked for
+    // Ask for pair m of the current row; m < 0: of the next tile's row.  false: there is none.
+    auto load = [&](int g, int m) -> bool {
+      if (m < 0) {
+        if (!more_tiles()) return false;
+        const int rs = g & (kRowsAhead - 1);
+        ok = ok && warp_wait(&c->rows_full[rs], (g / kRowsAhead) & 1, c, a.status);
+        from = ok ? c->rows[rs][row] : nullptr;
+        warp_arrive(&c->rows_empty[rs], lane);
+        --tiles;
+        m = kPairs - 1 - grp;
+      }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) codes[4 * i + k] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);  // zeros
+      for (int k = 0; k < 4; ++k) codes[k] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);  // zeros
+      scales = make_uint2(0, 0);
       if (from != nullptr) {
-        load32(from + 64 * m, &codes[4 * i]);
-        load32(from + 64 * m + 32, &codes[4 * i + 2]);
+        load32(from + 64 * m, &codes[0]);
+        load32(from + 64 * m + 32, &codes[2]);
+        scales = reinterpret_cast<const uint2*>(from + kD / 2)[m];
       }
-      scales[i] = from ? reinterpret_cast<const uint2*>(from + kD / 2)[m] : make_uint2(0, 0);
+      return true;
     };
-    bool more = more_tiles();
-    if (more) {
-      const uint8_t* from = row_of(0);
+    bool more = load(0, -1);
+    // not unrolled over the pairs: the roles' code shares an instruction cache
+#pragma unroll 1
+    for (int k2 = 0; more && ok; ++k2) {
+      const int g = k2 >> 1, m = kPairs - 1 - grp - 2 * (k2 & 1);
+      const uint32_t n = 4 * (uint32_t)g + grp + 2 * (k2 & 1), turn = n / kRing, ring = n - kRing * turn;
+      if (g >= 1) ok = warp_wait(&c->empty[m], (g - 1) & 1, c, a.status);
+      if (turn >= 1 && ok) ok = warp_wait(&c->ring_empty[ring], (turn - 1) & 1, c, a.status);
+      if (!ok) break;
+      tc_fence_after();
 #pragma unroll
-      for (int i = 0; i < 2; ++i) load(from, i, kPairs - 1 - grp - 2 * i);
-    }
-    for (int g = 0; more && ok; ++g) {
-      const uint8_t* next = nullptr;
-      more = more_tiles();
-      if (more) next = row_of(g + 1);
+      for (int k = 0; k < 4; ++k) {                // half a K-block: 32 dims
+        uint8_t* to = smem + OFF_SLOT + (2 * m + k / 2) * kSlotBytes + row * 128;
+        const uint32_t sc = (k / 2 ? scales.y : scales.x) >> (16 * (k & 1));
+        uint32_t v[16];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int m = kPairs - 1 - grp - 2 * i;
-        const uint32_t n = 4 * (uint32_t)g + grp + 2 * i, turn = n / kRing, ring = n - kRing * turn;
-        if (g >= 1 && ok) ok = warp_wait(&c->empty[m], (g - 1) & 1, c, a.status);
-        if (turn >= 1 && ok) ok = warp_wait(&c->ring_empty[ring], (turn - 1) & 1, c, a.status);
-        if (ok) {
-          tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {          // half a K-block: 32 dims
-            uint8_t* to = smem + OFF_SLOT + (2 * m + k / 2) * kSlotBytes + row * 128;
-            const uint32_t sc = (k / 2 ? scales[i].y : scales[i].x) >> (16 * (k & 1));
-            uint32_t v[16];
-#pragma unroll
-            for (int c4 = 0; c4 < 4; ++c4) {     // 16-byte chunk: one word of codes
-              const int ch = 4 * (k & 1) + c4;
-              const uint4 w4 = codes[4 * i + k];
-              const uint32_t w = c4 == 0 ? w4.x : c4 == 1 ? w4.y : c4 == 2 ? w4.z : w4.w;
-              const uint4 u = q4_word_bf16(w, (sc >> (8 * (c4 / 2))) & 255u);
-              *reinterpret_cast<uint4*>(to + ((ch ^ (row & 7)) << 4)) = u;
-              v[4 * c4] = u.x;
-              v[4 * c4 + 1] = u.y;
-              v[4 * c4 + 2] = u.z;
-              v[4 * c4 + 3] = u.w;
-            }
-            tmem_st16_async(tmem + ((uint32_t)(32 * quarter) << 16) + kRingTmem + 64 * ring + 16 * k, v);
-          }
-          tmem_wait_st();
-          tc_fence_before();
-          fence_proxy_async_smem();
-          warp_arrive(&c->full_g[m], lane);
+        for (int c4 = 0; c4 < 4; ++c4) {           // 16-byte chunk: one word of codes
+          const int ch = 4 * (k & 1) + c4;
+          const uint32_t w = c4 == 0 ? codes[k].x : c4 == 1 ? codes[k].y : c4 == 2 ? codes[k].z : codes[k].w;
+          const uint4 u = q4_word_bf16(w, (sc >> (8 * (c4 / 2))) & 255u);
+          *reinterpret_cast<uint4*>(to + ((ch ^ (row & 7)) << 4)) = u;
+          v[4 * c4] = u.x;
+          v[4 * c4 + 1] = u.y;
+          v[4 * c4 + 2] = u.z;
+          v[4 * c4 + 3] = u.w;
         }
-        if (more) load(next, i, m);
+        tmem_st16_async(tmem + ((uint32_t)(32 * quarter) << 16) + kRingTmem + 64 * ring + 16 * k, v);
       }
+      tmem_wait_st();
+      tc_fence_before();
+      fence_proxy_async_smem();
+      warp_arrive(&c->full_g[m], lane);
+      more = load(g + 1, m - 2);
     }
   }
 
