@@ -357,6 +357,14 @@ __device__ __forceinline__ float sink_mass(float s2, float m) {
 // its tiles.  Block c of the grid takes units [c * share, (c + 1) * share).
 __device__ __forceinline__ int share_of(int total, int ctas) { return (total + ctas - 1) / ctas; }
 
+// Whether a looked-up row lies in one of the caches (bound-checking build).
+__device__ __forceinline__ bool in_caches(const TreeArgs& a, const uint8_t* row) {
+  const uint8_t* tok = reinterpret_cast<const uint8_t*>(a.tok_cache);
+  const uint8_t* ent = reinterpret_cast<const uint8_t*>(a.ent_cache);
+  return (a.window != 0 && row >= tok && row < tok + a.tok_slots * kQ4RowBytes) ||
+         (a.ratio > 0 && row >= ent && row < ent + a.ent_slots * kQ4RowBytes);
+}
+
 // 32 bytes, one sector: half the requests of 16-byte loads where every lane reads a row of
 // its own, and no line of the little L1 that shared memory leaves (single tokens over long
 // caches 209 -> 195 us).
@@ -701,6 +709,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         const Piece pc = c->info[is];
         warp_arrive(&c->info_empty[is], lane);
         if (!ok || pc.done) break;
+        if (!V4_BOUND(pc.row >= 0 && pc.row < a.n_rows, a.status)) break;
         const TreeRow r = tree_row(a, pc.row);
         const int4 bits = *reinterpret_cast<const int4*>(a.plan + (size_t)pc.row * kPlanWords + 4);
         for (int j = 0; j < pc.tiles && ok; ++j) {
@@ -1065,6 +1074,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         const int rs = g & (kRowsAhead - 1);
         ok = ok && warp_wait(&c->rows_full[rs], (g / kRowsAhead) & 1, c, a.status);
         from = ok ? c->rows[rs][row] : nullptr;
+        if (from != nullptr && !V4_BOUND(in_caches(a, from), a.status)) from = nullptr;
         warp_arrive(&c->rows_empty[rs], lane);
         --tiles;
         m = kPairs - 1 - grp;
