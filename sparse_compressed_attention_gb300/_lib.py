@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 import torch
 
@@ -96,7 +97,7 @@ def lib(path=None):
                            "sparse_compressed_attention_gb300.build.build()" % path)
     L = C.CDLL(path)
     vp, i32, i64, f32, sz = C.c_void_p, C.c_int32, C.c_int64, C.c_float, C.c_size_t
-    cfgp, partp = C.POINTER(v4_config), C.POINTER(v4_norm_rope_part)
+    cfgp = C.POINTER(v4_config)
     sig = {
         "v4_rope_inv_freq": [f32, i32, f32, i32, f32, f32, vp],
         "v4_workspace_size": [cfgp, C.POINTER(sz)],
@@ -124,9 +125,9 @@ def lib(path=None):
         "v4_tree_workspace_size": [cfgp, i32, C.POINTER(sz)],
         "v4_tree_mqa_fwd": [cfgp, C.POINTER(v4_tree_inputs), vp, vp, vp, sz, vp],
         "v4_w4_pack": [vp, i32, i32, i32, i32, vp, vp, vp],
-        "v4_norm_rope_fwd": [partp, partp, i64, i32, vp, vp, i32, i32, i32, f32, i32, vp],
+        "v4_norm_rope_fwd": [vp, vp, i64, i32, vp, vp, i32, i32, i32, f32, i32, vp],
         "v4_norm_rope_workspace_size": [i32, C.POINTER(sz)],
-        "v4_norm_rope_bwd": [partp, partp, i64, i32, vp, vp, i32, i32, i32, f32, i32, vp, sz, vp],
+        "v4_norm_rope_bwd": [vp, vp, i64, i32, vp, vp, i32, i32, i32, f32, i32, vp, sz, vp],
         "v4_q4_row_bytes": [i32, C.POINTER(i32)],
         "v4_cache_append_q4": [vp, i64, i32, i64, vp, i64, i32, vp, vp],
         "v4_cache_read_q4": [vp, i64, vp, i64, i32, i32, vp, i64, vp],
@@ -603,32 +604,60 @@ def v4_w4_proj(x, codes, scales, y, norm_dim=0, eps=1e-6, norm_w=None, stream=No
     return y
 
 
-def _norm_part(dev, name, x, out, w, dy, dw):
-    """One part's struct; dy None: forward."""
-    px, sx = _strided(x, name, 3, dev)
-    po, so = _strided(out, name + "'s output", 3, dev)
-    shape, dt = x.shape, x.dtype
-    if out.shape != shape or out.dtype is not dt:
+_PART = struct.Struct("5Q6qi4x")                # v4_norm_rope_part, packed: half a microsecond less than the Structure
+
+
+def _norm_part(dev, name, x, out, w, dy, dw, dim, rows):
+    """One part's struct; dy None: forward.  rows, dim: the call's, of its first part."""
+    try:
+        dt, sh = x.dtype, x.shape
+        if (len(sh) == 3 and sh[0] == rows and sh[2] == dim and dt in _STORAGE_CODE and out.dtype is dt and out.shape == sh
+                and x.get_device() == dev and out.get_device() == dev):
+            sx, so = x.stride(), out.stride()
+            if dim <= 1 or sx[2] == 1 and so[2] == 1:
+                pg, g0, g1 = 0, 0, 0
+                if dy is not None:
+                    pg, sg = _strided(dy, name + "'s output gradient", 3, dev)
+                    if dy.shape != sh or dy.dtype is not dt:
+                        raise ValueError("%s's output gradient must have its shape and type" % name)
+                    g0, g1 = sg[0], sg[1]
+                return _PART.pack(x.data_ptr(), 0 if w is None else _shaped(w, name + "_w", (dim,), torch.float32, dev), pg,
+                                  out.data_ptr(),
+                                  0 if dw is None else _shaped(dw, "d" + name + "_w", (dim,), torch.float32, dev),
+                                  sx[0], sx[1], g0, g1, so[0], so[1], sh[1])
+    except AttributeError:
+        pass
+    _strided(x, name, 3, dev)
+    _strided(out, name + "'s output", 3, dev)
+    if out.shape != x.shape or out.dtype is not x.dtype:
         raise ValueError("%s's output must have its shape and type" % name)
-    pg, sg = None, (0, 0)
-    if dy is not None:
-        pg, sg = _strided(dy, name + "'s output gradient", 3, dev)
-        if dy.shape != shape or dy.dtype is not dt:
-            raise ValueError("%s's output gradient must have its shape and type" % name)
-    return v4_norm_rope_part(
-        px, None if w is None else _shaped(w, name + "_w", shape[2:], torch.float32, dev), pg, po,
-        None if dw is None else _shaped(dw, "d" + name + "_w", shape[2:], torch.float32, dev), sx[0], sx[1], sg[0], sg[1],
-        so[0], so[1], shape[1])
+    raise ValueError("%s must be [%d, heads, %d]" % (name, rows, dim))
 
 
-def _norm_common(q, k, pos, inv_freq, rope_begin, dev):
+def _norm_call(call, q, k, pos, inv_freq, rope_begin, layout, eps, q_out, k_out, q_w, k_w, dq_out, dk_out, dq_w, dk_w, more, stream):
+    dev = _current(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be a tensor [rows, heads, dim]")
     rows, _, dim = q.shape
-    if k is not None and (k.dim() != 3 or k.shape[0] != rows or k.shape[2] != dim or k.dtype is not q.dtype):
-        raise ValueError("k must be [%d, heads, %d] of q's type" % (rows, dim))
+    pq = _norm_part(dev, "q", q, q_out, q_w, dq_out, dq_w, dim, rows)
+    pk = None
+    if k is not None:
+        pk = _norm_part(dev, "k", k, k_out, k_w, dk_out, dk_w, dim, rows)
+        if k.dtype is not q.dtype:
+            raise TypeError("k must have q's type")
     half = 0 if inv_freq is None else inv_freq.numel()
-    pp = _shaped(pos, "pos", (rows,), torch.int32, dev) if half and rows else None
-    pf = _shaped(inv_freq, "inv_freq", (half,), torch.float32, dev) if half else None
-    return rows, dim, pp, pf, 2 * half, dim - 2 * half if rope_begin is None else rope_begin
+    pp = pf = None
+    if half:
+        pf = _shaped(inv_freq, "inv_freq", (half,), torch.float32, dev)
+        pp = _shaped(pos, "pos", (rows,), torch.int32, dev) if rows else None
+    st = call(pq, pk, rows, dim, pp, pf, 2 * half, dim - 2 * half if rope_begin is None else rope_begin, layout, eps,
+              _STORAGE_CODE[q.dtype], *more(dev), _stream_on(stream, dev))
+    if st:
+        _check(st)
+
+
+def _nothing_more(dev):
+    return ()
 
 
 def v4_norm_rope_fwd(q, k, pos, inv_freq, q_out, k_out=None, q_w=None, k_w=None, eps=1e-6, rope_begin=None,
@@ -637,13 +666,8 @@ def v4_norm_rope_fwd(q, k, pos, inv_freq, q_out, k_out=None, q_w=None, k_w=None,
     or None, rotated at pos [rows] on dims [rope_begin, rope_begin + R), into q_out and k_out (or in place).
 
     R = 2 * len(inv_freq) (None: no rotation); rope_begin defaults to the last R dims."""
-    dev = _current(q, "q")
-    pq = _norm_part(dev, "q", q, q_out, q_w, None, None)
-    pk = None if k is None else _norm_part(dev, "k", k, k_out, k_w, None, None)
-    rows, dim, pp, pf, R, begin = _norm_common(q, k, pos, inv_freq, rope_begin, dev)
-    if rows:
-        _check(lib().v4_norm_rope_fwd(pq, pk, rows, dim, pp, pf, R, begin, layout, eps, _STORAGE_CODE[q.dtype],
-                                      _stream_on(stream, dev)))
+    _norm_call(lib().v4_norm_rope_fwd, q, k, pos, inv_freq, rope_begin, layout, eps, q_out, k_out, q_w, k_w, None, None, None,
+               None, _nothing_more, stream)
     return q_out, k_out
 
 
@@ -661,17 +685,19 @@ def v4_norm_rope_bwd(q, k, dq_out, dk_out, pos, inv_freq, dq, dk=None, q_w=None,
                      rope_begin=None, layout=V4_ROPE_INTERLEAVED, workspace=None, stream=None):
     """Gradients of v4_norm_rope_fwd: from its inputs and the gradients dq_out, dk_out of its outputs, dq and dk (of q's
     type) and the weights' dq_w, dk_w [dim] fp32 (None: not wanted) are written.  workspace: alloc_norm_rope_workspace."""
-    dev = _current(q, "q")
-    _current(dq_out, "q's output gradient")
-    if k is not None:
-        _current(dk_out, "k's output gradient")
-    pq = _norm_part(dev, "q", q, dq, q_w, dq_out, dq_w)
-    pk = None if k is None else _norm_part(dev, "k", k, dk, k_w, dk_out, dk_w)
-    rows, dim, pp, pf, R, begin = _norm_common(q, k, pos, inv_freq, rope_begin, dev)
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a tensor")
+    if not q.is_cuda:
+        raise ValueError("q must be on a CUDA device")
+    for g, name in ((dq_out, "q's output gradient"), (dk_out if k is not None else dq_out, "k's output gradient")):
+        if not isinstance(g, torch.Tensor):
+            raise TypeError("%s must be a tensor" % name)
     size = 0 if workspace is None else workspace.numel()
-    _check(lib().v4_norm_rope_bwd(pq, pk, rows, dim, pp, pf, R, begin, layout, eps, _STORAGE_CODE[q.dtype],
-                                  None if workspace is None else _shaped(workspace, "workspace", (size,), torch.uint8, dev),
-                                  size, _stream_on(stream, dev)))
+
+    def more(dev):
+        return None if workspace is None else _shaped(workspace, "workspace", (size,), torch.uint8, dev), size
+    _norm_call(lib().v4_norm_rope_bwd, q, k, pos, inv_freq, rope_begin, layout, eps, dq, dk, q_w, k_w, dq_out,
+               dk_out if k is not None else None, dq_w, dk_w, more, stream)
     return dq, dk, dq_w, dk_w
 
 

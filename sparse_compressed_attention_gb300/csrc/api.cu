@@ -62,7 +62,7 @@ struct ProfRec {
   cudaEvent_t a, b;
 };
 static std::mutex g_prof_mu;
-static bool g_prof_on = false;
+static std::atomic<bool> g_prof_on{false};
 static std::vector<ProfRec> g_prof;
 
 enum { K_COMPRESS = 0, K_ROTATE = 1, K_IDX_PREP = 2, K_IDX_SCORE = 3, K_TOPK = 4, K_ATTN = 5,
@@ -95,6 +95,7 @@ struct ProfScope {
 };
 
 StageTiming::StageTiming(int kind, cudaStream_t st) : rec_(nullptr), st_(st) {
+  if (!g_prof_on.load(std::memory_order_relaxed)) return;        // no allocation, no lock: the usual case
   ProfScope* ps = new ProfScope(kind, st);
   if (ps->on) rec_ = ps;
   else delete ps;
