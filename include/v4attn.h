@@ -615,7 +615,7 @@ v4_status v4_w4_proj(const void* x, int64_t rows, int32_t groups, int32_t K, int
  *                are refused.  Views of one fused projection may be mixed as
  *                long as their row strides are equal.
  *   w          : [dim] fp32, NULL = ones.
- *   dw         : [dim] fp32 out, NULL = not wanted.
+ *   dw         : [dim] fp32 out, NULL = not wanted; the parts' must not overlap.
  * dim a multiple of 8 up to 1024 (above: V4_ERR_UNSUPPORTED); rows times heads
  * up to 2^30; rope_dim, rope_begin, layout, dtype and angles as v4_rope.
  * Squares, sums and products are fp32, results are rounded once.  A head of

@@ -745,12 +745,20 @@ def v4_cache_read_q4(cache, slot, out, stream=None):
 
 
 def _table(t, name, dev):
+    """Pointer, sequences and blocks of a block table."""
+    try:
+        n, blocks = t.shape
+        if t.dtype is torch.int32 and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr(), n, blocks
+    except (AttributeError, ValueError):
+        pass
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError("%s must be a tensor [sequences, blocks]" % name)
     return _shaped(t, name, t.shape, torch.int32, dev), t.shape[0], t.shape[1]
 
 
 def _pool(ref, dev):
+    """Pointer of the pages' counts."""
     if not isinstance(ref, torch.Tensor) or ref.dim() != 1:
         raise ValueError("ref must be a tensor [pages]")
     return _shaped(ref, "ref", ref.shape, torch.int32, dev)

@@ -132,6 +132,8 @@ static v4_status norm_rope(const v4_norm_rope_part* q, const v4_norm_rope_part* 
     for (int i = 0; i < n_in; ++i)
       if (!same_view(out[o], in[i]) && !apart(out[o], in[i]))
         return bad("an output overlaps an input and is not the same tensor");
+  if (c.part[0].dw && c.part[1].dw && overlap(c.part[0].dw, (int64_t)dim * 4, c.part[1].dw, (int64_t)dim * 4))
+    return bad("the weight gradients overlap");
   // the same tensor is read and written by the same lanes only within its own part
   if (n_out == 2) {
     if (!apart(out[0], out[1])) return bad("the outputs overlap");

@@ -50,20 +50,28 @@ __device__ __forceinline__ int block_scan(int v, GiveShared* sh, int* total) {
   return s - v + (warp > 0 ? before : 0);
 }
 
+// Counts of four pages; those behind the last are not free.
+__device__ __forceinline__ int4 four_counts(const int* ref, int pages, int p0) {
+  int4 r = make_int4(1, 1, 1, 1);
+  if (p0 + 3 < pages) {
+    r = *reinterpret_cast<const int4*>(ref + p0);
+  } else if (p0 < pages) {
+    r.x = ref[p0];
+    if (p0 + 1 < pages) r.y = ref[p0 + 1];
+    if (p0 + 2 < pages) r.z = ref[p0 + 2];
+  }
+  return r;
+}
+
 // The lowest free pages, up to `want` <= kList of them, in sh->list; *chunk is the page
 // from which the walk goes on.  Ends with a barrier.
-__device__ int list_free(const int* ref, int pages, int want, int* chunk, GiveShared* sh) {
+// ahead: this thread's counts of that chunk where they were asked for before, else null.
+__device__ int list_free(const int* ref, int pages, int want, int* chunk, GiveShared* sh, const int4* ahead) {
   int found = 0;
   while (found < want && *chunk < pages) {
     const int p0 = *chunk + 4 * (int)threadIdx.x;
-    int4 r = make_int4(1, 1, 1, 1);
-    if (p0 + 3 < pages) {
-      r = *reinterpret_cast<const int4*>(ref + p0);
-    } else if (p0 < pages) {
-      r.x = ref[p0];
-      if (p0 + 1 < pages) r.y = ref[p0 + 1];
-      if (p0 + 2 < pages) r.z = ref[p0 + 2];
-    }
+    const int4 r = ahead ? *ahead : four_counts(ref, pages, p0);
+    ahead = nullptr;
     const int f[4] = {r.x == 0, r.y == 0, r.z == 0, r.w == 0};
     int all;
     int at = found + block_scan(f[0] + f[1] + f[2] + f[3], sh, &all);
@@ -104,7 +112,7 @@ __device__ void give_pages(int n, int* ref, int pages, int* lack, int* status, G
   int given = 0;                                 // numbers below have their page
   int chunk = 0;                                 // first page of the next chunk
   while (given < total) {
-    const int found = list_free(ref, pages, min(kList, total - given), &chunk, sh);
+    const int found = list_free(ref, pages, min(kList, total - given), &chunk, sh, nullptr);
     if (found == 0) break;
     for (int i = warp; i < n; i += kGiveWarps) {
       const int lo = sh->before[i], hi = sh->before[i + 1];
@@ -215,6 +223,7 @@ __global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(const ForkArgs
   if (blockIdx.x == 0) {
     // a thread for each beam, 1024 at a time: at most one page each
     int chunk = 0, wanted = 0, given = 0;
+    const int4 ahead = four_counts(p.ref, p.pages, 4 * (int)threadIdx.x);      // asked for beside the beams' rows
     for (int i0 = 0; i0 < p.n; i0 += kForkThreads) {
       const int i = i0 + (int)threadIdx.x;
       int src, full = 0, rest = 0, old = -1;
@@ -222,7 +231,7 @@ __global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(const ForkArgs
       if (part) old = fork_page(p, src, full);
       int want;
       const int r = block_scan(old >= 0, sh, &want);
-      const int found = list_free(p.ref, p.pages, want, &chunk, sh);
+      const int found = list_free(p.ref, p.pages, want, &chunk, sh, i0 == 0 ? &ahead : nullptr);
       int pg = -1;
       if (old >= 0 && r < found) {
         pg = sh->list[r];

@@ -58,16 +58,16 @@ def norm(lib, grad=False, q=None, k=None, ws=(256, 1 << 30), **over):
     (dict(q=part(1 << 24, x_row_stride=1 << 40), rows=1 << 20), 1, "reaches"),
     (dict(q=part(1 << 24, out=(1 << 24) + 128)), 1, "not the same tensor"),
     (dict(q=part(1 << 24, out=1 << 24, out_row_stride=256)), 1, "not the same tensor"),
-    (dict(k=part(1 << 28, out=(1 << 28) + 64)), 1, "overlaps an input"),
-    (dict(q=part(1 << 24), k=part(1 << 28, out=(1 << 24) + (2 << 20))), 1, "the outputs overlap"),
-    (dict(q=part(1 << 24), k=part(1 << 28, out=1 << 24)), 1, "other part")])
+    (dict(k=part(1 << 28, out=(1 << 28) + 64, dw=4096)), 1, "overlaps an input"),
+    (dict(q=part(1 << 24), k=part(1 << 28, out=(1 << 24) + (2 << 20), dw=4096)), 1, "the outputs overlap"),
+    (dict(q=part(1 << 24), k=part(1 << 28, out=1 << 24, dw=4096)), 1, "other part")])
 def test_norm_refusals(lib, grad, over, status, text):
     refused(lib, norm(lib, grad, **over), status, text)
 
 
 def test_norm_gradient_refusals(lib):
     for over, status, text in ((dict(q=part(1 << 24, dy=None)), 1, "q.dy"), (dict(q=part(1 << 24, dw=24)), 1, "weight gradient"),
-                               (dict(ws=(256, 100)), 3, "needed"), (dict(ws=(None, 1 << 30)), 3, "NULL"),
+                               (dict(k=part(1 << 28, dw=32)), 1, "weight gradients overlap"), (dict(ws=(256, 100)), 3, "needed"), (dict(ws=(None, 1 << 30)), 3, "NULL"),
                                (dict(ws=(128, 1 << 30)), 3, "256-byte"),
                                (dict(q=part(1 << 24, out=(1 << 24) + (1 << 20) + 64)), 1, "not the same tensor")):
         refused(lib, norm(lib, True, **over), status, text)
