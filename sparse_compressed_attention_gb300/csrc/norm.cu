@@ -8,16 +8,16 @@
 // writes dx.  A head belongs to a group of 1 to 32 lanes that keeps it in
 // registers, so the mean is a butterfly over the group and nothing is read
 // twice.  A group takes a short run of consecutive heads, of queries or of keys,
-// that arrive through a ring in shared memory (16-byte asynchronous copies, up to
-// 256 bytes a lane in flight, which registers would not hold): the weight stays in
+// that arrive through a ring in shared memory (16-byte asynchronous copies, two or
+// three heads a group in flight, which registers would not hold): the weight stays in
 // registers and a row's angles are formed once in the run.  Weight gradients are
 // summed in registers over the run, then over the block's warps; a second kernel
 // adds the blocks' sums in a fixed order, so results repeat bit for bit.
 //
-// Times (device, in a replayed graph): 4096 rows of 64 + 1 heads of 512 in bf16 84 us
+// Times (device, in a replayed graph): 4096 rows of 64 + 1 heads of 512 in bf16 83 us
 // (6.5 TB/s; a block for 16 heads with loads into registers 111), their gradients 131
-// (6.2 TB/s; 310), gradients of 5003 rows of 32 + 8 heads of 128 in fp32, half layout, 62
-// (5.0 TB/s, bound by instructions and shared memory; 101), 16 rows of 64 + 1 heads 2.3
+// (6.2 TB/s; 310), gradients of 5003 rows of 32 + 8 heads of 128 in fp32, half layout, 58
+// (5.3 TB/s, bound by instructions and shared memory; 101), 16 rows of 64 + 1 heads 2.3
 // (launch).
 #include <math.h>
 
@@ -56,13 +56,15 @@ struct Args {
 
 // What a kernel keeps in shared memory for each warp: a ring of raw heads (x, and dy
 // for the gradient), the angles of each group's row, and for the forward half layout
-// the values that partners exchange.  Up to 256 bytes a lane are in flight.
+// the values that partners exchange.
 template <typename T, int U, bool kHalf, bool kGrad>
 struct Lay {
   static constexpr int kTensors = kGrad ? 2 : 1;
   static constexpr int kHead = 256 * U * (int)sizeof(T);          // bytes of a warp's heads
   static constexpr int kWant = 256 / (kTensors * U * 8 * (int)sizeof(T));
-  static constexpr int kStages = kWant < 2 ? 2 : kWant > 4 ? 4 : kWant;
+  // (three stages at most: fp32 gradients of 128-wide heads 57.6 us, 59.6 with four, 57.3 with two, which cost
+  // the bf16 gradients of 512-wide heads 138 instead of 131)
+  static constexpr int kStages = kWant < 2 ? 2 : kWant > 3 ? 3 : kWant;
   static constexpr int kTable = kStages * kTensors * kHead;       // offset of the angles
   static constexpr int kStrip = kTable + 128 * U * (int)sizeof(float2);
   static constexpr int kWarp = kStrip + (kHalf && !kGrad ? 256 * U * (int)sizeof(float) : 0);

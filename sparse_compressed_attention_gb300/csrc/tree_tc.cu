@@ -45,15 +45,14 @@
 // and join.  The CUDA-core kernel's times are in brackets, tiles are a block's:
 //   1 row, 512 selected entries + window        15 us     [246]     1 tile
 //   32 x up to 8 nodes, selected                49 us     [2196]    7
-//   8 x 8 nodes over 7812 entries each          95 us     [9681]    27
+//   8 x 8 nodes over 7812 entries each          94 us     [9681]    27
 //   16 rows over all of up to 49152 tokens      84 us     [19127]   20
-//   4 x 16 nodes over 32768 tokens              345 us    [40543]   109, 36% tensor pipe
+//   4 x 16 nodes over 32768 tokens              338 us    [40543]   109, 37% tensor pipe
 // (the last reads 134 MB of keys, more than L2 holds: one sequence with 64 nodes took 323
 // of 358.  The tiles' times above are from before the O rescale was rolled, which took
-// spills out of the tile loop and 3 to 7% off every case.)  Tried and not faster: 16
-// softmax warps, another split of the registers, the softmax in paired fp32 operations or
-// with its exponentials ahead of the vote, TMEM allocated before the shares, rows asked
-// two tiles ahead.
+// spills out of the tile loop, and the softmax was packed: 4 to 8% off every case.)
+// Tried and not faster: 16 softmax warps, another split of the registers, exponentials
+// ahead of the vote, TMEM allocated before the shares, rows asked two tiles ahead.
 //
 // 4-bit caches (kQ4: 640 threads).  A tile is 36 KB instead of 128, so HBM is no bound;
 // unpacking it is.  Warps 2-3 look up rows, up to four tiles ahead, and ask them into L2;
@@ -64,11 +63,12 @@
 // code ran out of the instruction cache.
 //   1 row, 512 selected entries + window        16 us     [248]
 //   32 x up to 8 nodes, selected                44 us     [2162]
-//   16 rows over all of up to 131072 tokens     183 us    [50400]   62 tiles, 33% tensor pipe
-// A tile takes 2.6 us: 1.4 of products, the softmax between them, and loads of codes, a
-// row of its own to each lane, of which the products hide a part (without any loads 2.1).
+//   16 rows over all of up to 131072 tokens     180 us    [50400]   62 tiles, 33% tensor pipe
+// A tile takes 2.6 us: 1.4 of products, between them the softmax (0.8) and the unpacking of
+// its last pairs, which slows down while the O products read shared memory at its full
+// rate; loads of codes, a row of its own to each lane, are hidden in part (without any 2.1).
 // Steps: unpacking by the four gather warps into the slots 265 us, two groups and look-ups
-// apart 209, 32-byte loads 195, rolled loops 183.  Slower: S products a tile ahead of the O
+// apart 209, 32-byte loads 195, rolled loops 183, packed softmax 180.  Slower: S products a tile ahead of the O
 // products with keys unpacked once for each (253: twice the loads and instructions).
 #include <cuda.h>
 #include <math.h>
