@@ -715,7 +715,7 @@ def v4_q4_row_bytes(dim):
 def _q4_cache(cache, dim, dev):
     """Pointer and rows of a 4-bit cache."""
     width = _q4_width(dim)
-    if not isinstance(cache, torch.Tensor) or cache.dim() < 2 or cache.shape[-1] != width:
+    if not width or not isinstance(cache, torch.Tensor) or cache.dim() < 2 or cache.shape[-1] != width:
         raise ValueError("cache must be a tensor [..., %d] for rows of %d values" % (width, dim))
     return _shaped(cache, "cache", cache.shape, torch.uint8, dev), cache.numel() // width
 

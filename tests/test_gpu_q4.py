@@ -199,3 +199,12 @@ def test_bad_pages_and_indices_are_skipped_and_flagged():
     ref_o, ref_l = c.run()
     assert torch.equal(o[1], ref_o[1]) and torch.equal(lse[1], ref_l[1])
     assert torch.isfinite(o.float()).all() and not torch.equal(o[0], ref_o[0])
+
+
+def test_rows_of_no_values_are_refused():
+    none = torch.empty(4, 0, dtype=torch.uint8, device="cuda")
+    x, slot = torch.empty(2, 0, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="cache"):
+        V.v4_cache_append_q4(x, slot, none)
+    with pytest.raises(ValueError, match="cache"):
+        V.v4_cache_read_q4(none, slot, x)
