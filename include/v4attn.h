@@ -618,9 +618,12 @@ v4_status v4_w4_proj(const void* x, int64_t rows, int32_t groups, int32_t K, int
  *   dw         : [dim] fp32 out, NULL = not wanted; the parts' must not overlap.
  * dim a multiple of 8 up to 1024 (above: V4_ERR_UNSUPPORTED); rows times heads
  * up to 2^30; rope_dim, rope_begin, layout, dtype and angles as v4_rope.
- * Squares, sums and products are fp32, results are rounded once.  A head of
- * zeros with eps = 0 becomes NaN.  Sums of dw have a fixed order: results repeat
- * bit for bit on the same device.  Workspace of the gradient:
+ * Squares, sums and products are fp32, results are rounded once: a head whose
+ * mean square is above fp32's range becomes zero; with eps = 0 one of zeros
+ * becomes NaN, and one whose mean square is below 2^-126 is inexact or not
+ * finite.  NaN and infinities stay within their head, but for dw, which sums all
+ * heads.  Sums of dw have a fixed order: results repeat bit for bit on the same
+ * device.  Workspace of the gradient:
  * v4_norm_rope_workspace_size(dim) bytes, 256-byte aligned, one for each of the
  * calls that may overlap.
  * --------------------------------------------------------------------*/
@@ -678,9 +681,9 @@ v4_status v4_cache_read_q4(const void* cache, int64_t n_slots, const int32_t* sl
 
 /* ----------------------------------------------------------------------
  * v4_tree_mqa_fwd over 4-bit caches: tok_cache and ent_cache hold rows of
- * v4_q4_row_bytes(D) bytes and are 32-byte aligned, everything else (keys, masks, sinks, padding, bad
- * indices, workspace, dtype of q and o, shapes of either path) is
- * v4_tree_mqa_fwd's.  The values of the rows are exact in bf16, so on the same
+ * v4_q4_row_bytes(D) bytes and are 32-byte aligned, everything else (keys,
+ * masks, sinks, padding, bad indices, workspace, dtype of q and o, shapes of
+ * either path) is v4_tree_mqa_fwd's.  The values of the rows are exact in bf16, so on the same
  * values both give the same sums but for their order.
  * --------------------------------------------------------------------*/
 v4_status v4_tree_mqa_fwd_q4(const v4_config* cfg, const v4_tree_inputs* in, void* o, float* lse,

@@ -393,7 +393,7 @@ __device__ __forceinline__ void add2(float* x, float a, float b) {
 }
 
 // Whether a looked-up row lies in one of the caches (bound-checking build).
-__device__ __forceinline__ bool in_caches(const TreeArgs& a, const uint8_t* row) {
+[[maybe_unused]] __device__ __forceinline__ bool in_caches(const TreeArgs& a, const uint8_t* row) {
   const uint8_t* tok = reinterpret_cast<const uint8_t*>(a.tok_cache);
   const uint8_t* ent = reinterpret_cast<const uint8_t*>(a.ent_cache);
   return (a.window != 0 && row >= tok && row < tok + a.tok_slots * kQ4RowBytes) ||

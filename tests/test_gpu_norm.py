@@ -193,6 +193,21 @@ def test_special_values_stay_in_their_head():
     assert (zero == 0).all()
 
 
+def test_special_values_of_the_gradient_stay_in_their_head():
+    g = torch.Generator().manual_seed(2)
+    x, dy = (torch.randn(5, 2, 64, generator=g).cuda() for _ in range(2))
+    pos, f = torch.arange(5, dtype=torch.int32).cuda(), torch.rand(8).cuda()
+    ws = V.alloc_norm_rope_workspace(64)
+    dx, want, dw = torch.empty_like(x), torch.empty_like(x), torch.empty(64, device="cuda")
+    V.v4_norm_rope_bwd(x, None, dy, None, pos, f, want, workspace=ws)
+    x[1, 0, 5], x[2, 1, 7], dy[3, 1, 9] = float("nan"), float("inf"), float("-inf")
+    V.v4_norm_rope_bwd(x, None, dy, None, pos, f, dx, dq_w=dw, workspace=ws)
+    bad = torch.zeros(5, 2, dtype=torch.bool)
+    bad[1, 0] = bad[2, 1] = bad[3, 1] = True
+    assert torch.equal(dx[~bad], want[~bad])
+    assert not torch.isfinite(dx[bad]).all(dim=1).any() and not torch.isfinite(dw).all()
+
+
 def test_gradient_against_differences_of_the_forward():
     """Central differences of the fp32 kernel's own forward: the step's error is about h^2 of the third derivative (1e-6
     here), the difference's 2 U / h of the sum (6e-5 of values of one)."""
