@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(kKeepThreads) pages_keep_kernel(const KeepArgs
   };
   auto find = [&](int round) {
     const int i = round * rows + t;
-    bad = next < i || (next > i && before >= next);
+    bad = next < i || before >= next;                    // a thread without a row: next = i, before = -1
     moves = next > i && !bad;
     pages = make_int2(-1, -1);
     if (moves) {
