@@ -731,7 +731,8 @@ v4_status v4_tree_mqa_fwd_q4(const v4_config* cfg, const v4_tree_inputs* in, voi
  * status) and touch nothing: a length that the table does not hold or a source
  * outside it (that row gets nothing), a page outside the pool (taken for -1), a
  * release of a page that is free, a copy outside the pool, a kept row that is
- * not above the one before or not held (it is not moved).
+ * not above the one before, below its place in the list or not held, even where it
+ * would stay (it is not moved).
  * --------------------------------------------------------------------*/
 v4_status v4_pages_alloc(int32_t n, int32_t* table, int32_t blocks, int32_t page_size,
                          const int32_t* have, const int32_t* need, int32_t* ref, int32_t pages,

@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kKeepThreads) pages_keep_kernel(const KeepArgs
   // copies, its pages one round ahead, so that no load of the chain is waited for.
   int next = 0, before = -1;                             // keep[i], keep[i - 1] of the next look-up
   int2 pages = make_int2(-1, -1), offset;                // pages and rows within them, from and to
-  bool bad = false, moves = false;
+  bool bad = false, here = false, moves = false;         // here: the thread has a row, which has to be held even where it stays
   auto index = [&](int round) {
     const int i = round * rows + t;
     const bool mine = t < rows && i < n;
@@ -388,9 +388,10 @@ __global__ void __launch_bounds__(kKeepThreads) pages_keep_kernel(const KeepArgs
   auto find = [&](int round) {
     const int i = round * rows + t;
     bad = next < i || before >= next;                    // a thread without a row: next = i, before = -1
-    moves = next > i && !bad;
+    here = t < rows && i < n && !bad;
+    moves = here && next > i;
     pages = make_int2(-1, -1);
-    if (moves) {
+    if (here) {
       const long long at[2] = {(long long)base + next, (long long)base + i};
       int blk[2];
 #pragma unroll
@@ -403,10 +404,9 @@ __global__ void __launch_bounds__(kKeepThreads) pages_keep_kernel(const KeepArgs
     const int slot = round & (kKeepStages - 1);
     if (round * rows < n) {                              // the same for all threads
       int2 r = make_int2(-1, -1);
-      if (moves && pages.x >= 0 && pages.x < p.pages && pages.y >= 0 && pages.y < p.pages)
-        r = make_int2(pages.x * p.page + offset.x, pages.y * p.page + offset.y);
-      else if (moves || bad)
-        set_status(p.status, kStatusBadIndex);
+      const bool held = pages.x >= 0 && pages.x < p.pages && pages.y >= 0 && pages.y < p.pages;
+      if (moves && held) r = make_int2(pages.x * p.page + offset.x, pages.y * p.page + offset.y);
+      if (bad || (here && !held)) set_status(p.status, kStatusBadIndex);
       s_rows[slot][t] = r;
       __syncthreads();
       find(round + 1);

@@ -54,3 +54,19 @@ def test_kept_lists_that_do_not_ascend_are_flagged(keep, bad, width):
     V.v4_pages_compact(cache, i32([np.arange(pages)]), i32([0]), i32([len(keep)]), i32(lists))
     assert torch.equal(cache[0].view(-1, 288), want)
     assert flagged() == bad
+
+
+@pytest.mark.parametrize("width", [0, 20])
+@pytest.mark.parametrize("table,base,keep,bad", [
+    ([[4, -1]], 0, [0, 1], False), ([[4, -1]], 0, [0, 1, 2], True), ([[4, 9]], 0, [0, 1, 2], True), ([[4, -7]], 2, [0], True),
+    ([[4, 5]], 3, [0, 1], True), ([[4, 5]], 4, [0], True), ([[4, 5]], 2 ** 31 - 1, [0], True), ([[4, 5]], 2, [0, 1], False)])
+def test_kept_rows_that_are_not_held_are_flagged(table, base, keep, bad, width):
+    """Also where a row would stay at its place: a table that does not hold it is the caller's mistake all the same."""
+    V.v4_reset_device_status()
+    cache = torch.from_numpy(np.random.default_rng(3).integers(0, 255, (6, 2, 16), dtype=np.uint8)).cuda()
+    was = cache.clone()
+    lists = np.full((1, max(len(keep), width)), 7)
+    lists[0, :len(keep)] = keep
+    V.v4_pages_compact(cache, i32(table), i32([base]), i32([len(keep)]), i32(lists))
+    assert torch.equal(cache, was)
+    assert flagged() == bad
