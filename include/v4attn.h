@@ -730,7 +730,7 @@ v4_status v4_tree_mqa_fwd_q4(const v4_config* cfg, const v4_tree_inputs* in, voi
  * V4_ERR_UNSUPPORTED).  Bad values are flagged (V4_ERR_BAD_INDEX in the device
  * status) and touch nothing: a length that the table does not hold or a source
  * outside it (that row gets nothing), a page outside the pool (taken for -1), a
- * release of a page that is free, a copy outside the pool, a kept row that is
+ * fork (taken for -1) or a release of a page that is free, a copy outside the pool, a kept row that is
  * not above the one before, below its place in the list or not held, even where it
  * would stay (it is not moved).
  * --------------------------------------------------------------------*/

@@ -70,3 +70,78 @@ def test_kept_rows_that_are_not_held_are_flagged(table, base, keep, bad, width):
     V.v4_pages_compact(cache, i32(table), i32([base]), i32([len(keep)]), i32(lists))
     assert torch.equal(cache, was)
     assert flagged() == bad
+
+
+def forked(table, ref, src, length, out_blocks, page):
+    """Fork by its definition: a page whose count is 0 when the call begins is none."""
+    free, shared = [p for p, n in enumerate(ref) if n == 0], list(ref)
+    out, copies, bad = np.full((len(src), out_blocks), -1), [], False
+
+    def held(p):
+        nonlocal bad
+        good = p == -1 or (0 <= p < len(ref) and ref[p] > 0)
+        bad = bad or not good
+        return p if good else -1
+    for i, (s, n) in enumerate(zip(src, length)):
+        copy = [-1, -1, 0]
+        for k in range(n // page):
+            out[i, k] = held(table[s][k])
+            if out[i, k] >= 0:
+                shared[out[i, k]] += 1
+        if n % page:
+            old = held(table[s][n // page])
+            if old >= 0 and free:
+                out[i, n // page] = free.pop(0)
+                shared[out[i, n // page]] = 1
+                copy = [old, out[i, n // page], n % page]
+        copies.append(copy)
+    return out, copies, shared, bad
+
+
+@pytest.mark.parametrize("beams", [1, 3, 64, 1500])
+@pytest.mark.parametrize("zero", [[], [0], [1], [2], [0, 1, 2], [0, 5]])
+def test_fork_shares_and_copies_no_free_page(zero, beams):
+    """Pages 0, 1 whole and 2 partly filled; some of them are free by their counts, so they are the first to be given."""
+    V.v4_reset_device_status()
+    page, pages, table = 4, 8 + beams, [[0, 1, 2]]
+    ref = [1, 1, 1] + [0] * (pages - 3)
+    for z in zero:
+        ref[z] = 0
+    src, length = [0] * beams, [10 - i % 3 for i in range(beams)]
+    want, copies, shared, bad = forked(table, ref, src, length, 3, page)
+    assert bad == bool(zero)
+    for _ in range(20):
+        counts, out, cp = i32(ref), i32(np.full((beams, 3), 9)), i32(np.full((beams, 3), 9))
+        V.v4_pages_fork(i32(table), i32(src), i32(length), out, counts, page, cp)
+        same(out, want), same(cp, copies), same(counts, shared)
+        assert flagged() == bad
+
+
+def test_beams_step_by_step_without_a_pause():
+    """The beams of a step give their pages back and the next are forked at once, each call right behind the one before."""
+    rng = np.random.default_rng(8)
+    page, blocks, n, steps = 8, 6, 90, 60
+    pages = 3 * blocks + n + 5
+    perm = rng.permutation(pages)
+    table = perm[:3 * blocks].reshape(3, blocks)
+    ref = np.zeros(pages, int)
+    ref[table] = 1
+    src = rng.integers(-1, 3, (steps, n))
+    length = rng.integers(0, page * blocks + 1, (steps, n))
+    dt, dref = i32(table), i32(ref)
+    dsrc, dlen = [i32(s) for s in src], [i32(s) for s in length]
+    outs = [i32(np.full((n, blocks), -1)) for _ in range(steps + 1)]
+    copies = [i32(np.full((n, 3), 9)) for _ in range(steps)]
+    torch.cuda.synchronize()
+    for k in range(steps):
+        V.v4_pages_fork(dt, dsrc[k], dlen[k], outs[k + 1], dref, page, copies[k])
+        V.v4_pages_free(outs[k + 1], dref, page)          # all of them: -1 again
+    for k in range(steps):                                # and with the pages kept for a step
+        V.v4_pages_free(outs[k], dref, page)
+        V.v4_pages_fork(dt, dsrc[k], dlen[k], outs[k + 1], dref, page, copies[k])
+    for k in range(steps):
+        want, cp, ref2, bad = forked(table, list(ref), src[k], np.where(src[k] < 0, 0, length[k]), blocks, page)
+        assert not bad
+        same(copies[k], cp)
+    same(outs[steps], want), same(dref, ref2)
+    assert not flagged()
