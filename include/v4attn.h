@@ -702,7 +702,7 @@ v4_status v4_tree_mqa_fwd_q4(const v4_config* cfg, const v4_tree_inputs* in, voi
  * v4_pages_alloc gives sequence i a page for every entry -1 among the blocks
  *   that tokens have[i] .. need[i] - 1 need beyond those of the first have[i]
  *   tokens (blocks ceil(have / page_size) .. ceil(need / page_size) - 1; have
- *   NULL = 0).  Entries that hold a page keep it.
+ *   NULL = 0).  Entries of these blocks that hold a page keep it.
  * v4_pages_fork makes out_table[i] a copy of the first len[i] tokens of
  *   sequence src[i] of `table` (src -1: an empty row): whole blocks are shared
  *   (their counts rise), a partly filled last block gets a free page, and

@@ -156,8 +156,15 @@ __global__ void __launch_bounds__(kGiveThreads) pages_alloc_kernel(const AllocAr
       [&](int i) {
         int lo, hi, c = 0;
         range(i, &lo, &hi);
-        for (int k = lo; k < hi; k += 32)
-          c += __popc(__ballot_sync(0xffffffffu, k + lane < hi && p.table[(size_t)i * p.blocks + k + lane] == -1));
+        for (int k = lo; k < hi; k += 32) {
+          int32_t* at = p.table + (size_t)i * p.blocks + k + lane;
+          const int pg = k + lane < hi ? *at : 0;
+          if (pg < -1 || pg >= p.pages) {         // no page of the pool: taken for -1
+            set_status(p.status, kStatusBadIndex);
+            *at = -1;
+          }
+          c += __popc(__ballot_sync(0xffffffffu, pg < 0 || pg >= p.pages));
+        }
         return c;
       },
       [&](int i, int first, int from, int to, const int* list) {

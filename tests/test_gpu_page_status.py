@@ -145,3 +145,17 @@ def test_beams_step_by_step_without_a_pause():
         same(copies[k], cp)
     same(outs[steps], want), same(dref, ref2)
     assert not flagged()
+
+
+def test_pages_outside_the_pool_are_replaced_when_pages_are_given():
+    """Taken for -1, as in a fork or a release: flagged, and the entry gets a page where its tokens want one."""
+    V.v4_reset_device_status()
+    table, ref, lack = i32([[4, 1, -5, 7], [-1, 2 ** 31 - 1, 0, -1]]), i32([1, 1, 0, 0]), i32([9])
+    V.v4_pages_alloc(table, ref, i32([12, 8]), 4, lack=lack)
+    same(table, [[2, 1, 3, 7], [-1, -1, 0, -1]])
+    same(ref, [1, 1, 1, 1]), same(lack, [2])
+    assert flagged()
+    table = i32([[4, 1, 0, 7]])
+    V.v4_pages_alloc(table, ref, i32([12]), 4, have=i32([4]))       # block 0 and block 3 are not looked at
+    same(table, [[4, 1, 0, 7]])
+    assert not flagged()
