@@ -710,8 +710,9 @@ v4_status v4_tree_mqa_fwd_q4(const v4_config* cfg, const v4_tree_inputs* in, voi
  *   entries become -1: what out_table held before is overwritten, not released.
  *   The tables must not overlap.  An entry -1 of `table` stays one.
  * v4_pages_free releases the entries of sequence i whose blocks hold no token
- *   in [lo[i], hi[i]) (lo NULL = 0; hi NULL: all of them): they become -1 and
- *   their pages' counts fall.
+ *   in [lo[i], hi[i]) (lo NULL = 0; hi NULL: all of them; any int32, so a hi
+ *   above every length keeps all from lo on): they become -1 and their pages'
+ *   counts fall.
  * v4_pages_copy copies the first copies[i][2] rows of page copies[i][0] to page
  *   copies[i][1] in each layer.  A target may be named once and must be no
  *   source.

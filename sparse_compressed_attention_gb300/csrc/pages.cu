@@ -144,11 +144,11 @@ __global__ void __launch_bounds__(kGiveThreads) pages_alloc_kernel(const AllocAr
   auto range = [&](int i, int* lo, int* hi) {
     const long long have = p.have ? p.have[i] : 0, need = p.need[i];
     *lo = *hi = 0;
-    if (have < 0 || need < 0 || (need + p.page - 1) / p.page > p.blocks) {
+    if (have < 0 || need < 0 || (max(have, need) + p.page - 1) / p.page > p.blocks) {
       set_status(p.status, kStatusBadIndex);
       return;
     }
-    *lo = (int)min((have + p.page - 1) / p.page, (long long)p.blocks);
+    *lo = (int)((have + p.page - 1) / p.page);
     *hi = (int)((need + p.page - 1) / p.page);
   };
   give_pages(

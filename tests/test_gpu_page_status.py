@@ -159,3 +159,13 @@ def test_pages_outside_the_pool_are_replaced_when_pages_are_given():
     V.v4_pages_alloc(table, ref, i32([12]), 4, have=i32([4]))       # block 0 and block 3 are not looked at
     same(table, [[4, 1, 0, 7]])
     assert not flagged()
+
+
+def test_tokens_that_the_table_does_not_hold_are_flagged():
+    V.v4_reset_device_status()
+    ref = i32([0, 0, 0])
+    for have, need, bad in ((9, 4, True), (2 ** 31 - 1, 8, True), (8, 8, False), (8, 3, False), (-1, 3, True), (0, 9, True), (0, -1, True)):
+        table = i32([[-1, -1]])
+        V.v4_pages_alloc(table, ref, i32([need]), 4, have=i32([have]))
+        same(table, [[-1, -1]]), same(ref, [0, 0, 0])
+        assert flagged() == bad, (have, need)
