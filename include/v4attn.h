@@ -618,12 +618,14 @@ v4_status v4_w4_proj(const void* x, int64_t rows, int32_t groups, int32_t K, int
  *   dw         : [dim] fp32 out, NULL = not wanted; the parts' must not overlap.
  * dim a multiple of 8 up to 1024 (above: V4_ERR_UNSUPPORTED); rows times heads
  * up to 2^30; rope_dim, rope_begin, layout, dtype and angles as v4_rope.
- * Squares, sums and products are fp32, results are rounded once: a head whose
- * mean square is above fp32's range becomes zero; with eps = 0 one of zeros
- * becomes NaN, and one whose mean square is below 2^-126 is inexact or not
- * finite.  NaN and infinities stay within their head, but for dw, which sums all
- * heads.  Sums of dw have a fixed order: results repeat bit for bit on the same
- * device.  Workspace of the gradient:
+ * Squares, sums and products are fp32, results are rounded once.  A head whose
+ * sum of squares is 2^128 or more (of 512 values: a root mean square above
+ * 8.2e17) becomes zero, and for finite w and dy so do its dx and its part of dw;
+ * where the sum of w g x alone passes the range, that head's dx is not finite.
+ * With eps = 0 a head of zeros becomes NaN, and one whose mean square is below
+ * 2^-126 is inexact or not finite.  NaN and infinities stay within their head, but
+ * for dw, which sums all heads.  Sums of dw have a fixed order: results repeat bit
+ * for bit on the same device.  Workspace of the gradient:
  * v4_norm_rope_workspace_size(dim) bytes, 256-byte aligned, one for each of the
  * calls that may overlap.
  * --------------------------------------------------------------------*/

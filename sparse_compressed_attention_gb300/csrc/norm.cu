@@ -256,7 +256,8 @@ __global__ void __launch_bounds__(kThreads, (Lay<T, U, kHalf, kGrad>::kBlocks)) 
     const float r = rsqrtf(fmaf(t_sq, p.inv_dim, p.eps));
     const float2 r2 = make_float2(r, r);
     if (kGrad) {
-      const float m = -t_dot * p.inv_dim * (r * r) * r;
+      // r = 0: the sum of squares passed fp32's range and the head counts as zero, though t_dot may be infinite
+      const float m = r == 0.f ? 0.f : -t_dot * p.inv_dim * (r * r) * r;
       const float2 m2 = make_float2(m, m);
       if (live) {                                // r of nothing may be infinite
 #pragma unroll
