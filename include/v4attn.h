@@ -611,11 +611,13 @@ v4_status v4_w4_proj(const void* x, int64_t rows, int32_t groups, int32_t K, int
  *   x, dy, out : element (t, h, c) at t * row_stride + h * head_stride + c, in
  *                elements; strides >= 0, multiples of 16 bytes.  An output may
  *                be an input of its own part with the same strides (in place);
- *                outputs that meet themselves, each other or any other input
- *                are refused.  Views of one fused projection may be mixed as
- *                long as their row strides are equal.
+ *                outputs that meet themselves, each other, any other input (w,
+ *                pos and inv_freq among them), dw or the workspace are refused.
+ *                Views of one fused projection may be mixed as long as their
+ *                row strides are equal.
  *   w          : [dim] fp32, NULL = ones.
  *   dw         : [dim] fp32 out, NULL = not wanted; the parts' must not overlap.
+ *                Written when everything has been read.
  * dim a multiple of 8 up to 1024 (above: V4_ERR_UNSUPPORTED); rows times heads
  * up to 2^30; rope_dim, rope_begin, layout, dtype and angles as v4_rope.
  * Squares, sums and products are fp32, results are rounded once.  A head whose

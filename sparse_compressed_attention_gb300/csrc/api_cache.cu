@@ -46,6 +46,28 @@ static bool apart(const View& a, const View& b) {
   return na <= step && nb <= step && d >= na && d + nb <= step;
 }
 
+// Whether a view has an element among n bytes at p.  Its runs of dim values are nested (the
+// inner runs of one outer step end before the next); where they are not, as a broadcast
+// input's, everything from the first to the last element counts.
+static bool meets(const View& v, const void* p, int64_t n) {
+  if (p == nullptr || !overlap(v.p, v.bytes(), p, n)) return false;
+  const bool rows_outer = v.rows > 1 && (v.heads == 1 || v.rs >= v.hs);
+  const int64_t no = rows_outer ? v.rows : v.heads, so = (rows_outer ? v.rs : v.hs) * v.es;
+  const int64_t ni = rows_outer ? v.heads : v.rows, si = (rows_outer ? v.hs : v.rs) * v.es, run = v.dim * v.es;
+  if ((ni > 1 && si < run) || (no > 1 && so < (ni - 1) * si + run)) return true;
+  const int64_t span = (ni - 1) * si + run, at = (int64_t)((intptr_t)p - (intptr_t)v.p);
+  // outer steps whose span reaches behind `at`, the first of them: of three that begin below
+  // at + n, the middle one begins among the bytes
+  const int64_t o0 = no > 1 && at >= span ? (at - span) / so + 1 : 0;
+  for (int64_t o = o0; o < no && o < o0 + 3 && o * so < at + n; ++o) {
+    const int64_t from = at - o * so;              // the bytes, relative to this step's first run
+    const int64_t i0 = ni > 1 && from >= run ? (from - run) / si + 1 : 0;
+    for (int64_t i = i0; i < ni && i < i0 + 1 && i * si < from + n; ++i)
+      if (from < i * si + run) return true;
+  }
+  return false;
+}
+
 // An output: its rows and heads must not meet each other.
 static v4_status check_out(const View& v, const char* name) {
   const bool rows_outer = (v.heads == 1 || v.hs >= v.dim) && (v.rows == 1 || v.rs >= (v.heads - 1) * v.hs + v.dim);
@@ -151,6 +173,30 @@ static v4_status norm_rope(const v4_norm_rope_part* q, const v4_norm_rope_part* 
     }
     if (!workspace) return set_error(V4_ERR_WORKSPACE, "workspace is NULL");
     if ((uintptr_t)workspace & 255u) return set_error(V4_ERR_WORKSPACE, "workspace not 256-byte aligned");
+  }
+  // What all blocks read: no output may lie there (dw may, it is written when everything is read).
+  const struct {
+    const void* p;
+    int64_t n;
+  } shared[] = {{c.part[0].w, (int64_t)dim * 4}, {c.part[1].w, (int64_t)dim * 4}, {rope_dim > 0 ? pos : nullptr, rows * 4},
+                {rope_dim > 0 ? inv_freq : nullptr, (int64_t)rope_dim * 2}};
+  const int64_t scratch = grad ? (int64_t)norm_rope_workspace(dim) : 0;
+  for (const auto& f : shared) {
+    for (int o = 0; o < n_out; ++o)
+      if (meets(out[o], f.p, f.n)) return bad("an output overlaps weights, positions or frequencies");
+    if (grad && f.p && overlap(f.p, f.n, workspace, scratch)) return bad("the workspace overlaps an input");
+  }
+  if (grad) {
+    for (int i = 0; i < n_in; ++i)
+      if (meets(in[i], workspace, scratch)) return bad("the workspace overlaps an input");
+    for (int o = 0; o < n_out; ++o)
+      if (meets(out[o], workspace, scratch)) return bad("the workspace overlaps an output");
+    for (const NormPartCall& d : c.part) {
+      if (!d.dw) continue;
+      if (overlap(d.dw, (int64_t)dim * 4, workspace, scratch)) return bad("the workspace overlaps a weight gradient");
+      for (int o = 0; o < n_out; ++o)
+        if (meets(out[o], d.dw, (int64_t)dim * 4)) return bad("an output overlaps a weight gradient");
+    }
   }
   StageTiming ps(grad ? 21 : 20, st);
   return cuda_result(launch_norm_rope(c, st), "norm kernel");
