@@ -216,6 +216,7 @@ static v4_status q4_rows(const void* x, void* out, int64_t rows, int32_t dim, in
   if (rows < 0 || rows > (1 << 24)) return bad("rows must be in [0, 2^24]");
   if (rows * (dim / kQ4Group) > 0x7FFFFFFF) return bad("rows times dim above 2^35");
   TRY(check_stride(stride, es, "row stride"));
+  if ((double)rows * (double)stride > 1e15) return bad("rows reach above 10^15 elements");
   if (n_slots < 0 || n_slots > 0x7FFFFFFF) return bad("n_slots must be in [0, 2^31)");
   if (read && rows > 1 && stride < dim) return bad("out's rows overlap");
   if (rows == 0) return V4_OK;
