@@ -9,6 +9,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import glob
 import os
+import re
 import shutil
 import subprocess
 
@@ -25,6 +26,23 @@ DEBUG_LIB = os.path.join(DEBUG_OUT, "libv4attn_debug.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", INCLUDE, "-I", CSRC]
+
+# Kernels that exchange registers between their warps count on what a launch starts with:
+# part of the mangled name, the constant of the source that says how many.
+REGISTERS = {"tree_tc.cu": ("tree_tc_kernelILb1E", "kRegsStart")}
+
+
+def check_registers(src, log):
+    """Refuse a build of `src` whose kernel has other registers than its split needs (log: ptxas -v)."""
+    if os.path.basename(src) not in REGISTERS:
+        return
+    kernel, constant = REGISTERS[os.path.basename(src)]
+    with open(src) as f:
+        want = re.search(r"\b%s = (\d+)" % constant, f.read())
+    got = re.search(r"Compiling entry function '[^']*%s(?:(?!Compiling entry).)*?Used (\d+) registers" % kernel, log, re.S)
+    if not want or not got or want.group(1) != got.group(1):
+        raise RuntimeError("%s: %s was compiled to %s registers, its split needs %s" % (
+            os.path.basename(src), kernel, got.group(1) if got else "an unknown number of", want.group(1) if want else "?"))
 
 
 def _nvcc():
@@ -62,12 +80,14 @@ def build(force=False, verbose=False, extra_flags=None, debug=False):
 
     def compile_one(src):
         obj = os.path.join(out_dir, os.path.basename(src)[:-3] + ".o")
-        cmd = [nvcc, *ARCH, *FLAGS, *extra, "-c", src, "-o", obj]
+        info = ["-Xptxas", "-v"] if os.path.basename(src) in REGISTERS else []
+        cmd = [nvcc, *ARCH, *FLAGS, *info, *extra, "-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError("nvcc failed for %s:\n%s\n%s" % (src, " ".join(cmd), r.stderr))
         if verbose and r.stderr:
             print(r.stderr)
+        check_registers(src, r.stdout + r.stderr)
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
