@@ -169,3 +169,40 @@ def test_tokens_that_the_table_does_not_hold_are_flagged():
         V.v4_pages_alloc(table, ref, i32([need]), 4, have=i32([have]))
         same(table, [[-1, -1]]), same(ref, [0, 0, 0])
         assert flagged() == bad, (have, need)
+
+
+def test_a_captured_beam_step_replays():
+    """Release, fork and copies of 70 beams in a graph; the table, lengths and counts change between replays."""
+    rng = np.random.default_rng(12)
+    page, blocks, n, layers = 8, 5, 70, 2
+    pages = 4 * blocks + n + 3
+    dt, dref = i32(np.zeros((4, blocks))), i32(np.zeros(pages))
+    dsrc, dlen, out, copies = i32(np.zeros(n)), i32(np.zeros(n)), i32(np.full((n, blocks), -1)), i32(np.zeros((n, 3)))
+    lack = i32([9])
+    cache = torch.zeros(layers, pages, page, 32, dtype=torch.uint8, device="cuda")
+
+    def step():
+        V.v4_pages_free(out, dref, page)
+        V.v4_pages_fork(dt, dsrc, dlen, out, dref, page, copies, lack=lack)
+        V.v4_pages_copy(cache, copies)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(4):
+        table = rng.permutation(pages)[:4 * blocks].reshape(4, blocks)
+        ref = np.zeros(pages, int)
+        ref[table] = 1
+        src, length = rng.integers(0, 4, n), rng.integers(0, page * blocks + 1, n)
+        want, cp, counts, bad = forked(table, list(ref), src, length, blocks, page)
+        rows = torch.from_numpy(rng.integers(0, 255, tuple(cache.shape), dtype=np.uint8))
+        moved_rows = rows.clone()
+        for a, b, r in cp:
+            if a >= 0:
+                moved_rows[:, b, :r] = rows[:, a, :r]
+        dt.copy_(i32(table)), dref.copy_(i32(ref)), dsrc.copy_(i32(src)), dlen.copy_(i32(length)), out.fill_(-1), cache.copy_(rows)
+        graph.replay()
+        same(out, want), same(copies, cp), same(dref, counts), same(lack, [0])
+        assert torch.equal(cache.cpu(), moved_rows) and not bad
+    assert not flagged()
