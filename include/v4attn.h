@@ -665,7 +665,7 @@ v4_status v4_norm_rope_bwd(const v4_norm_rope_part* q, const v4_norm_rope_part* 
  * (v4_norm_rope_fwd and v4_rope rotate): scale = max|x| / 7 over 16 values,
  * rounded to the nearest scale (ties to even; at least 2^-20, at most 3840),
  * code = 8 + clamp(round_to_even(x / scale), -8, 7).  Infinities take the
- * largest scale and code; NaN is stored as zero.
+ * largest scale and the last code of their sign; NaN is stored as zero.
  * v4_cache_read_q4 makes dense rows of it, exactly: the rows that
  * v4_sparse_mqa_fwd and v4_sparse_mqa_bwd take, for instance.  A slot of -1
  * reads zeros.

@@ -15,9 +15,9 @@
 // adds the blocks' sums in a fixed order, so results repeat bit for bit.
 //
 // Times (device, in a replayed graph): 4096 rows of 64 + 1 heads of 512 in bf16 83 us
-// (6.5 TB/s; a block for 16 heads with loads into registers 111), their gradients 131
+// (6.5 TB/s; a block for 16 heads with loads into registers 111), their gradients 132
 // (6.2 TB/s; 310), gradients of 5003 rows of 32 + 8 heads of 128 in fp32, half layout, 58
-// (5.3 TB/s, bound by instructions and shared memory; 101), 16 rows of 64 + 1 heads 2.3
+// (5.3 TB/s, bound by instructions and shared memory; 101), 16 rows of 64 + 1 heads 2.4
 // (launch).
 #include <math.h>
 
@@ -68,7 +68,8 @@ struct Lay {
   static constexpr int kTable = kStages * kTensors * kHead;       // offset of the angles
   static constexpr int kStrip = kTable + 128 * U * (int)sizeof(float2);
   static constexpr int kWarp = kStrip + (kHalf && !kGrad ? 256 * U * (int)sizeof(float) : 0);
-  static constexpr int kBlocks = kGrad ? (U == 1 ? 5 : U == 2 ? 4 : 2) : U > 2 ? 3 : 8;      // resident, without spills
+  // resident on an SM, without spills (but 8 bytes in the forward bf16 half layout of U = 2)
+  static constexpr int kBlocks = kGrad ? (U == 1 ? 5 : U == 2 ? 4 : 2) : U > 2 ? 3 : 8;
 };
 
 __device__ __forceinline__ void copy_16(void* dst, const void* src) {

@@ -375,8 +375,12 @@ struct KeepArgs {
 };
 
 // Threads and words of a thread: many threads for long lists (half of 8 x 16000 rows of
-// 1 KB in 4 layers: 87 us with 512 x 1, 106 with 128 x 2), few for short ones, where more
-// blocks fit on an SM (6 of 16 rows for 32 sequences in 43 layers: 5.8 and 3.5 us).
+// 1 KB in 4 layers: 88 us with 512 x 1, 106 with 128 x 2), few for short ones, where more
+// blocks fit on an SM (6 of 16 rows for 32 sequences in 43 layers: 6.6 and 4.2 us).  The
+// two cross somewhere above the rule's 16 rows: half of 2 n rows kept, 512 x 1 against
+// 128 x 2, 32 sequences in 43 layers: n = 64 28.9 and 25.8, 256 116.5 and 121.8; 8 in 4:
+// 64 3.9 and 2.8, 1024 12.7 and 11.9, 4096 47.0 and 55.8; 64 in 8: 64 11.4 and 11.1, 128 21.1
+// and 21.3.
 template <int kKeepThreads, int kKeepWords>
 __global__ void __launch_bounds__(kKeepThreads) pages_keep_kernel(const KeepArgs p) {
   __shared__ uint4 s_ring[kKeepStages][kKeepWords][kKeepThreads];
