@@ -54,11 +54,11 @@ __device__ __forceinline__ int block_scan(int v, GiveShared* sh, int* total) {
 __device__ __forceinline__ int4 four_counts(const int* ref, int pages, int p0) {
   int4 r = make_int4(1, 1, 1, 1);
   if (p0 + 3 < pages) {
-    r = __ldcg(reinterpret_cast<const int4*>(ref + p0));
+    r = *reinterpret_cast<const int4*>(ref + p0);
   } else if (p0 < pages) {
-    r.x = __ldcg(ref + p0);
-    if (p0 + 1 < pages) r.y = __ldcg(ref + p0 + 1);
-    if (p0 + 2 < pages) r.z = __ldcg(ref + p0 + 2);
+    r.x = ref[p0];
+    if (p0 + 1 < pages) r.y = ref[p0 + 1];
+    if (p0 + 2 < pages) r.z = ref[p0 + 2];
   }
   return r;
 }
@@ -186,16 +186,18 @@ __global__ void __launch_bounds__(kGiveThreads) pages_alloc_kernel(const AllocAr
 }
 
 // ---------------------------------------------------------------------------
-// Fork, two launches: the whole pages are shared, then the partly filled last ones get
-// a free page each.  In the first a count of 0 stays 0 and others only rise, so what is
-// held and what is free are the counts' at the call's start, whatever the order of
-// blocks (in one launch a page that a table names though its count is 0 could be shared
-// and given out at once).  The second looks for its pages while the first runs, since
-// that does not change them, and writes once it has ended: 64 beams of 16 with release
-// and copies take 9.9 us, 11.5 where it waits first, 8.9 in one launch.
+// Fork.  The whole pages are shared, the partly filled last ones get a free page each.
+// While pages are shared a count of 0 stays 0 and others only rise, and the pages given
+// are written when that is over: what is held and what is free are the counts' at the
+// call's start, whatever the order of blocks.  (Without that order a page that a table
+// names though its count is 0 could be shared and given out at once.)
 // ---------------------------------------------------------------------------
 constexpr int kForkThreads = kGiveThreads, kForkRounds = kMaxSeqs / kForkThreads;
 static_assert(kMaxSeqs <= kList, "one list serves all beams");
+// One launch of one cluster while its sharing blocks have two entries a thread at most, two
+// launches above.  A release and a fork, one launch against two: 64 beams of 32 blocks 6.5
+// and 8.8 us, 256 of 64 9.0 and 9.4, 512 of 64 13.1 and 11.2, 8192 of 64 126 and 58.
+constexpr int kClusterBlocks = 8, kForkCluster = 2 * (kClusterBlocks - 1);
 
 struct ForkArgs {
   const int32_t *table, *src, *len;
@@ -208,7 +210,7 @@ struct ForkArgs {
 
 // Whole blocks and rows of the last of beam i; false: nothing is shared.
 __device__ __forceinline__ bool fork_row(const ForkArgs& p, int i, int* src, int* full, int* rest) {
-  const int s = __ldcg(p.src + i), L = __ldcg(p.len + i);
+  const int s = p.src[i], L = p.len[i];
   *src = s;
   *full = *rest = 0;
   if (s == -1) return false;
@@ -224,20 +226,19 @@ __device__ __forceinline__ bool fork_row(const ForkArgs& p, int i, int* src, int
 
 // Page of block k, -1 (flagged) where it is none of the pool's or free.
 __device__ __forceinline__ int fork_page(const ForkArgs& p, int src, int k) {
-  const int pg = __ldcg(p.table + (size_t)src * p.blocks + k);
-  if (pg == -1 || (pg >= 0 && pg < p.pages && __ldcg(p.ref + pg) > 0)) return pg;
+  const int pg = p.table[(size_t)src * p.blocks + k];
+  if (pg == -1 || (pg >= 0 && pg < p.pages && p.ref[pg] > 0)) return pg;
   set_status(p.status, kStatusBadIndex);
   return -1;
 }
 
-__global__ void __launch_bounds__(kForkThreads) pages_share_kernel(const ForkArgs p) {
-  after_previous();
-  for (long long j = (long long)blockIdx.x * kForkThreads + threadIdx.x; j < p.items;
-       j += (long long)gridDim.x * kForkThreads) {
+// The share of one of `blocks` thread blocks in the whole pages and the empty entries.
+__device__ __forceinline__ void fork_share(const ForkArgs& p, int block, int blocks) {
+  for (long long j = (long long)block * kForkThreads + threadIdx.x; j < p.items; j += (long long)blocks * kForkThreads) {
     const int i = (int)p.by_out.div((uint32_t)j), k = (int)(j - (long long)i * p.out_blocks);
     int src, full, rest, pg = -1;
     const bool live = fork_row(p, i, &src, &full, &rest);
-    if (live && k == full && rest > 0) continue;         // the second launch's
+    if (live && k == full && rest > 0) continue;         // gets a page of its own
     if (live && k < full) {
       pg = fork_page(p, src, k);
       if (pg >= 0) atomicAdd(p.ref + pg, 1);
@@ -246,13 +247,29 @@ __global__ void __launch_bounds__(kForkThreads) pages_share_kernel(const ForkArg
   }
 }
 
-// A thread for each beam, 1024 at a time.  Launched behind pages_share_kernel, whose
-// blocks let it start once the kernels before them have ended: until wait_previous() it
-// reads (past L1) only what those have written, and writes nothing but flags.
+__global__ void __launch_bounds__(kForkThreads) pages_share_kernel(const ForkArgs p) {
+  after_previous();
+  fork_share(p, blockIdx.x, gridDim.x);
+}
+
+// A thread for each beam, 1024 at a time.  kCluster: one launch of one cluster, whose first
+// block gives while the others share; else the second launch, behind pages_share_kernel.
+template <bool kCluster>
 __global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(const ForkArgs p) {
   extern __shared__ __align__(16) uint8_t smem[];
   GiveShared* sh = reinterpret_cast<GiveShared*>(smem);
   const int t = threadIdx.x;
+  after_previous();
+  auto all_shared = [] {
+    if (kCluster)
+      asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  };
+  if (kCluster && blockIdx.x > 0) {
+    fork_share(p, blockIdx.x - 1, gridDim.x - 1);
+    __syncwarp();
+    all_shared();
+    return;
+  }
   const int4 ahead = four_counts(p.ref, p.pages, 4 * t);         // asked for beside the beams' rows
   int old[kForkRounds], full[kForkRounds], rest[kForkRounds], at[kForkRounds];
   int wanted = 0, chunk = 0;
@@ -268,7 +285,7 @@ __global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(const ForkArgs
     wanted += want;
   }
   const int given = list_free(p.ref, p.pages, wanted, &chunk, sh, &ahead);
-  after_previous();
+  all_shared();
 #pragma unroll
   for (int k = 0; k < kForkRounds; ++k) {
     const int i = k * kForkThreads + t;
@@ -467,12 +484,15 @@ __global__ void __launch_bounds__(kKeepThreads) pages_keep_kernel(const KeepArgs
   }
 }
 
-cudaError_t give_shared(void (*kern)(const AllocArgs), void (*fork)(const ForkArgs)) {
+cudaError_t give_shared() {
   static OncePerDevice once;
-  return once.run([&] {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(GiveShared));
-    if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(fork, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(GiveShared));
+  return once.run([] {
+    cudaError_t e = cudaFuncSetAttribute(pages_alloc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(GiveShared));
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(pages_fork_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(GiveShared));
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(pages_fork_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(GiveShared));
+    return e;
   });
 }
 
@@ -482,7 +502,7 @@ int pages_max_sequences() { return kMaxSeqs; }
 
 cudaError_t launch_pages_alloc(int n, int32_t* table, int blocks, int page, const int32_t* have, const int32_t* need,
                                int32_t* ref, int pages, int32_t* lack, int* status, cudaStream_t st) {
-  cudaError_t e = give_shared(pages_alloc_kernel, pages_fork_kernel);
+  cudaError_t e = give_shared();
   if (e != cudaSuccess) return e;
   AllocArgs p;
   p.table = table;
@@ -503,7 +523,7 @@ cudaError_t launch_pages_alloc(int n, int32_t* table, int blocks, int page, cons
 cudaError_t launch_pages_fork(int B, const int32_t* table, int blocks, int n, const int32_t* src, const int32_t* len,
                               int32_t* out, int out_blocks, int page, int32_t* ref, int pages, int32_t* copies,
                               int32_t* lack, int* status, cudaStream_t st) {
-  cudaError_t e = give_shared(pages_alloc_kernel, pages_fork_kernel);
+  cudaError_t e = give_shared();
   if (e != cudaSuccess) return e;
   ForkArgs p;
   p.table = table;
@@ -522,14 +542,29 @@ cudaError_t launch_pages_fork(int B, const int32_t* table, int blocks, int n, co
   p.page = page;
   p.pages = pages;
   p.by_out.set((uint32_t)out_blocks);
-  long long grid = (p.items + kForkThreads - 1) / kForkThreads;
-  if (grid > 304) grid = 304;
-  if (grid > 0) {
-    e = launch_overlapped(pages_share_kernel, dim3((unsigned)grid), dim3(kForkThreads), 0, st, p);
-    if (e != cudaSuccess) return e;
-    note_launch();
+  const long long sharing = (p.items + kForkThreads - 1) / kForkThreads;       // blocks with an entry for each thread
+  if (sharing <= kForkCluster) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kClusterBlocks);
+    cfg.blockDim = dim3(kForkThreads);
+    cfg.dynamicSmemBytes = sizeof(GiveShared);
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = kClusterBlocks;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, pages_fork_kernel<true>, (const ForkArgs)p);
+    if (e == cudaSuccess) note_launch();
+    return e;
   }
-  e = launch_overlapped(pages_fork_kernel, dim3(1), dim3(kForkThreads), sizeof(GiveShared), st, p);
+  e = launch_overlapped(pages_share_kernel, dim3((unsigned)(sharing < 304 ? sharing : 304)), dim3(kForkThreads), 0, st, p);
+  if (e != cudaSuccess) return e;
+  note_launch();
+  e = launch_overlapped(pages_fork_kernel<false>, dim3(1), dim3(kForkThreads), sizeof(GiveShared), st, p);
   if (e == cudaSuccess) note_launch();
   return e;
 }

@@ -98,7 +98,7 @@ def forked(table, ref, src, length, out_blocks, page):
     return out, copies, shared, bad
 
 
-@pytest.mark.parametrize("beams", [1, 3, 64, 1500])
+@pytest.mark.parametrize("beams", [1, 3, 64, 1500, 6000])      # one launch up to 14336 entries, two above
 @pytest.mark.parametrize("zero", [[], [0], [1], [2], [0, 1, 2], [0, 5]])
 def test_fork_shares_and_copies_no_free_page(zero, beams):
     """Pages 0, 1 whole and 2 partly filled; some of them are free by their counts, so they are the first to be given."""
